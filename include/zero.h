@@ -359,6 +359,113 @@ int zero_fsdp_step_sched(zero_ctx *ctx, const void *const *grads,
                          void *const *params_out, zero_dtype param_dtype,
                          hipStream_t stream);
 
+/* ---- AdamW over many tensors at once ----------------------------------
+ * The per-parameter layout with decoupled weight decay, gradient clipping by
+ * a norm that stays on the device, and states in 32 or in 8 bits; the whole
+ * list takes one launch. Gradients and outputs are bound once
+ * (zero_adamw_bind), so a step marshals no pointers and can be captured into
+ * a HIP graph.
+ *
+ * Per element of tensor k, with g the mean of the bound replicas' gradients
+ * (binary32, added in rank order), S the sum of squares the caller passes and
+ * c = min(1, max_norm / (sqrt(S) + 1e-6)):
+ *   g    = g * c                                   (with a sum only)
+ *   lr_k = lr * lr_scale[k];  keep = 1 - lr_k * weight_decay[k]
+ *   m = b1*m + (1-b1)*g ;  v = b2*v + (1-b2)*g*g
+ *   master = master * keep - lr_k * (m/(1-b1^t)) / (sqrt(v/(1-b2^t)) + eps)
+ *   output = master, rounded to bf16 (nearest, ties to even) or fp32
+ * Without decay, scale and clipping the 32-bit step equals zero_fsdp_step
+ * bit for bit.
+ *
+ * 8-bit states: master stays fp32; m and r = sqrt(v) are e4m3 codes with one
+ * scale 2^(e-127), a byte e, per 32 elements. Each step decodes them, works
+ * in binary32 on the fresh m and v, and rounds both stochastically (a
+ * deterministic hash of the seed, t and the element's place: the same call on
+ * the same state gives the same bits). Rounding to nearest would freeze v: a
+ * step moves it by about 1-b2 of itself, the codes of r are 6-12% apart. A
+ * nonzero v is never stored as zero; an infinite or NaN moment is stored as
+ * NaN and does not touch the scale of its neighbours.
+ *
+ * A context's calls read and write its state, its device table and one
+ * workspace: order them among themselves (one stream, or events), replays of
+ * two captured graphs included. */
+
+/* Context for `ntensors` parameters, split by rows as zero_fsdp_init does.
+ * In master/m/v every tensor's local piece starts on a multiple of 2048
+ * elements and is followed by zeros; zero_shard_info reports the padded
+ * length as `shard`. state_bits is 32 or 8; seed belongs to the 8-bit
+ * rounding (with 32 bits it is not used). Weight decay starts at 0 and the
+ * learning-rate scale at 1 for every tensor.
+ * zero_fsdp_local, zero_fsdp_load_master, zero_set_lr, the schedule calls,
+ * zero_get_state / zero_set_state, zero_shard_state_bytes and zero_destroy
+ * apply; zero_fsdp_step does with 32 bits only. zero_get_state gives m and v
+ * of 8-bit states in fp32 exactly; zero_set_state rounds them to the nearest
+ * codes, which leaves values that came from zero_get_state unchanged, except
+ * a v below 2^-126, which fp32 cannot square exactly.
+ * EINVAL: as zero_fsdp_init (but any world up to ZERO_MAX_WORLD), state_bits
+ * not 8 or 32, more elements than 64 bits count. EUNSUPPORTED: more than 3.4e10
+ * local elements. ENOMEM / EHIP as zero_shard_init. Synchronous. */
+int zero_adamw_init(int32_t ntensors, const int64_t *dim0,
+                    const int64_t *row_numel, int32_t world, int32_t rank,
+                    double lr, double beta1, double beta2, double eps,
+                    int32_t state_bits, uint32_t seed, zero_ctx **out);
+
+/* Weight decay and learning-rate scale per tensor (host arrays of ntensors;
+ * NULL: 0, or 1, for all), rounded to fp32, for the steps after it on the
+ * stream; a captured step takes what holds when it replays. EINVAL: not an
+ * AdamW context, a decay that is negative or not finite, a scale that is not
+ * finite. */
+int zero_adamw_groups(zero_ctx *ctx, const double *weight_decay,
+                      const double *lr_scale, hipStream_t stream);
+
+/* The gradients that later calls read and the outputs that steps write, for
+ * the calls after it on the stream. grads: host array of n_replicas *
+ * ntensors device pointers, replica-major, each to this rank's first element
+ * of the tensor (the rows zero_fsdp_local gives), any alignment of the
+ * dtype. n_replicas is world for gradients still to be reduced, 1 for
+ * reduced ones: the mean is over what is bound. params_out: ntensors device
+ * pointers to this rank's rows, or NULL to bind gradients alone (for
+ * zero_adamw_sumsq). Pointers of tensors of which this rank holds no rows
+ * may be NULL. The buffers stay the caller's and must live until the last
+ * call or graph replay that uses them. A later bind may change any pointer,
+ * also under graphs captured before it, but not the replica count, a dtype,
+ * or whether outputs are bound (EINVAL). Other EINVAL: not an AdamW context,
+ * n_replicas outside [1, ZERO_FSDP_MAX_WORLD], null or misaligned pointers,
+ * ranges past their allocations. */
+int zero_adamw_bind(zero_ctx *ctx, const void *const *grads,
+                    int32_t n_replicas, zero_dtype grad_dtype,
+                    void *const *params_out, zero_dtype param_dtype,
+                    hipStream_t stream);
+
+/* *sumsq (device) = sum of the squares of the mean gradient over this rank's
+ * elements, in binary64 throughout and in a fixed order: the same gradients
+ * give the same bits. Ranks that hold different rows add theirs (one
+ * all-reduce of one number); its root is the gradient's norm. One launch.
+ * EINVAL: not an AdamW context, nothing bound, null or misaligned sum. */
+int zero_adamw_sumsq(zero_ctx *ctx, double *sumsq, hipStream_t stream);
+
+/* One step at step number t >= 1 on the bound buffers. sumsq: device pointer
+ * to the sum to clip by, read when the step runs, or NULL for no clipping
+ * (max_norm is then not read). Where it is infinite or NaN the step writes
+ * nothing at all: state and outputs keep their values. EINVAL: not an AdamW
+ * context, t < 1, no gradients or outputs bound, misaligned sum, max_norm
+ * not finite or <= 0. */
+int zero_adamw_step(zero_ctx *ctx, int64_t t, const double *sumsq,
+                    double max_norm, hipStream_t stream);
+
+/* zero_step_begin followed by zero_adamw_step at the step just begun (the
+ * count advances also where a step that is not finite writes nothing). */
+int zero_adamw_step_sched(zero_ctx *ctx, const double *sumsq, double max_norm,
+                          hipStream_t stream);
+
+/* Device addresses of the state: fp32 master, m and v with 32 bits; with 8
+ * the fp32 master, the codes of m and of r (one byte each) and the scales
+ * (per 2048 elements 64 bytes of m, then 64 of r; scale is NULL with 32
+ * bits). They hold until zero_destroy. Any out-pointer may be NULL. EINVAL:
+ * not an AdamW context. */
+int zero_adamw_state(const zero_ctx *ctx, void **master, void **m, void **v,
+                     void **scale);
+
 /* Copy the fp32 state out of / into the context (checkpoint and resume):
  * the master copy of this rank's slice and the two moments that [ZeRO and
  * FSDP], ZeroAdam constructor, creates per rank (master = the slice of the

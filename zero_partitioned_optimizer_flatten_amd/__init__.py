@@ -79,6 +79,14 @@ def lib():
     L.zero_step_range_sched.argtypes = [vp, i64, i64, vp, i32, ctypes.c_int, i64, vp,
                                         ctypes.c_int, i64, vp]
     L.zero_fsdp_step_sched.argtypes = [vp, vp, i32, ctypes.c_int, vp, ctypes.c_int, vp]
+    u32, pvp = ctypes.c_uint32, ctypes.POINTER(vp)
+    L.zero_adamw_init.argtypes = [i32, vp, vp, i32, i32, dbl, dbl, dbl, dbl, i32, u32, pvp]
+    L.zero_adamw_groups.argtypes = [vp, vp, vp, vp]
+    L.zero_adamw_bind.argtypes = [vp, vp, i32, ctypes.c_int, vp, ctypes.c_int, vp]
+    L.zero_adamw_sumsq.argtypes = [vp, vp, vp]
+    L.zero_adamw_step.argtypes = [vp, i64, vp, dbl, vp]
+    L.zero_adamw_step_sched.argtypes = [vp, vp, dbl, vp]
+    L.zero_adamw_state.argtypes = [vp, pvp, pvp, pvp, pvp]
     L.zero_get_state.argtypes = [vp, vp, vp, vp, vp]
     L.zero_set_state.argtypes = [vp, vp, vp, vp, vp]
     L.zero_state_bytes.argtypes = [i32, dbl, dbl, ctypes.POINTER(dbl)]
@@ -418,12 +426,16 @@ class FsdpShardState(ShardState):
                                         float(betas[0]), float(betas[1]), float(eps),
                                         ctypes.byref(h)))
         self._h = h
+        self._read_layout()
+
+    def _read_layout(self):
+        """shard, numel and every parameter's (first row, rows, state offset)."""
         s_, lo, p = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
         _check(lib().zero_shard_info(self._h, ctypes.byref(s_), ctypes.byref(lo), ctypes.byref(p)))
         self.shard, self.lo, self.padded = s_.value, lo.value, p.value
         self.numel = sum(int(torch.Size(s).numel()) for s in self.shapes)
         self.local = []
-        for k in range(n):
+        for k in range(len(self.shapes)):
             f, r, off = ctypes.c_int64(), ctypes.c_int64(), ctypes.c_int64()
             _check(lib().zero_fsdp_local(self._h, k, ctypes.byref(f), ctypes.byref(r),
                                          ctypes.byref(off)))
@@ -509,3 +521,189 @@ class FsdpShardState(ShardState):
                                           if len(self.shapes[k]) > 1 else 1)]
                         for k, (_, r, off) in enumerate(self.local)])
         return out
+
+
+class _Memory:
+    """Library memory as torch sees it: torch.as_tensor(_Memory(...)) shares
+    the buffer and keeps `owner` alive."""
+
+    def __init__(self, owner, ptr: int, count: int, typestr: str):
+        self.owner = owner
+        self.__cuda_array_interface__ = dict(shape=(count,), typestr=typestr,
+                                             data=(ptr, False), version=2)
+
+
+class AdamWState(FsdpShardState):
+    """AdamW over many tensors at once, one rank of the per-parameter layout:
+    decoupled weight decay and a learning-rate scale per parameter (a number
+    for all, or one each), clipping by a norm that stays on the device, and
+    states in 32 or 8 bits. Gradients and outputs are bound once; a step is
+    one launch and can be captured in a HIP graph.
+
+        st = AdamWState([p.shape for p in params], world, rank, lr, weight_decay=0.1)
+        st.load_master(params)
+        st.bind([[p.grad for p in params]], params_out)
+        s = st.sumsq()                       # all_reduce(s) where ranks share a model
+        st.step(t, sumsq=s, max_norm=1.0)
+
+    Inherits get_state / set_state / state_bytes / set_lr / load_master and the
+    schedule calls; calls on one state must be ordered among themselves."""
+
+    def __init__(self, shapes, world: int, rank: int, lr: float,
+                 betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
+                 weight_decay=0.0, lr_scale=1.0, state_bits: int = 32, seed: int = 0,
+                 device=None):
+        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
+            else torch.device(device)
+        if self.device.index is None:
+            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.shapes = [tuple(int(d) for d in s) for s in shapes]
+        self.world, self.rank, self.state_bits = int(world), int(rank), int(state_bits)
+        if not 0 <= int(seed) < 1 << 32:
+            raise ValueError(f"seed must be in [0, 2^32), got {seed}")
+        n = len(self.shapes)
+        dim0 = (ctypes.c_int64 * max(1, n))(*[s[0] if s else 1 for s in self.shapes])
+        # a parameter without elements has no rows; the library wants rows of >= 1
+        rown = [int(torch.Size(s[1:]).numel()) if len(s) > 1 else 1 for s in self.shapes]
+        for k, r in enumerate(rown):
+            if r == 0:
+                dim0[k], rown[k] = 0, 1
+        rown = (ctypes.c_int64 * max(1, n))(*rown)
+        h = ctypes.c_void_p()
+        with torch.cuda.device(self.device):
+            _check(lib().zero_adamw_init(n, dim0, rown, self.world, self.rank, float(lr),
+                                         float(betas[0]), float(betas[1]), float(eps),
+                                         self.state_bits, int(seed), ctypes.byref(h)))
+        self._h = h
+        self._bound = None
+        self._read_layout()
+        self.set_groups(weight_decay, lr_scale)
+
+    def _stream(self, stream):
+        """The given stream, or this device's current one (whatever device is
+        current in the caller)."""
+        s = torch.cuda.current_stream(self.device) if stream is None else stream
+        if s.device != self.device:
+            raise ValueError(f"stream is on {s.device}, state is on {self.device}")
+        return ctypes.c_void_p(s.cuda_stream)
+
+    def set_groups(self, weight_decay=0.0, lr_scale=1.0, stream=None):
+        """Weight decay and learning-rate scale of later steps: a number for
+        every parameter, or a sequence with one each."""
+        n = len(self.shapes)
+        arrays = []
+        for name, x in (("weight_decay", weight_decay), ("lr_scale", lr_scale)):
+            x = [float(v) for v in x] if isinstance(x, (list, tuple)) else [float(x)] * n
+            if len(x) != n:
+                raise ValueError(f"{name}: need {n} values, got {len(x)}")
+            arrays.append((ctypes.c_double * max(1, n))(*x))
+        _check(lib().zero_adamw_groups(self._h, *arrays, self._stream(stream)))
+
+    def _local_ptr(self, x: Optional[torch.Tensor], k: int, what: str, whole: bool) -> int:
+        """Address of this rank's elements of parameter k in x, which holds
+        these alone or, for a gradient (`whole`), the whole parameter."""
+        local = self.local_numel(k)
+        if local == 0:
+            return 0
+        if x is None:
+            raise ValueError(f"{what} is None but this rank holds rows of it")
+        self._dev(x, what)
+        full = int(torch.Size(self.shapes[k]).numel())
+        if x.numel() == local:
+            return x.data_ptr()
+        if whole and x.numel() == full:
+            first, rows, _ = self.local[k]
+            return x.data_ptr() + first * (local // rows) * x.element_size()
+        raise ValueError(f"{what} has {x.numel()} elements, need {local}"
+                         + (f" (this rank's) or {full}" if whole else ""))
+
+    def bind(self, grads: Sequence[Sequence[Optional[torch.Tensor]]],
+             params_out: Optional[Sequence[Optional[torch.Tensor]]] = None, stream=None):
+        """grads[q][k]: replica q's gradient of parameter k, this rank's rows
+        or all of them; the mean is over the replicas given (one list for
+        gradients that are reduced already). params_out[k]: this rank's rows,
+        written by steps; None binds gradients alone (for sumsq). None is
+        taken for parameters of which this rank holds no rows. The state
+        keeps the tensors alive until the next bind."""
+        n = len(self.shapes)
+        for q, gl in enumerate(grads):
+            if len(gl) != n:
+                raise ValueError(f"grads[{q}]: need {n} tensors, got {len(gl)}")
+        if params_out is not None and len(params_out) != n:
+            raise ValueError(f"params_out: need {n} tensors, got {len(params_out)}")
+        held = [k for k in range(n) if self.local_numel(k)]
+        gdts = {gl[k].dtype for gl in grads for k in held if gl[k] is not None}
+        pdts = {params_out[k].dtype for k in held if params_out[k] is not None} \
+            if params_out is not None else set()
+        if len(gdts) > 1 or len(pdts) > 1:
+            raise TypeError("gradients must share one dtype, and outputs one")
+        gptrs = _ptr_array([self._local_ptr(gl[k], k, f"grads[{q}][{k}]", True)
+                            for q, gl in enumerate(grads) for k in range(n)])
+        optrs = None if params_out is None else _ptr_array(
+            [self._local_ptr(x, k, f"params_out[{k}]", False) for k, x in enumerate(params_out)])
+        gdt = _dtype_code(gdts.pop()) if gdts else ZERO_F32
+        pdt = _dtype_code(pdts.pop()) if pdts else ZERO_F32
+        _check(lib().zero_adamw_bind(self._h, gptrs, len(grads), gdt, optrs, pdt,
+                                     self._stream(stream)))
+        self._bound = ([list(gl) for gl in grads],
+                       None if params_out is None else list(params_out))
+
+    def _sum_ptr(self, x: Optional[torch.Tensor]):
+        if x is None:
+            return None
+        self._dev(x, "sumsq")
+        if x.dtype != torch.float64 or x.numel() != 1:
+            raise ValueError("sumsq must be one float64")
+        return x.data_ptr()
+
+    def sumsq(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """Sum of squares of the mean gradient over this rank's elements, as
+        one float64 on the device (its root is the norm); written to `out`,
+        or to a new tensor of the call's stream."""
+        if out is None:
+            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+                out = torch.empty(1, dtype=torch.float64, device=self.device)
+        _check(lib().zero_adamw_sumsq(self._h, self._sum_ptr(out), self._stream(stream)))
+        return out
+
+    def step(self, t: int, sumsq: Optional[torch.Tensor] = None,
+             max_norm: Optional[float] = None, stream=None):
+        """One step at step number t on the bound buffers. With sumsq (the
+        sum over all ranks, on the device) the gradient is scaled by
+        min(1, max_norm / (sqrt(sumsq) + 1e-6)), and a sum that is not finite
+        makes the step write nothing."""
+        if sumsq is not None and max_norm is None:
+            raise ValueError("clipping needs max_norm")
+        _check(lib().zero_adamw_step(self._h, int(t), self._sum_ptr(sumsq),
+                                     float(max_norm or 0.0), self._stream(stream)))
+
+    def step_sched(self, sumsq: Optional[torch.Tensor] = None,
+                   max_norm: Optional[float] = None, stream=None):
+        """step() at the device schedule's next step count and lr; advances
+        the count. Capturable in a HIP graph."""
+        if sumsq is not None and max_norm is None:
+            raise ValueError("clipping needs max_norm")
+        _check(lib().zero_adamw_step_sched(self._h, self._sum_ptr(sumsq),
+                                           float(max_norm or 0.0), self._stream(stream)))
+
+    def state_tensors(self) -> dict:
+        """The state itself, sharing the library's memory (until close()):
+        master, m, v in fp32, or with 8 bits master in fp32, m and r = sqrt(v)
+        as float8_e4m3fn codes and scale as float8_e8m0fnu, shaped
+        [shard / 2048, 2, 64]: of every 32 elements of m, then of r."""
+        ptr = [ctypes.c_void_p() for _ in range(4)]
+        _check(lib().zero_adamw_state(self._h, *[ctypes.byref(p) for p in ptr]))
+
+        def share(p, count, typestr):
+            if count == 0:
+                dt = torch.float32 if typestr == "<f4" else torch.uint8
+                return torch.empty(0, dtype=dt, device=self.device)
+            return torch.as_tensor(_Memory(self, p.value, count, typestr), device=self.device)
+
+        n = self.shard
+        if self.state_bits == 32:
+            return dict(zip(("master", "m", "v"), (share(p, n, "<f4") for p in ptr[:3])))
+        return dict(master=share(ptr[0], n, "<f4"),
+                    m=share(ptr[1], n, "|u1").view(torch.float8_e4m3fn),
+                    r=share(ptr[2], n, "|u1").view(torch.float8_e4m3fn),
+                    scale=share(ptr[3], n // 16, "|u1").view(torch.float8_e8m0fnu).view(-1, 2, 64))

@@ -8,7 +8,7 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libzero.so")
-SOURCES = ["zero_api.hip", "zero_kernels.hip"]
+SOURCES = ["zero_api.hip", "zero_kernels.hip", "adamw_kernels.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Numerics: no implicit fusion, correctly rounded fp32 divide and sqrt,

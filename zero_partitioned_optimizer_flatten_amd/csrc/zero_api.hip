@@ -50,6 +50,24 @@ struct zero_ctx {
     // is refused. Host call order is the launch order on a stream, also
     // under capture.
     bool begun;
+    // AdamW over many tensors (zero_adamw_init): state_bits 32 or 8, 0 on
+    // other contexts. With 8 the moments are m8, r8 and scale, and m, v are
+    // null. aw_mem holds the device table of tensors, the piece-to-tensor
+    // map and the workspace of the sum of squares; aw_tensors mirrors the
+    // table on the host.
+    int32_t state_bits;
+    uint32_t sr_seed;            // mixed seed of the stochastic rounding
+    uint8_t *m8, *r8, *scale;
+    int64_t npieces;
+    void *aw_mem;
+    zk::AdamwTensor *aw_table;
+    int32_t *aw_map;
+    double *aw_partial;
+    uint32_t *aw_done;
+    std::vector<zk::AdamwTensor> aw_tensors;
+    int32_t aw_n;                // replicas bound (0: nothing bound yet)
+    zero_dtype aw_grad_dtype, aw_param_dtype;
+    bool aw_has_out;             // outputs bound
 };
 
 // The static schedule block of zero_schedule_init_noalloc: one per device
@@ -113,6 +131,10 @@ int reject_fsdp(const zero_ctx *c) {
         return fail(ZERO_EINVAL, "this context holds the per-parameter (dim-0) layout; "
                                  "use the zero_fsdp_* calls");
     return ZERO_OK;
+}
+
+zk::AdamwStateRef adamw_state(const zero_ctx *c) {
+    return {c->master, c->m, c->v, c->m8, c->r8, c->scale};
 }
 
 // Make the context's device current for the duration of a call.
@@ -330,6 +352,27 @@ static int check_hparams(int32_t world, double lr, double beta1, double beta2, d
     return ZERO_OK;
 }
 
+// The current device becomes the context's.
+static int use_current_device(zero_ctx *c) {
+    int dev = 0;
+    hipError_t e = hipGetDevice(&dev);
+    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
+    int cus = 0;
+    e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
+    if (e != hipSuccess) return hip_fail(e, "hipDeviceGetAttribute");
+    c->device = dev;
+    c->num_cus = cus > 0 ? cus : 256;
+    // the static schedule block's address on this device, resolved at set-up
+    // so that zero_schedule_init_noalloc makes no runtime query later; a
+    // failure here only matters to that call, which resolves it again and
+    // reports it
+    if (dev >= 0 && dev < kMaxDevices) {
+        void *unused = nullptr;
+        if (scratch_address(dev, &unused) != ZERO_OK) g_last_error.clear();
+    }
+    return ZERO_OK;
+}
+
 // Device, master/m/v (`shard` elements each, zeroed) for a filled-in context.
 // Each of master | m | v starts on a 2 MiB boundary of the allocation
 // (measured: arrays packed at 256-byte granularity, which leaves m and v
@@ -351,22 +394,9 @@ static const size_t kStateStagger = (size_t)1 << 20;
 // elements, on wavefront blocks that fill whole 128-byte lines of every
 // stream.
 static int alloc_state(zero_ctx *c, int shift) {
-    int dev = 0;
-    hipError_t e = hipGetDevice(&dev);
-    if (e != hipSuccess) return hip_fail(e, "hipGetDevice");
-    int cus = 0;
-    e = hipDeviceGetAttribute(&cus, hipDeviceAttributeMultiprocessorCount, dev);
-    if (e != hipSuccess) return hip_fail(e, "hipDeviceGetAttribute");
-    c->device = dev;
-    c->num_cus = cus > 0 ? cus : 256;
-    // the static schedule block's address on this device, resolved at set-up
-    // so that zero_schedule_init_noalloc makes no runtime query later; a
-    // failure here only matters to that call, which resolves it again and
-    // reports it
-    if (dev >= 0 && dev < kMaxDevices) {
-        void *unused = nullptr;
-        if (scratch_address(dev, &unused) != ZERO_OK) g_last_error.clear();
-    }
+    int rc = use_current_device(c);
+    if (rc) return rc;
+    hipError_t e;
     // master | m | v, each segment a whole number of kStateAlign blocks plus
     // kStateStagger, the first starting on a kStateAlign boundary inside the
     // allocation
@@ -509,6 +539,7 @@ int zero_fsdp_load_master(zero_ctx *c, const void *const *params, zero_dtype dty
     if (!c || !c->fsdp) return fail(ZERO_EINVAL, "not a per-parameter layout context");
     if (!params) return fail(ZERO_EINVAL, "null parameter array");
     CaptureScope cs(stream);
+    const bool q8 = c->state_bits == 8;
     if (!valid_dtype(dtype)) return fail(ZERO_EINVAL, "unknown dtype %d", (int)dtype);
     const int64_t es = (int64_t)dtype_size(dtype);
     for (size_t k = 0; k < c->tensors.size(); ++k) {
@@ -521,10 +552,20 @@ int zero_fsdp_load_master(zero_ctx *c, const void *const *params, zero_dtype dty
     }
     DeviceGuard g(c->device);
     if (g.error() != hipSuccess) return hip_fail(g.error(), "hipSetDevice");
+    if (q8) {
+        hipError_t e = zk::launch_adamw_clear(adamw_state(c), c->npieces, stream);
+        if (e != hipSuccess) return hip_fail(e, "clearing the 8-bit states");
+    }
     for (size_t k = 0; k < c->tensors.size(); ++k) {
         const zero_fsdp_tensor &t = c->tensors[k];
         if (t.rows == 0) continue;
         const char *base = (const char *)params[k] + t.first_row * t.row_numel * es;
+        if (q8) {
+            hipError_t e = zk::launch_widen(base, dtype == ZERO_BF16, c->master + t.state_off,
+                                            t.rows * t.row_numel, stream);
+            if (e != hipSuccess) return hip_fail(e, "load_master launch");
+            continue;
+        }
         hipError_t e = zk::launch_load_master(base, dtype == ZERO_BF16, c->master + t.state_off,
                                               c->m + t.state_off, c->v + t.state_off,
                                               t.rows * t.row_numel, stream);
@@ -538,6 +579,8 @@ static int fsdp_step_common(zero_ctx *c, const void *const *grads, int32_t n_rep
                             zero_dtype param_dtype, int64_t t, StepMode mode,
                             hipStream_t stream) {
     if (!c || !c->fsdp) return fail(ZERO_EINVAL, "not a per-parameter layout context");
+    if (c->state_bits == 8)
+        return fail(ZERO_EINVAL, "this context holds 8-bit states; use zero_adamw_step");
     CaptureScope cs(stream);
     if (n_replicas != c->world)
         return fail(ZERO_EINVAL, "n_replicas (%d) must equal world (%d)", n_replicas, c->world);
@@ -636,6 +679,12 @@ int zero_shard_state_bytes(const zero_ctx *c, int64_t *bytes) {
         for (const zero_fsdp_tensor &t : c->tensors) elems += t.rows * t.row_numel;
     }
     *bytes = 3 * (int64_t)sizeof(float) * elems;
+    if (c->state_bits == 8) {
+        // fp32 master, two codes, and two scales per block of a tensor
+        *bytes = ((int64_t)sizeof(float) + 2) * elems;
+        for (const zero_fsdp_tensor &t : c->tensors)
+            *bytes += 2 * ((t.rows * t.row_numel + zk::kAdamwBlock - 1) / zk::kAdamwBlock);
+    }
     return ZERO_OK;
 }
 
@@ -1021,8 +1070,32 @@ static int copy_state(const zero_ctx *c, const float *const src[3], float *const
     return ZERO_OK;
 }
 
+// The 8-bit states as fp32 m and v, out of or into the context.
+static int convert_state(const zero_ctx *c, float *get_m, float *get_v, const float *set_m,
+                         const float *set_v, hipStream_t stream) {
+    CaptureScope cs(stream);
+    const void *p[4] = {get_m, get_v, set_m, set_v};
+    for (const void *x : p) {
+        if (!x) continue;
+        if ((uintptr_t)x % sizeof(float)) return fail(ZERO_EINVAL, "state buffer misaligned");
+        int rc = check_range(x, c->shard * (int64_t)sizeof(float), "state buffer");
+        if (rc) return rc;
+    }
+    DeviceGuard g(c->device);
+    if (g.error() != hipSuccess) return hip_fail(g.error(), "hipSetDevice");
+    hipError_t e = zk::launch_adamw_decode(adamw_state(c), c->npieces, get_m, get_v, stream);
+    if (e == hipSuccess)
+        e = zk::launch_adamw_encode(adamw_state(c), c->npieces, set_m, set_v, stream);
+    return e == hipSuccess ? ZERO_OK : hip_fail(e, "8-bit state conversion");
+}
+
 int zero_get_state(const zero_ctx *c, float *master, float *m, float *v, hipStream_t stream) {
     if (!c) return fail(ZERO_EINVAL, "null context");
+    if (c->state_bits == 8) {
+        int rc = convert_state(c, m, v, nullptr, nullptr, stream);
+        if (rc) return rc;
+        m = v = nullptr;
+    }
     const float *src[3] = {c->master, c->m, c->v};
     float *dst[3] = {master, m, v};
     return copy_state(c, src, dst, stream, "get_state copy");
@@ -1031,9 +1104,366 @@ int zero_get_state(const zero_ctx *c, float *master, float *m, float *v, hipStre
 int zero_set_state(zero_ctx *c, const float *master, const float *m, const float *v,
                    hipStream_t stream) {
     if (!c) return fail(ZERO_EINVAL, "null context");
+    if (c->state_bits == 8) {
+        int rc = convert_state(c, nullptr, nullptr, m, v, stream);
+        if (rc) return rc;
+        m = v = nullptr;
+    }
     const float *src[3] = {master, m, v};
     float *dst[3] = {c->master, c->m, c->v};
     return copy_state(c, src, dst, stream, "set_state copy");
+}
+
+// ------------------------------------------------- AdamW over many tensors
+
+static_assert(zk::kAdamwMaxReplicas == ZERO_FSDP_MAX_WORLD, "one replica limit");
+
+static int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; }
+
+// The table and map of a filled-in context, and the workspace of the sum of
+// squares, in one allocation; uploaded before the call returns.
+static int alloc_adamw_table(zero_ctx *c) {
+    const size_t nt = c->aw_tensors.size();
+    const size_t table = (size_t)round_up((int64_t)(nt * sizeof(zk::AdamwTensor)), 256);
+    const size_t map = (size_t)round_up(c->npieces * (int64_t)sizeof(int32_t), 256);
+    const size_t partial = zk::kSumsqGroups * sizeof(double);
+    const size_t bytes = table + map + partial + 256;
+    std::vector<int32_t> host_map;
+    try {
+        host_map.resize((size_t)c->npieces);
+    } catch (...) {
+        return fail(ZERO_ENOMEM, "host allocation failed");
+    }
+    for (size_t k = 0; k < nt; ++k) {
+        const int64_t p0 = c->aw_tensors[k].piece0;
+        const int64_t np = round_up(c->aw_tensors[k].numel, zk::kAdamwPiece) / zk::kAdamwPiece;
+        for (int64_t p = p0; p < p0 + np; ++p) host_map[(size_t)p] = (int32_t)k;
+    }
+    hipError_t e = hipMalloc(&c->aw_mem, bytes);
+    if (e != hipSuccess) {
+        (void)hipGetLastError();
+        c->aw_mem = nullptr;
+        return fail(ZERO_ENOMEM, "hipMalloc of %zu bytes for the tensor table failed", bytes);
+    }
+    char *base = (char *)c->aw_mem;
+    c->aw_table = (zk::AdamwTensor *)base;
+    c->aw_map = (int32_t *)(base + table);
+    c->aw_partial = (double *)(base + table + map);
+    c->aw_done = (uint32_t *)(base + table + map + partial);
+    e = hipMemset(c->aw_mem, 0, bytes);
+    if (e == hipSuccess)
+        e = hipMemcpy(c->aw_table, c->aw_tensors.data(), nt * sizeof(zk::AdamwTensor),
+                      hipMemcpyHostToDevice);
+    if (e == hipSuccess && c->npieces > 0)
+        e = hipMemcpy(c->aw_map, host_map.data(), (size_t)c->npieces * sizeof(int32_t),
+                      hipMemcpyHostToDevice);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    return e == hipSuccess ? ZERO_OK : hip_fail(e, "uploading the tensor table");
+}
+
+// master | m codes | r codes | scales of an 8-bit context, zeroed, every
+// scale the smallest. Each starts on kStateAlign, a kStateStagger further
+// than the one before, as in alloc_state.
+static int alloc_state8(zero_ctx *c) {
+    int rc = use_current_device(c);
+    if (rc) return rc;
+    const size_t n = (size_t)c->shard;
+    const size_t need[4] = {n * sizeof(float), n, n, n / zk::kAdamwBlock * 2};
+    size_t at[4], bytes = 0;
+    for (int k = 0; k < 4; ++k) {
+        at[k] = bytes;
+        bytes += (size_t)round_up((int64_t)need[k], (int64_t)kStateAlign) + kStateStagger;
+    }
+    bytes += kStateAlign;
+    hipError_t e = hipMalloc(&c->state, bytes);
+    if (e != hipSuccess) {
+        (void)hipGetLastError();
+        c->state = nullptr;
+        return fail(ZERO_ENOMEM, "hipMalloc of %zu bytes for the 8-bit states failed: %s", bytes,
+                    hipGetErrorString(e));
+    }
+    char *base = (char *)(((uintptr_t)c->state + kStateAlign - 1) & ~(uintptr_t)(kStateAlign - 1));
+    c->master = (float *)(base + at[0]);
+    c->m8 = (uint8_t *)(base + at[1]);
+    c->r8 = (uint8_t *)(base + at[2]);
+    c->scale = (uint8_t *)(base + at[3]);
+    e = hipMemset(c->state, 0, bytes);
+    if (e == hipSuccess) e = hipMemset(c->scale, 1, need[3]);
+    if (e == hipSuccess) e = hipDeviceSynchronize();
+    return e == hipSuccess ? ZERO_OK : hip_fail(e, "clearing the 8-bit states");
+}
+
+int zero_adamw_init(int32_t ntensors, const int64_t *dim0, const int64_t *row_numel,
+                    int32_t world, int32_t rank, double lr, double beta1, double beta2, double eps,
+                    int32_t state_bits, uint32_t seed, zero_ctx **out) {
+    if (!out) return fail(ZERO_EINVAL, "null output pointer");
+    *out = nullptr;
+    if (ntensors < 1 || !dim0 || !row_numel)
+        return fail(ZERO_EINVAL, "need ntensors >= 1 and both shape arrays");
+    if (world < 1 || rank < 0 || rank >= world)
+        return fail(ZERO_EINVAL, "rank must be in [0, world) with world >= 1");
+    if (state_bits != 8 && state_bits != 32)
+        return fail(ZERO_EINVAL, "state_bits must be 8 or 32 (got %d)", state_bits);
+    int rc = check_hparams(world, lr, beta1, beta2, eps);
+    if (rc) return rc;
+    zero_ctx *c = new (std::nothrow) zero_ctx();
+    if (!c) return fail(ZERO_ENOMEM, "host allocation failed");
+    c->fsdp = true;
+    c->world = world;
+    c->rank = rank;
+    c->lr = lr;
+    c->beta1 = beta1;
+    c->beta2 = beta2;
+    c->eps = eps;
+    c->state_bits = state_bits;
+    c->sr_seed = zk::adamw_mix(seed);
+    try {
+        c->tensors.resize((size_t)ntensors);
+        c->aw_tensors.resize((size_t)ntensors);
+    } catch (...) {
+        delete c;
+        return fail(ZERO_ENOMEM, "host allocation failed");
+    }
+    for (int32_t k = 0; k < ntensors; ++k) {
+        int64_t full = 0;
+        if (dim0[k] < 0 || row_numel[k] < 1 ||
+            __builtin_mul_overflow(dim0[k], row_numel[k], &full) ||
+            __builtin_add_overflow(c->numel, full, &c->numel)) {
+            delete c;
+            return fail(ZERO_EINVAL, "tensor %d: need dim0 >= 0, row_numel >= 1 and a total "
+                                     "element count that fits 64 bits", k);
+        }
+    }
+    int64_t piece = 0;
+    for (int32_t k = 0; k < ntensors; ++k) {
+        zero_fsdp_tensor &t = c->tensors[(size_t)k];
+        t.dim0 = dim0[k];
+        t.row_numel = row_numel[k];
+        dim0_split(t.dim0, world, rank, &t.first_row, &t.rows);
+        t.state_off = piece * zk::kAdamwPiece;
+        zk::AdamwTensor &a = c->aw_tensors[(size_t)k];
+        a = {};
+        a.numel = t.rows * t.row_numel;
+        a.piece0 = piece;
+        a.decay = 0.0f;
+        a.factor = 1.0f;
+        const int64_t np = a.numel / zk::kAdamwPiece + (a.numel % zk::kAdamwPiece != 0 ? 1 : 0);
+        if (np > zk::kAdamwMaxPieces - piece) {
+            delete c;
+            return fail(ZERO_EUNSUPPORTED, "this rank's elements exceed the %lld of one launch",
+                        (long long)(zk::kAdamwMaxPieces * zk::kAdamwPiece));
+        }
+        piece += np;
+    }
+    c->npieces = piece;
+    c->shard = c->padded = piece * zk::kAdamwPiece;
+    c->lo = 0;
+    rc = state_bits == 8 ? alloc_state8(c) : alloc_state(c, 0);
+    if (!rc) rc = alloc_adamw_table(c);
+    if (rc) {
+        zero_destroy(c);      // leaves the message of the failure
+        return rc;
+    }
+    *out = c;
+    return ZERO_OK;
+}
+
+static int need_adamw(const zero_ctx *c) {
+    if (!c) return fail(ZERO_EINVAL, "null context");
+    if (!c->state_bits)
+        return fail(ZERO_EINVAL, "not a context of zero_adamw_init");
+    return ZERO_OK;
+}
+
+// The host's table to the device, stream-ordered, carried by kernel
+// arguments: no staging buffer that the call would have to keep.
+static int upload_table(zero_ctx *c, const std::vector<zk::AdamwTensor> &tab, hipStream_t stream) {
+    static_assert(sizeof(zk::AdamwTensor) % sizeof(uint32_t) == 0, "whole words");
+    DeviceGuard g(c->device);
+    if (g.error() != hipSuccess) return hip_fail(g.error(), "hipSetDevice");
+    const size_t words = tab.size() * sizeof(zk::AdamwTensor) / sizeof(uint32_t);
+    const char *src = (const char *)tab.data();
+    uint32_t *dst = (uint32_t *)c->aw_table;
+    zk::WordChunk chunk;
+    for (size_t done = 0; done < words; done += (size_t)chunk.n) {
+        chunk.n = (int)(words - done < (size_t)zk::kWordChunk ? words - done : zk::kWordChunk);
+        std::memcpy(chunk.w, src + done * sizeof(uint32_t), (size_t)chunk.n * sizeof(uint32_t));
+        hipError_t e = zk::launch_fill_words(dst + done, chunk, stream);
+        if (e != hipSuccess) return hip_fail(e, "uploading the tensor table");
+    }
+    return ZERO_OK;
+}
+
+int zero_adamw_groups(zero_ctx *c, const double *weight_decay, const double *lr_scale,
+                      hipStream_t stream) {
+    int rc = need_adamw(c);
+    if (rc) return rc;
+    std::vector<zk::AdamwTensor> tab;
+    try {
+        tab = c->aw_tensors;
+    } catch (...) {
+        return fail(ZERO_ENOMEM, "host allocation failed");
+    }
+    for (size_t k = 0; k < tab.size(); ++k) {
+        const double d = weight_decay ? weight_decay[k] : 0.0, f = lr_scale ? lr_scale[k] : 1.0;
+        if (!std::isfinite(d) || d < 0.0 || !std::isfinite(f))
+            return fail(ZERO_EINVAL, "tensor %zu: weight decay must be finite and >= 0 and the "
+                                     "learning-rate scale finite (got %g, %g)", k, d, f);
+        tab[k].decay = (float)d;
+        tab[k].factor = (float)f;
+    }
+    rc = upload_table(c, tab, stream);
+    if (rc) return rc;
+    c->aw_tensors.swap(tab);
+    return ZERO_OK;
+}
+
+int zero_adamw_bind(zero_ctx *c, const void *const *grads, int32_t n_replicas,
+                    zero_dtype grad_dtype, void *const *params_out, zero_dtype param_dtype,
+                    hipStream_t stream) {
+    int rc = need_adamw(c);
+    if (rc) return rc;
+    CaptureScope cs(stream);
+    if (!grads) return fail(ZERO_EINVAL, "null gradient array");
+    if (n_replicas < 1 || n_replicas > ZERO_FSDP_MAX_WORLD)
+        return fail(ZERO_EINVAL, "n_replicas must be in [1, %d] (got %d)", ZERO_FSDP_MAX_WORLD,
+                    n_replicas);
+    if (!valid_dtype(grad_dtype) || (params_out && !valid_dtype(param_dtype)))
+        return fail(ZERO_EINVAL, "unknown dtype");
+    if (c->aw_n && (n_replicas != c->aw_n || grad_dtype != c->aw_grad_dtype))
+        return fail(ZERO_EINVAL, "a context keeps the replica count and gradient dtype of its "
+                                 "first bind (a captured step has them compiled in)");
+    if (c->aw_has_out && (!params_out || param_dtype != c->aw_param_dtype))
+        return fail(ZERO_EINVAL, "a context keeps its outputs and their dtype once bound (a "
+                                 "captured step has them compiled in)");
+    const int64_t ge = (int64_t)dtype_size(grad_dtype);
+    const int64_t pe = params_out ? (int64_t)dtype_size(param_dtype) : 1;
+    const size_t nt = c->tensors.size();
+    std::vector<zk::AdamwTensor> tab;
+    try {
+        tab = c->aw_tensors;
+    } catch (...) {
+        return fail(ZERO_ENOMEM, "host allocation failed");
+    }
+    for (size_t k = 0; k < nt; ++k) {
+        zk::AdamwTensor &t = tab[k];
+        if (t.numel == 0) continue;
+        for (int q = 0; q < n_replicas; ++q) {
+            const void *gp = grads[(size_t)q * nt + k];
+            if (!gp) return fail(ZERO_EINVAL, "gradient of replica %d, tensor %zu is null", q, k);
+            if ((uintptr_t)gp % (uintptr_t)ge)
+                return fail(ZERO_EINVAL, "gradient of replica %d, tensor %zu misaligned", q, k);
+            rc = check_range(gp, t.numel * ge, "gradient");
+            if (rc) return rc;
+            t.grads[q] = gp;
+        }
+        if (!params_out) continue;
+        if (!params_out[k]) return fail(ZERO_EINVAL, "output %zu is null", k);
+        if ((uintptr_t)params_out[k] % (uintptr_t)pe)
+            return fail(ZERO_EINVAL, "output %zu misaligned", k);
+        rc = check_range(params_out[k], t.numel * pe, "output");
+        if (rc) return rc;
+        t.out = params_out[k];
+    }
+    rc = upload_table(c, tab, stream);
+    if (rc) return rc;
+    c->aw_tensors.swap(tab);
+    c->aw_n = n_replicas;
+    c->aw_grad_dtype = grad_dtype;
+    if (params_out) {
+        c->aw_has_out = true;
+        c->aw_param_dtype = param_dtype;
+    }
+    return ZERO_OK;
+}
+
+int zero_adamw_sumsq(zero_ctx *c, double *sumsq, hipStream_t stream) {
+    int rc = need_adamw(c);
+    if (rc) return rc;
+    CaptureScope cs(stream);
+    if (!c->aw_n) return fail(ZERO_EINVAL, "no gradients bound: call zero_adamw_bind first");
+    if (!sumsq || (uintptr_t)sumsq % sizeof(double))
+        return fail(ZERO_EINVAL, "null or misaligned sum");
+    rc = check_range(sumsq, sizeof(double), "sum of squares");
+    if (rc) return rc;
+    DeviceGuard g(c->device);
+    if (g.error() != hipSuccess) return hip_fail(g.error(), "hipSetDevice");
+    const zk::SumsqArgs a = {c->aw_table, c->aw_map, c->npieces, c->aw_n,
+                             c->aw_grad_dtype == ZERO_BF16, c->aw_partial, c->aw_done, sumsq};
+    hipError_t e = zk::launch_sumsq(a, stream);
+    return e == hipSuccess ? ZERO_OK : hip_fail(e, "sum-of-squares launch");
+}
+
+static int adamw_step(zero_ctx *c, int64_t t, StepMode mode, const double *sumsq, double max_norm,
+                      hipStream_t stream) {
+    int rc = need_adamw(c);
+    if (rc) return rc;
+    CaptureScope cs(stream);
+    if (mode == kHostT && t < 1)
+        return fail(ZERO_EINVAL, "step t must be >= 1 (got %lld)", (long long)t);
+    if (mode != kHostT) {
+        rc = need_schedule(c);
+        if (rc) return rc;
+    }
+    if (!c->aw_n || !c->aw_has_out)
+        return fail(ZERO_EINVAL, "no gradients and outputs bound: call zero_adamw_bind first");
+    if (sumsq) {
+        if ((uintptr_t)sumsq % sizeof(double)) return fail(ZERO_EINVAL, "misaligned sum");
+        if (!std::isfinite(max_norm) || max_norm <= 0.0)
+            return fail(ZERO_EINVAL, "max_norm must be finite and > 0 (got %g)", max_norm);
+        rc = check_range(sumsq, sizeof(double), "sum of squares");
+        if (rc) return rc;
+    }
+    DeviceGuard g(c->device);
+    if (g.error() != hipSuccess) return hip_fail(g.error(), "hipSetDevice");
+    if (mode == kBeginDevice) {
+        hipError_t e = begin_device_step(c, stream);
+        if (e != hipSuccess) return hip_fail(e, "begin-step launch");
+        c->begun = true;
+    }
+    zk::AdamwArgs a = {};
+    a.table = c->aw_table;
+    a.map = c->aw_map;
+    a.npieces = c->npieces;
+    a.n = c->aw_n;
+    a.grad_bf16 = c->aw_grad_dtype == ZERO_BF16;
+    a.out_bf16 = c->aw_param_dtype == ZERO_BF16;
+    a.q8 = c->state_bits == 8;
+    a.st = adamw_state(c);
+    a.sc = make_scalars(c, mode == kHostT ? t : 1);
+    // the mean is over the bound replicas, which need not be `world`
+    a.sc.nf = (float)c->aw_n;
+    a.sc.n_pow2 = (c->aw_n & (c->aw_n - 1)) == 0;
+    a.sc.inv_n = (float)(1.0 / (double)c->aw_n);
+    a.sc_dev = mode == kHostT ? nullptr : c->sc_dev;
+    a.ds = c->ds;
+    a.seed = c->sr_seed;
+    a.t = (uint32_t)(uint64_t)t;
+    a.sumsq = sumsq;
+    a.max_norm = max_norm;
+    a.stream_state = zk::state_streams(c->shard);
+    hipError_t e = zk::launch_adamw(a, stream);
+    return e == hipSuccess ? ZERO_OK : hip_fail(e, "AdamW step launch");
+}
+
+int zero_adamw_step(zero_ctx *c, int64_t t, const double *sumsq, double max_norm,
+                    hipStream_t stream) {
+    return adamw_step(c, t, kHostT, sumsq, max_norm, stream);
+}
+
+int zero_adamw_step_sched(zero_ctx *c, const double *sumsq, double max_norm, hipStream_t stream) {
+    return adamw_step(c, 0, kBeginDevice, sumsq, max_norm, stream);
+}
+
+int zero_adamw_state(const zero_ctx *c, void **master, void **m, void **v, void **scale) {
+    int rc = need_adamw(c);
+    if (rc) return rc;
+    const bool q8 = c->state_bits == 8;
+    if (master) *master = c->master;
+    if (m) *m = q8 ? (void *)c->m8 : (void *)c->m;
+    if (v) *v = q8 ? (void *)c->r8 : (void *)c->v;
+    if (scale) *scale = q8 ? (void *)c->scale : nullptr;
+    return ZERO_OK;
 }
 
 void zero_destroy(zero_ctx *c) {
@@ -1042,6 +1472,7 @@ void zero_destroy(zero_ctx *c) {
     (void)hipDeviceSynchronize();
     if (c->state) (void)hipFree(c->state);
     if (c->sched_mem) (void)hipFree(c->sched_mem);
+    if (c->aw_mem) (void)hipFree(c->aw_mem);
     {
         std::lock_guard<std::mutex> lk(g_scratch_mu);
         if (c->device >= 0 && c->device < kMaxDevices && g_scratch_owner[c->device] == c)

@@ -116,4 +116,84 @@ hipError_t launch_load_master(const void *flat, bool flat_bf16, float *master,
                               float *m, float *v, int64_t shard,
                               hipStream_t stream);
 
+// ---- AdamW over many tensors (adamw_kernels.hip)
+// The state is cut into pieces of kAdamwPiece elements; every tensor's local
+// elements start on one and the elements behind its last are zero. A device
+// table holds one entry per tensor, and a map the tensor of every piece, so
+// one launch covers a list of any length.
+constexpr int kAdamwPiece = 2048;
+// Elements that share one scale in the 8-bit states.
+constexpr int kAdamwBlock = 32;
+constexpr int kAdamwScales = kAdamwPiece / kAdamwBlock;   // per piece and moment
+constexpr int kAdamwMaxReplicas = kFsdpMaxWorld;
+// A dispatch holds at most 2^32-1 work-items, 256 of them for a piece.
+constexpr int64_t kAdamwMaxPieces = 0xFFFFFFFFll / 256;
+
+struct AdamwTensor {
+    const void *grads[kAdamwMaxReplicas];   // replica q's gradient at this rank's first element
+    void *out;                              // this rank's output elements
+    int64_t numel;                          // local elements
+    int64_t piece0;                         // first piece in the state
+    float decay;                            // decoupled weight decay
+    float factor;                           // of the learning rate
+};
+
+// The state, either kind. 8 bits: codes m8 and r8 (r = sqrt(v)) and, per
+// piece, kAdamwScales scales of m followed by as many of r.
+struct AdamwStateRef {
+    float *master, *m, *v;
+    uint8_t *m8, *r8, *scale;
+};
+
+struct AdamwArgs {
+    const AdamwTensor *table;
+    const int32_t *map;           // piece -> tensor
+    int64_t npieces;
+    int n;
+    bool grad_bf16, out_bf16, q8;
+    AdamwStateRef st;
+    StepScalars sc;
+    const StepScalars *sc_dev;    // as in StepArgs
+    const DevSchedule *ds;        // with sc_dev: the step begun is ds->t - 1
+    uint32_t seed;                // mixed seed of the stochastic rounding
+    uint32_t t;                   // step, without sc_dev
+    const double *sumsq;          // clip by its root, or null
+    double max_norm;
+    bool stream_state;            // as in StepArgs
+};
+hipError_t launch_adamw(const AdamwArgs &a, hipStream_t stream);
+
+// Workgroups of the sum of squares, each with one partial sum.
+constexpr int kSumsqGroups = 2048;
+struct SumsqArgs {
+    const AdamwTensor *table;
+    const int32_t *map;
+    int64_t npieces;
+    int n;
+    bool grad_bf16;
+    double *partial;              // kSumsqGroups
+    uint32_t *done;               // workgroups done, 0 between launches
+    double *out;
+};
+hipError_t launch_sumsq(const SumsqArgs &a, hipStream_t stream);
+
+// 8-bit states to and from fp32 m and v, over whole pieces. A null m or v is
+// left out.
+hipError_t launch_adamw_decode(const AdamwStateRef &st, int64_t npieces, float *m, float *v,
+                               hipStream_t stream);
+hipError_t launch_adamw_encode(const AdamwStateRef &st, int64_t npieces, const float *m,
+                               const float *v, hipStream_t stream);
+// The 8-bit states of m = v = 0: every code 0, every scale the smallest.
+hipError_t launch_adamw_clear(const AdamwStateRef &st, int64_t npieces, hipStream_t stream);
+// master[i] = fp32(src[i]) for i < n.
+hipError_t launch_widen(const void *src, bool src_bf16, float *master, int64_t n,
+                        hipStream_t stream);
+// The mixing step of the rounding's counter hash (host and device).
+__host__ __device__ inline uint32_t adamw_mix(uint32_t x) {
+    x *= 0x9E3B5A35u;
+    x ^= x >> 15;
+    x *= 0x5D2C9E1Bu;
+    return x ^ (x >> 16);
+}
+
 }  // namespace zk
