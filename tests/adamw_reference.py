@@ -78,13 +78,17 @@ def step32(p, m, v, g, dg, sc, factor, decay):
 
 
 def step8(p, m, r, g, dg, sc, factor, decay):
-    """(p, m, r) before coding, and their bounds. r*r rounds once. The step:
-    lr_k (2), bc1, quotient, product; root, bc2 through the root (1/2), its
-    root, its reciprocal, product, eps, sum, quotient: 12.5 U."""
+    """(p, m, r) before coding, and their bounds. r*r rounds once. The root is
+    a Newton step from the hardware's: at most one ulp, 2 U, off. The step
+    (lr_k/bc1) * (m / (r/sqrt(bc2) + eps)): lr_k (2), bc1 and their quotient;
+    r's root (2), 1/sqrt(bc2) as bc2 through the root (1/2), root and
+    reciprocal, the sum in one fma, the hardware's reciprocal of it (one ulp,
+    2), the product: 12.5 U. The last product is inside the fma that _update
+    counts."""
     mn, dm, vn, dv = moments(g, dg, m, r * r, sc)
     dv = dv + U * sc["b2"] * r * r
     rn = np.sqrt(vn)
-    dr = SAFE * (0.5 * rn * _ratio(dv, vn) + U * rn)
+    dr = SAFE * (0.5 * rn * _ratio(dv, vn) + 2 * U * rn)
     den = rn / np.sqrt(sc["bc2"]) + sc["eps"]
     lr = sc["lr"] * factor
     u = _ratio(lr * mn / sc["bc1"], den)

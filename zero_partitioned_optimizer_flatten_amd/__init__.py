@@ -114,6 +114,17 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
     return ctypes.c_void_p(s.cuda_stream)
 
 
+# torch's own lookup of a device's current stream handle: 0.1 us, where building
+# the stream object costs 1.7 us of a 5.6 us step call.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_stream_handle(device: torch.device) -> int:
+    if _raw_stream is not None:
+        return _raw_stream(device.index)
+    return torch.cuda.current_stream(device).cuda_stream
+
+
 def _ptr_array(ptrs: Sequence[int]):
     arr = (ctypes.c_void_p * max(1, len(ptrs)))()
     for i, p in enumerate(ptrs):
@@ -582,10 +593,11 @@ class AdamWState(FsdpShardState):
     def _stream(self, stream):
         """The given stream, or this device's current one (whatever device is
         current in the caller)."""
-        s = torch.cuda.current_stream(self.device) if stream is None else stream
-        if s.device != self.device:
-            raise ValueError(f"stream is on {s.device}, state is on {self.device}")
-        return ctypes.c_void_p(s.cuda_stream)
+        if stream is None:
+            return _current_stream_handle(self.device)
+        if stream.device != self.device:
+            raise ValueError(f"stream is on {stream.device}, state is on {self.device}")
+        return stream.cuda_stream
 
     def set_groups(self, weight_decay=0.0, lr_scale=1.0, stream=None):
         """Weight decay and learning-rate scale of later steps: a number for

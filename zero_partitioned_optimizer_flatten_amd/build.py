@@ -37,10 +37,11 @@ def build(verbose: bool = False) -> str:
 def asm(out_dir: str) -> None:
     """Write the gfx950 assembly of the kernels (for inspection)."""
     os.makedirs(out_dir, exist_ok=True)
-    src = os.path.join(CSRC, "zero_kernels.hip")
     flags = [f for f in FLAGS if f not in ("-shared", "-fPIC")]
-    subprocess.check_call([HIPCC, *flags, "--cuda-device-only", "-S", src,
-                           "-o", os.path.join(out_dir, "zero_kernels.s")])
+    for name in ("zero_kernels", "adamw_kernels"):
+        subprocess.check_call([HIPCC, *flags, "--cuda-device-only", "-S",
+                               os.path.join(CSRC, name + ".hip"),
+                               "-o", os.path.join(out_dir, name + ".s")])
 
 
 if __name__ == "__main__":

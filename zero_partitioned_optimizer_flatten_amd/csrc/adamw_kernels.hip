@@ -11,7 +11,7 @@
 //   8-bit states: m and r = sqrt(v) are held as e4m3 codes, 32 elements to a
 //   power-of-two scale
 //     m = fma(g, 1-b1, m*b1);  v = fma((1-b2)*g, g, (r*r)*b2);  r = sqrt(v)
-//     p = p * keep_k - ((lr_k / bc1) * m) / (r * (1/sqrt(bc2)) + eps)
+//     p = p * keep_k - (lr_k / bc1) * (m / (r * (1/sqrt(bc2)) + eps))
 // with bc = 1 - b^t. The 32-bit step without decay and clipping is bit for
 // bit the per-parameter step of zero_kernels.hip.
 //
@@ -27,18 +27,60 @@ namespace {
 
 constexpr int kWave = 64;
 constexpr int kQuad = 4;                         // elements per lane and load
-constexpr int kWaveElems = 8 * kWave;            // a wave's part of a piece
+constexpr int kSplit = 2;                        // quads of a lane
+constexpr int kWaveElems = kSplit * kQuad * kWave;   // a wave's part of a piece
 constexpr int kPieceWaves = kAdamwPiece / kWaveElems;
+
+// Dynamic LDS that a workgroup reserves and does not touch, to set how many
+// share a compute unit (160 KiB each).
+// 32-bit states, one-wave workgroups, 10 per unit: 3.91-3.97 ms on the
+// Llama-7B list (rank of 8, reduced fp32 gradients) against 4.04 at 13, 3.94-
+// 3.97 at 8 and 4.34 at 6; GPT-2 small whole 538 us against 555, 543 and 607.
+#ifndef ZA_LDS32
+#define ZA_LDS32 16384
+#endif
+// 8-bit states, one piece per workgroup (so that each 128-byte line of scales
+// is one workgroup's), 4 per unit: 2.14-2.15 ms on the same list in four runs
+// against 2.15-2.33 at 6 and 2.14-2.28 uncapped; one- and two-wave workgroups
+// 2.11-2.39.
+#ifndef ZA_LDS8
+#define ZA_LDS8 40960
+#endif
+// Cache policies of buffer instructions (gfx950: nt = 2, sc1 = 16). Loads and
+// stores stream (nt): what a step touches does not outlive the forward and
+// backward pass that follows it in the Infinity Cache. Default-policy stores
+// ran at 4.60 ms where nt ones took 4.05 (32 bits, Llama-7B) and 2.58 where
+// these took 2.38 (8 bits).
+constexpr int kPolDefault = 0, kPolNT = 2;
+// 32-bit states larger than the 256 MB Infinity Cache store at device scope as
+// well (nt sc1): 3.92-3.95 ms against 3.96-4.05 (Llama-7B), 547 us against 560
+// (GPT-2 small whole); smaller ones do not: 116 us against 110 (GPT-2 small,
+// rank 3 of 8, three states in turn).
+constexpr int kPolDevice = 18;
+
+template <int V> struct Const { static constexpr int value = V; };
+
+typedef unsigned int u32x4_t __attribute__((ext_vector_type(4)));
+typedef unsigned int u32x2_t __attribute__((ext_vector_type(2)));
+typedef float f32x2_t __attribute__((ext_vector_type(2)));
+typedef __amdgpu_buffer_rsrc_t span_t;
+
+// A descriptor over `nbytes` at a wave-uniform address, for instructions
+// that take a lane's byte offset into it and a cache policy.
+__device__ __forceinline__ span_t span_of(const void *base, int nbytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, nbytes,
+                                             0x00020000);
+}
 
 __device__ __forceinline__ float widen_bf16(uint32_t bits16) {
     return __uint_as_float(bits16 << 16);
 }
 
-// binary32 -> bf16 bits, round to nearest, ties to even; NaN stays NaN.
-__device__ __forceinline__ uint32_t round_bf16(float x) {
-    uint32_t u = __float_as_uint(x);
-    uint32_t r = (u + 0x7FFFu + ((u >> 16) & 1u)) >> 16;
-    return ((u & 0x7FFFFFFFu) > 0x7F800000u) ? ((u >> 16) | 0x40u) : r;
+// Two values to bf16, nearest, ties to even, NaN kept (one instruction).
+__device__ __forceinline__ uint32_t round_bf16x2(float lo, float hi) {
+    typedef __bf16 bf16x2_t __attribute__((ext_vector_type(2)));
+    const f32x2_t x = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t));
 }
 
 template <bool B>
@@ -47,24 +89,87 @@ __device__ __forceinline__ float elem(const void *base, int64_t i) {
              : static_cast<const float *>(base)[i];
 }
 
-// Elements [i, i + 4) of a gradient at its own alignment; `left` of them
-// exist, the others are zero.
+// Four elements as loaded: 8 bytes of bf16 or 16 of fp32.
+template <bool B> struct RawQuad;
+template <> struct RawQuad<true> { u32x2_t w; };
+template <> struct RawQuad<false> { u32x4_t w; };
+
+__device__ __forceinline__ void widen(const RawQuad<true> &r, float (&x)[kQuad]) {
+    x[0] = widen_bf16(r.w.x & 0xFFFFu);
+    x[1] = __uint_as_float(r.w.x & 0xFFFF0000u);
+    x[2] = widen_bf16(r.w.y & 0xFFFFu);
+    x[3] = __uint_as_float(r.w.y & 0xFFFF0000u);
+}
+__device__ __forceinline__ void widen(const RawQuad<false> &r, float (&x)[kQuad]) {
+    x[0] = __uint_as_float(r.w.x);
+    x[1] = __uint_as_float(r.w.y);
+    x[2] = __uint_as_float(r.w.z);
+    x[3] = __uint_as_float(r.w.w);
+}
+
+template <bool B>
+__device__ __forceinline__ RawQuad<B> narrow(const float (&x)[kQuad]) {
+    RawQuad<B> r;
+    if constexpr (B) {
+        r.w.x = round_bf16x2(x[0], x[1]);
+        r.w.y = round_bf16x2(x[2], x[3]);
+    } else {
+        r.w = {__float_as_uint(x[0]), __float_as_uint(x[1]), __float_as_uint(x[2]),
+               __float_as_uint(x[3])};
+    }
+    return r;
+}
+
+// A whole quad `off` elements into a wave's part of a caller's buffer, which
+// starts at `base`. AL: the part is aligned for the instruction's width, and
+// goes through a buffer instruction with its policy; otherwise through a
+// load or store at the element's own alignment.
+template <bool B, bool AL, int POL>
+__device__ __forceinline__ RawQuad<B> load_raw(const char *base, int off) {
+    constexpr int es = B ? 2 : 4;
+    RawQuad<B> r;
+    if constexpr (AL) {
+        const span_t sp = span_of(base, kAdamwPiece * es);
+        if constexpr (B) r.w = __builtin_amdgcn_raw_buffer_load_b64(sp, off * es, 0, POL);
+        else r.w = __builtin_amdgcn_raw_buffer_load_b128(sp, off * es, 0, POL);
+    } else {
+        __builtin_memcpy(&r, base + off * es, sizeof r);
+    }
+    return r;
+}
+
+template <bool B, bool AL, int POL>
+__device__ __forceinline__ void store_raw(char *base, int off, const RawQuad<B> &r) {
+    constexpr int es = B ? 2 : 4;
+    if constexpr (AL) {
+        const span_t sp = span_of(base, kWaveElems * es);
+        if constexpr (B) __builtin_amdgcn_raw_buffer_store_b64(r.w, sp, off * es, 0, POL);
+        else __builtin_amdgcn_raw_buffer_store_b128(r.w, sp, off * es, 0, POL);
+    } else {
+        __builtin_memcpy(base + off * es, &r, sizeof r);
+    }
+}
+
+template <int POL>
+__device__ __forceinline__ void load_f4(span_t sp, int off, float (&x)[kQuad]) {
+    RawQuad<false> r;
+    r.w = __builtin_amdgcn_raw_buffer_load_b128(sp, off * 4, 0, POL);
+    widen(r, x);
+}
+template <int POL>
+__device__ __forceinline__ void store_f4(span_t sp, int off, const float (&x)[kQuad]) {
+    __builtin_amdgcn_raw_buffer_store_b128(narrow<false>(x).w, sp, off * 4, 0, POL);
+}
+
+// The same at a tensor's end: `left` elements of the quad exist, the others
+// read as zero and are not written.
 template <bool B>
 __device__ __forceinline__ void load_quad(const void *base, int64_t i, int64_t left,
                                           float (&x)[kQuad]) {
     if (left >= kQuad) {
-        if constexpr (B) {
-            uint2 w;
-            __builtin_memcpy(&w, static_cast<const uint16_t *>(base) + i, sizeof w);
-            x[0] = widen_bf16(w.x & 0xFFFFu);
-            x[1] = widen_bf16(w.x >> 16);
-            x[2] = widen_bf16(w.y & 0xFFFFu);
-            x[3] = widen_bf16(w.y >> 16);
-        } else {
-            float4 w;
-            __builtin_memcpy(&w, static_cast<const float *>(base) + i, sizeof w);
-            x[0] = w.x; x[1] = w.y; x[2] = w.z; x[3] = w.w;
-        }
+        RawQuad<B> r;
+        __builtin_memcpy(&r, static_cast<const char *>(base) + i * (B ? 2 : 4), sizeof r);
+        widen(r, x);
     } else {
 #pragma unroll
         for (int e = 0; e < kQuad; ++e) x[e] = e < left ? elem<B>(base, i + e) : 0.0f;
@@ -75,28 +180,34 @@ template <bool B>
 __device__ __forceinline__ void store_quad(void *base, int64_t i, int64_t left,
                                            const float (&x)[kQuad]) {
     if (left >= kQuad) {
-        if constexpr (B) {
-            const uint2 w = make_uint2(round_bf16(x[0]) | (round_bf16(x[1]) << 16),
-                                       round_bf16(x[2]) | (round_bf16(x[3]) << 16));
-            __builtin_memcpy(static_cast<uint16_t *>(base) + i, &w, sizeof w);
-        } else {
-            const float4 w = make_float4(x[0], x[1], x[2], x[3]);
-            __builtin_memcpy(static_cast<float *>(base) + i, &w, sizeof w);
-        }
+        const RawQuad<B> r = narrow<B>(x);
+        __builtin_memcpy(static_cast<char *>(base) + i * (B ? 2 : 4), &r, sizeof r);
     } else {
 #pragma unroll
         for (int e = 0; e < kQuad; ++e) {
             if (e < left) {
-                if (B) static_cast<uint16_t *>(base)[i + e] = (uint16_t)round_bf16(x[e]);
+                if (B) static_cast<uint16_t *>(base)[i + e] = (uint16_t)round_bf16x2(x[e], 0.0f);
                 else static_cast<float *>(base)[i + e] = x[e];
             }
         }
     }
 }
 
+// What a launch only reads, at addresses that are uniform over a wave, goes
+// through the constant address space: scalar loads, and values that the
+// compiler knows to be uniform (a descriptor over a pointer it does not know
+// to be uniform costs a loop around every access).
+#define ZK_CONSTANT __attribute__((address_space(4)))
+typedef const ZK_CONSTANT AdamwTensor Tensor;
+
+template <class T>
+__device__ __forceinline__ const ZK_CONSTANT T *constant(const T *p) {
+    return (const ZK_CONSTANT T *)(uintptr_t)p;
+}
+
 struct KernelArgs {
-    const AdamwTensor *__restrict__ table;
-    const int32_t *__restrict__ map;
+    const AdamwTensor *table;
+    const int32_t *map;
     int n;
     AdamwStateRef st;
     StepScalars sc;
@@ -105,6 +216,7 @@ struct KernelArgs {
     uint32_t seed, t;
     const double *sumsq;
     double max_norm;
+    int stream_state;
 };
 
 // The clip factor; false where the sum of squares is not finite, and then
@@ -112,78 +224,227 @@ struct KernelArgs {
 __device__ __forceinline__ bool clip_factor(const double *sumsq, double max_norm, float &c) {
     c = 1.0f;
     if (!sumsq) return true;
-    const double s = *sumsq;
+    const double s = *constant(sumsq);
     if (!(s >= 0.0 && s < __builtin_inf())) return false;
     const double f = max_norm / (__builtin_sqrt(s) + 1e-6);
     if (f < 1.0) c = (float)f;
     return true;
 }
 
-// Mean gradient of a lane's quad, clipped.
-template <int NR, bool GB>
-__device__ __forceinline__ void mean_quad(const AdamwTensor &tn, const KernelArgs &a, float clip,
-                                          int64_t i, int64_t left, float (&g)[kQuad]) {
-    const int n = NR > 0 ? NR : a.n;
-    const bool pow2 = NR > 0 ? (NR & (NR - 1)) == 0 : a.sc.n_pow2 != 0;
-    load_quad<GB>(tn.grads[0], i, left, g);
+// What a wave needs beside its data: uniform over the wave. The scalars that
+// depend on the replica count are the binding's, also where the schedule's
+// come from the device.
+struct Uniform {
+    StepScalars sc;
+    bool pow2;
+    float scale;          // of the sum over the replicas: clip factor, and 1/N where exact
+    float lr, keep;
+};
+
+template <int NR>
+__device__ __forceinline__ bool uniforms(const KernelArgs &a, Tensor &tn, Uniform &u) {
+    float clip;
+    if (!clip_factor(a.sumsq, a.max_norm, clip)) return false;
+    u.sc = a.sc;
+    if (a.sc_dev) {
+        const ZK_CONSTANT StepScalars &d = *constant(a.sc_dev);
+        u.sc.b1 = d.b1; u.sc.c1 = d.c1; u.sc.b2 = d.b2; u.sc.c2 = d.c2;
+        u.sc.lr = d.lr; u.sc.eps = d.eps; u.sc.bc1 = d.bc1; u.sc.bc2 = d.bc2;
+    }
+    u.pow2 = NR > 0 ? (NR & (NR - 1)) == 0 : a.sc.n_pow2 != 0;
+    u.scale = u.pow2 ? a.sc.inv_n * clip : clip;      // a power of two: the same bits
+    u.lr = u.sc.lr * tn.factor;
+    u.keep = 1.0f - u.lr * tn.decay;
+    return true;
+}
+
+__device__ __forceinline__ void mean_clip(const Uniform &u, float (&g)[kQuad]) {
+    if (!u.pow2) {
 #pragma unroll
+        for (int e = 0; e < kQuad; ++e) g[e] = g[e] / u.sc.nf;
+    }
+#pragma unroll
+    for (int e = 0; e < kQuad; ++e) g[e] = g[e] * u.scale;
+}
+
+// Mean gradient of a quad at a tensor's end.
+template <int NR, bool GB>
+__device__ __forceinline__ void mean_quad(Tensor &tn, int nrep, const Uniform &u,
+                                          int64_t i, int64_t left, float (&g)[kQuad]) {
+    const int n = NR > 0 ? NR : nrep;
+    load_quad<GB>(tn.grads[0], i, left, g);
+#pragma unroll 1
     for (int q = 1; q < n; ++q) {
         float x[kQuad];
         load_quad<GB>(tn.grads[q], i, left, x);
 #pragma unroll
         for (int e = 0; e < kQuad; ++e) g[e] = g[e] + x[e];
     }
+    mean_clip(u, g);
+}
+
+// Replicas' loads that are in flight together.
+constexpr int kGroup = 8;
+
+// Mean gradients of a lane's quads in a full part (element i0 of the tensor
+// onwards). `first` runs once the first group's loads are on their way.
+template <int NR, bool GB, bool AL, class F>
+__device__ __forceinline__ void mean_full(Tensor &tn, int nrep, const Uniform &u,
+                                          int64_t i0, int lane, float (&g)[kSplit][kQuad],
+                                          F &&first) {
+    const int n = NR > 0 ? NR : nrep;
+    constexpr int es = GB ? 2 : 4;
+    constexpr int grp = NR > 0 && NR < kGroup ? NR : kGroup;
+#pragma unroll 1
+    for (int q0 = 0; q0 < n; q0 += grp) {
+        RawQuad<GB> raw[grp][kSplit];
 #pragma unroll
-    for (int e = 0; e < kQuad; ++e) {
-        // the replica count is the binding's, also where the schedule's
-        // scalars come from the device
-        g[e] = pow2 ? g[e] * a.sc.inv_n : g[e] / a.sc.nf;
-        g[e] = g[e] * clip;
+        for (int k = 0; k < grp; ++k)
+            if (NR > 0 || q0 + k < n) {
+                const char *base = static_cast<const char *>(tn.grads[q0 + k]) + i0 * es;
+#pragma unroll
+                for (int h = 0; h < kSplit; ++h)
+                    raw[k][h] = load_raw<GB, AL, AL ? kPolNT : kPolDefault>(
+                        base, kQuad * (lane + h * kWave));
+            }
+        if (q0 == 0) first();
+#pragma unroll
+        for (int k = 0; k < grp; ++k)
+            if (NR > 0 || q0 + k < n) {
+#pragma unroll
+                for (int h = 0; h < kSplit; ++h) {
+                    float x[kQuad];
+                    widen(raw[k][h], x);
+#pragma unroll
+                    for (int e = 0; e < kQuad; ++e)
+                        g[h][e] = q0 + k == 0 ? x[e] : g[h][e] + x[e];
+                }
+            }
     }
+#pragma unroll
+    for (int h = 0; h < kSplit; ++h) mean_clip(u, g[h]);
+}
+
+// Whether every stream of a part is aligned for whole-quad instructions.
+template <bool GB>
+__device__ __forceinline__ bool aligned_grads(Tensor &tn, int n) {
+    uintptr_t bits = 0;
+    for (int q = 0; q < n; ++q) bits |= (uintptr_t)tn.grads[q] % (GB ? 8 : 16);
+    return bits == 0;
+}
+
+// Elements before the first at which every replica's quads are aligned, -1
+// where the replicas do not share a phase.
+template <bool GB>
+__device__ __forceinline__ int common_head(Tensor &tn, int n) {
+    constexpr uintptr_t es = GB ? 2 : 4;
+    const int phase = (int)((uintptr_t)tn.grads[0] / es % kQuad);
+    for (int q = 1; q < n; ++q)
+        if ((int)((uintptr_t)tn.grads[q] / es % kQuad) != phase) return -1;
+    return (kQuad - phase) % kQuad;
+}
+
+template <bool GB, bool PB>
+__device__ __forceinline__ bool aligned_part(Tensor &tn, int n) {
+    return (uintptr_t)tn.out % (PB ? 8 : 16) == 0 && aligned_grads<GB>(tn, n);
 }
 
 // ------------------------------------------------------------ 32-bit states
+// The moments (m, v updated in place) and the step they give.
+__device__ __forceinline__ float moments32(float g, float &m, float &v, const Uniform &u) {
+    m = __builtin_fmaf(g, u.sc.c1, m * u.sc.b1);
+    v = __builtin_fmaf(u.sc.c2 * g, g, v * u.sc.b2);
+    return (u.lr * (m / u.sc.bc1)) / (__builtin_sqrtf(v / u.sc.bc2) + u.sc.eps);
+}
+
+template <int NR, bool GB, bool PB, bool AL>
+__device__ __forceinline__ void full32(const KernelArgs &a, Tensor &tn,
+                                       const Uniform &u, int64_t i0, int64_t s0, int lane) {
+    const span_t sp = span_of(a.st.master + s0, kWaveElems * 4);
+    const span_t sm = span_of(a.st.m + s0, kWaveElems * 4);
+    const span_t sv = span_of(a.st.v + s0, kWaveElems * 4);
+    float g[kSplit][kQuad], p[kSplit][kQuad], m[kSplit][kQuad], v[kSplit][kQuad];
+    mean_full<NR, GB, AL>(tn, a.n, u, i0, lane, g, [&] {
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h) {
+            const int off = kQuad * (lane + h * kWave);
+            load_f4<kPolNT>(sm, off, m[h]);
+            load_f4<kPolNT>(sv, off, v[h]);
+            load_f4<kPolNT>(sp, off, p[h]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    });
+    float d[kSplit][kQuad];
+#pragma unroll
+    for (int h = 0; h < kSplit; ++h)
+#pragma unroll
+        for (int e = 0; e < kQuad; ++e) d[h][e] = moments32(g[h][e], m[h][e], v[h][e], u);
+    char *out = static_cast<char *>(tn.out) + i0 * (PB ? 2 : 4);
+#pragma unroll
+    for (int h = 0; h < kSplit; ++h)
+#pragma unroll
+        for (int e = 0; e < kQuad; ++e) p[h][e] = p[h][e] * u.keep - d[h][e];
+    const auto store = [&](auto pol) {
+        constexpr int P = decltype(pol)::value;
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h) store_f4<P>(sp, kQuad * (lane + h * kWave), p[h]);
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h) store_f4<P>(sm, kQuad * (lane + h * kWave), m[h]);
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h) store_f4<P>(sv, kQuad * (lane + h * kWave), v[h]);
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h)
+            store_raw<PB, AL, P>(out, kQuad * (lane + h * kWave), narrow<PB>(p[h]));
+    };
+    if (a.stream_state) store(Const<kPolDevice>());
+    else store(Const<kPolNT>());
+}
+
+// The part a tensor ends in.
+template <int NR, bool GB, bool PB>
+__device__ __forceinline__ void last32(const KernelArgs &a, Tensor &tn,
+                                       const Uniform &u, int64_t i0, int64_t s0, int lane) {
+#pragma unroll 1
+    for (int h = 0; h < kSplit; ++h) {
+        const int off = kQuad * (lane + h * kWave);
+        const int64_t left = tn.numel - (i0 + off);
+        if (left <= 0) break;
+        float g[kQuad];
+        mean_quad<NR, GB>(tn, a.n, u, i0 + off, left, g);
+        float *pp = a.st.master + s0 + off, *pm = a.st.m + s0 + off, *pv = a.st.v + s0 + off;
+        float p[kQuad];
+#pragma unroll
+        for (int e = 0; e < kQuad; ++e) {
+            p[e] = 0.0f;
+            if (e < left) {
+                float m = pm[e], v = pv[e];
+                const float d = moments32(g[e], m, v, u);
+                p[e] = pp[e] * u.keep - d;
+                pp[e] = p[e];
+                pm[e] = m;
+                pv[e] = v;
+            }
+        }
+        store_quad<PB>(tn.out, i0 + off, left, p);
+    }
+}
+
 template <int NR, bool GB, bool PB>
 __global__ void __launch_bounds__(kWave) adamw32_kernel(KernelArgs a) {
     const int64_t piece = blockIdx.x / kPieceWaves;
-    const AdamwTensor &tn = a.table[a.map[piece]];
-    const int64_t numel = tn.numel;
+    Tensor &tn = constant(a.table)[constant(a.map)[piece]];
     const int64_t i0 = (piece - tn.piece0) * kAdamwPiece + (blockIdx.x % kPieceWaves) * kWaveElems;
-    if (i0 >= numel) return;
-    float clip;
-    if (!clip_factor(a.sumsq, a.max_norm, clip)) return;
-    const StepScalars sc = a.sc_dev ? *a.sc_dev : a.sc;
-    const float lr = sc.lr * tn.factor;
-    const float keep = 1.0f - lr * tn.decay;
+    if (i0 >= tn.numel) return;
+    Uniform u;
+    if (!uniforms<NR>(a, tn, u)) return;
     const int64_t s0 = (int64_t)blockIdx.x * kWaveElems;
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int off = kQuad * (threadIdx.x + h * kWave);
-        const int64_t left = numel - (i0 + off);
-        if (left <= 0) continue;
-        float g[kQuad];
-        mean_quad<NR, GB>(tn, a, clip, i0 + off, left, g);
-        float4 *pp = reinterpret_cast<float4 *>(a.st.master + s0 + off);
-        float4 *pm = reinterpret_cast<float4 *>(a.st.m + s0 + off);
-        float4 *pv = reinterpret_cast<float4 *>(a.st.v + s0 + off);
-        const float4 p4 = *pp, m4 = *pm, v4 = *pv;
-        float p[kQuad] = {p4.x, p4.y, p4.z, p4.w};
-        float m[kQuad] = {m4.x, m4.y, m4.z, m4.w};
-        float v[kQuad] = {v4.x, v4.y, v4.z, v4.w};
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-            const float mm = __builtin_fmaf(g[e], sc.c1, m[e] * sc.b1);
-            const float vv = __builtin_fmaf(sc.c2 * g[e], g[e], v[e] * sc.b2);
-            const float u = (lr * (mm / sc.bc1)) / (__builtin_sqrtf(vv / sc.bc2) + sc.eps);
-            const bool in = e < left;
-            p[e] = in ? p[e] * keep - u : 0.0f;
-            m[e] = in ? mm : 0.0f;
-            v[e] = in ? vv : 0.0f;
-        }
-        *pp = make_float4(p[0], p[1], p[2], p[3]);
-        *pm = make_float4(m[0], m[1], m[2], m[3]);
-        *pv = make_float4(v[0], v[1], v[2], v[3]);
-        store_quad<PB>(tn.out, i0 + off, left, p);
+    const int lane = threadIdx.x;
+    if (i0 + kWaveElems > tn.numel) {
+        last32<NR, GB, PB>(a, tn, u, i0, s0, lane);
+    } else if (aligned_part<GB, PB>(tn, NR > 0 ? NR : a.n)) {
+        full32<NR, GB, PB, true>(a, tn, u, i0, s0, lane);
+    } else {
+        full32<NR, GB, PB, false>(a, tn, u, i0, s0, lane);
     }
 }
 
@@ -198,23 +459,30 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
 __device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
 __device__ __forceinline__ float scale_inv(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 
-// Largest over the 8 lanes that hold a block.
-__device__ __forceinline__ uint32_t block_max(uint32_t x) {
-    uint32_t y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0xB1, 0xF, 0xF, false);
-    x = x > y ? x : y;                                   // lanes 1 apart
-    y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x4E, 0xF, 0xF, false);
-    x = x > y ? x : y;                                   // 2 apart
-    y = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x141, 0xF, 0xF, false);
-    return x > y ? x : y;                                // the other four
+// Largest over the 8 lanes that hold a block (of values that are not negative).
+__device__ __forceinline__ float block_max(float x) {
+    const auto lane = [](float v, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value,
+                                                          0xF, 0xF, false));
+    };
+    x = __builtin_fmaxf(x, lane(x, Const<0xB1>()));            // 1 lane apart
+    x = __builtin_fmaxf(x, lane(x, Const<0x4E>()));            // 2 apart
+    return __builtin_fmaxf(x, lane(x, Const<0x141>()));        // the other four
 }
 
-constexpr uint32_t kInfBits = 0x7F800000u;
+__device__ __forceinline__ bool finite(float x) {
+    return (__float_as_uint(x) & 0x7FFFFFFFu) < 0x7F800000u;
+}
 
-// Magnitude bits for the block's maximum: what is not finite does not count,
-// so an infinity or NaN of one element leaves its neighbours' codes alone.
-__device__ __forceinline__ uint32_t top_bits(float x) {
-    const uint32_t u = __float_as_uint(x) & 0x7FFFFFFFu;
-    return u < kInfBits ? u : 0u;
+// Largest magnitude of a quad. SAFE: what is not finite does not count, so
+// an infinity or NaN of one element leaves its neighbours' codes alone.
+template <bool SAFE>
+__device__ __forceinline__ float quad_max(const float (&x)[kQuad]) {
+    float t = 0.0f;
+#pragma unroll
+    for (int e = 0; e < kQuad; ++e)
+        t = __builtin_fmaxf(t, SAFE && !finite(x[e]) ? 0.0f : __builtin_fabsf(x[e]));
+    return t;
 }
 
 __device__ __forceinline__ uint32_t pack4(const float (&y)[kQuad]) {
@@ -222,96 +490,205 @@ __device__ __forceinline__ uint32_t pack4(const float (&y)[kQuad]) {
     return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(y[2], y[3], w, true);
 }
 
-typedef float f32x2_t __attribute__((ext_vector_type(2)));
-
 __device__ __forceinline__ void unpack4(uint32_t w, float scale, float (&x)[kQuad]) {
     const f32x2_t a = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
     const f32x2_t b = __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true);
     x[0] = a.x * scale; x[1] = a.y * scale; x[2] = b.x * scale; x[3] = b.y * scale;
 }
 
-// A quad to codes. `noise` (16 bits per element, its bit 15 worth half a
-// step) carries into the third mantissa bit and what is below is cut, which
-// rounds without bias wherever e4m3 has three mantissa bits (2^-6 scales and
-// up); below, to nearest. ROOT: r > 0 stays at least the smallest code, so a
-// moment that is there never becomes none. Not finite: NaN.
-template <bool ROOT>
+// r > 0 stays at least the smallest code, so a second moment that is there
+// never becomes none: the median of y, that code and r times a large number,
+// which is 0 for r = 0 and above every code otherwise (r, a root of a
+// binary32, is at least 2^-75).
+__device__ __forceinline__ float at_least_a_code(float y, float r) {
+    return __builtin_amdgcn_fmed3f(y, 0x1p-9f, r * 0x1p120f);
+}
+
+// A quad to codes on the scale 1/inv. `noise` (16 bits per element, its bit 15
+// worth half a step) carries into the third mantissa bit and what is below is
+// cut, which rounds without bias wherever e4m3 has three mantissa bits (2^-6
+// scales and up); below, to nearest. SAFE: what is not finite becomes NaN;
+// without it every value is finite.
+template <bool ROOT, bool SAFE>
 __device__ __forceinline__ uint32_t encode4(const float (&x)[kQuad], const uint32_t (&noise)[kQuad],
                                             float inv) {
     float y[kQuad];
 #pragma unroll
     for (int e = 0; e < kQuad; ++e) {
-        const uint32_t u = __float_as_uint(x[e]);
-        y[e] = __uint_as_float((u + (noise[e] << 4)) & 0xFFF00000u) * inv;
-        if (ROOT) y[e] = x[e] > 0.0f ? __builtin_fmaxf(y[e], 0x1p-9f) : y[e];
-        if ((u & 0x7FFFFFFFu) >= kInfBits) y[e] = __builtin_nanf("");
+        y[e] = __uint_as_float((__float_as_uint(x[e]) + (noise[e] << 4)) & 0xFFF00000u) * inv;
+        if (ROOT) y[e] = at_least_a_code(y[e], x[e]);
+        if (SAFE && !finite(x[e])) y[e] = __builtin_nanf("");
     }
     return pack4(y);
+}
+
+struct Uniform8 : Uniform {
+    float lrc, rs;
+    uint32_t key;
+};
+
+// sqrt(v) from the hardware's reciprocal root (1 ulp) and one Newton step whose
+// residue is exact: correctly rounded but for about one v in 2^21, off by one
+// ulp there. A v below 2^-126 (gradients under 1e-18) gives less than its
+// root, an infinite one NaN.
+__device__ __forceinline__ float root(float v) {
+    const float y = __builtin_amdgcn_rsqf(__builtin_fmaxf(v, 0x1p-126f));
+    const float s = v * y;
+    return __builtin_fmaf(__builtin_fmaf(-s, s, v), 0.5f * y, s);
+}
+
+// Fresh moments of a quad from the old ones, and the step d they give. Only d
+// takes the hardware's reciprocal (1 ulp; its operand is 0 or at least
+// 2^-75): the codes do not depend on it.
+__device__ __forceinline__ void moments8(const float (&g)[kQuad], float (&m)[kQuad],
+                                         float (&r)[kQuad], float (&d)[kQuad], const Uniform8 &u) {
+#pragma unroll
+    for (int e = 0; e < kQuad; ++e) {
+        m[e] = __builtin_fmaf(g[e], u.sc.c1, m[e] * u.sc.b1);
+        r[e] = root(__builtin_fmaf(u.sc.c2 * g[e], g[e], (r[e] * r[e]) * u.sc.b2));
+        d[e] = m[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[e], u.rs, u.sc.eps));
+    }
+}
+
+// Codes and scales of the quad q (its place in the state / 4).
+template <bool SAFE>
+__device__ __forceinline__ void encode8(const float (&m)[kQuad], const float (&r)[kQuad],
+                                        const Uniform8 &u, int64_t q, uint32_t &cm, uint32_t &cr,
+                                        uint32_t &em, uint32_t &er) {
+    em = scale_byte(__float_as_uint(block_max(quad_max<SAFE>(m))));
+    er = scale_byte(__float_as_uint(block_max(quad_max<SAFE>(r))));
+    const uint32_t x = adamw_mix((uint32_t)q + (uint32_t)(q >> 32) * 0x7F4A7C15u + u.key);
+    const uint32_t w[kQuad] = {x, x * 0xB5297A4Du, x * 0x68E31DA5u, x * 0x1B56C4E9u};
+    uint32_t nm[kQuad], nr[kQuad];
+#pragma unroll
+    for (int e = 0; e < kQuad; ++e) {
+        nm[e] = w[e] >> 16;
+        nr[e] = w[e] & 0xFFFFu;
+    }
+    cm = encode4<false, SAFE>(m, nm, scale_inv(em));
+    cr = encode4<true, SAFE>(r, nr, scale_inv(er));
+}
+
+// Whether a step of the quad is NaN, as it is where a moment is not finite:
+// an infinite m or g comes with an infinite v, whose root is NaN.
+__device__ __forceinline__ bool nan_step(const float (&d)[kQuad]) {
+    return __builtin_isunordered(d[0], d[1]) || __builtin_isunordered(d[2], d[3]);
+}
+
+template <int NR, bool GB, bool PB, bool AL>
+__device__ __forceinline__ void full8(const KernelArgs &a, Tensor &tn,
+                                      const Uniform8 &u, int64_t i0, int64_t s0, uint8_t *scale,
+                                      int lane) {
+    const span_t sp = span_of(a.st.master + s0, kWaveElems * 4);
+    const span_t sm = span_of(a.st.m8 + s0, kWaveElems), sr = span_of(a.st.r8 + s0, kWaveElems);
+    float g[kSplit][kQuad], p[kSplit][kQuad], m[kSplit][kQuad], r[kSplit][kQuad];
+    uint32_t cm[kSplit], cr[kSplit], em[kSplit], er[kSplit];
+    mean_full<NR, GB, AL>(tn, a.n, u, i0, lane, g, [&] {
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h) {
+            const int off = kQuad * (lane + h * kWave);
+            cm[h] = __builtin_amdgcn_raw_buffer_load_b32(sm, off, 0, kPolNT);
+            cr[h] = __builtin_amdgcn_raw_buffer_load_b32(sr, off, 0, kPolNT);
+            em[h] = scale[off / kAdamwBlock];
+            er[h] = scale[kAdamwScales + off / kAdamwBlock];
+            load_f4<kPolNT>(sp, off, p[h]);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    });
+    float d[kSplit][kQuad];
+    bool bad = false;
+#pragma unroll
+    for (int h = 0; h < kSplit; ++h) {
+        unpack4(cm[h], scale_of(em[h]), m[h]);
+        unpack4(cr[h], scale_of(er[h]), r[h]);
+        moments8(g[h], m[h], r[h], d[h], u);
+        bad |= nan_step(d[h]);
+    }
+    const int64_t q = s0 / kQuad + lane;
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(bad) != 0, 0)) {
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h)
+            encode8<true>(m[h], r[h], u, q + h * kWave, cm[h], cr[h], em[h], er[h]);
+    } else {
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h)
+            encode8<false>(m[h], r[h], u, q + h * kWave, cm[h], cr[h], em[h], er[h]);
+    }
+    char *out = static_cast<char *>(tn.out) + i0 * (PB ? 2 : 4);
+#pragma unroll
+    for (int h = 0; h < kSplit; ++h) {
+        const int off = kQuad * (lane + h * kWave);
+#pragma unroll
+        for (int e = 0; e < kQuad; ++e)
+            p[h][e] = __builtin_fmaf(-u.lrc, d[h][e], p[h][e] * u.keep);
+        store_f4<kPolNT>(sp, off, p[h]);
+        store_raw<PB, AL, kPolNT>(out, off, narrow<PB>(p[h]));
+        __builtin_amdgcn_raw_buffer_store_b32(cm[h], sm, off, 0, kPolNT);
+        __builtin_amdgcn_raw_buffer_store_b32(cr[h], sr, off, 0, kPolNT);
+        if (lane % (kAdamwBlock / kQuad) == 0) {
+            scale[off / kAdamwBlock] = (uint8_t)em[h];
+            scale[kAdamwScales + off / kAdamwBlock] = (uint8_t)er[h];
+        }
+    }
+}
+
+// The part a tensor ends in: what is behind the last element reads as zero
+// and stays zero.
+template <int NR, bool GB, bool PB>
+__device__ __forceinline__ void last8(const KernelArgs &a, Tensor &tn,
+                                      const Uniform8 &u, int64_t i0, int64_t s0, uint8_t *scale,
+                                      int lane) {
+#pragma unroll 1
+    for (int h = 0; h < kSplit; ++h) {
+        const int off = kQuad * (lane + h * kWave);
+        const int64_t left = tn.numel - (i0 + off);
+        float g[kQuad] = {0.0f, 0.0f, 0.0f, 0.0f}, m[kQuad], r[kQuad], d[kQuad], p[kQuad];
+        if (left > 0) mean_quad<NR, GB>(tn, a.n, u, i0 + off, left, g);
+        uint32_t *pm = reinterpret_cast<uint32_t *>(a.st.m8 + s0 + off);
+        uint32_t *pr = reinterpret_cast<uint32_t *>(a.st.r8 + s0 + off);
+        float *pp = a.st.master + s0 + off;
+        uint8_t *sc = scale + off / kAdamwBlock;
+        unpack4(*pm, scale_of(sc[0]), m);
+        unpack4(*pr, scale_of(sc[kAdamwScales]), r);
+        uint32_t cm, cr, em, er;
+        moments8(g, m, r, d, u);
+        encode8<true>(m, r, u, (s0 + off) / kQuad, cm, cr, em, er);
+        *pm = cm;
+        *pr = cr;
+        if (lane % (kAdamwBlock / kQuad) == 0) {
+            sc[0] = (uint8_t)em;
+            sc[kAdamwScales] = (uint8_t)er;
+        }
+#pragma unroll
+        for (int e = 0; e < kQuad; ++e) {
+            p[e] = 0.0f;
+            if (e < left) pp[e] = p[e] = __builtin_fmaf(-u.lrc, d[e], pp[e] * u.keep);
+        }
+        if (left > 0) store_quad<PB>(tn.out, i0 + off, left, p);
+    }
 }
 
 template <int NR, bool GB, bool PB>
 __global__ void __launch_bounds__(kWave *kPieceWaves) adamw8_kernel(KernelArgs a) {
     const int64_t piece = blockIdx.x;
-    const AdamwTensor &tn = a.table[a.map[piece]];
-    const int64_t numel = tn.numel;
-    const int wave = threadIdx.x / kWave, lane = threadIdx.x % kWave;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const int lane = threadIdx.x % kWave;
+    Tensor &tn = constant(a.table)[constant(a.map)[piece]];
     const int64_t i0 = (piece - tn.piece0) * kAdamwPiece + wave * kWaveElems;
-    if (i0 >= numel) return;
-    float clip;
-    if (!clip_factor(a.sumsq, a.max_norm, clip)) return;
-    const StepScalars sc = a.sc_dev ? *a.sc_dev : a.sc;
-    const uint32_t key = adamw_mix(a.seed ^ (a.sc_dev ? (uint32_t)(a.ds->t - 1) : a.t));
-    const float lr = sc.lr * tn.factor;
-    const float keep = 1.0f - lr * tn.decay;
-    const float lrc = lr / sc.bc1;
-    const float rs = 1.0f / __builtin_sqrtf(sc.bc2);
+    if (i0 >= tn.numel) return;
+    Uniform8 u;
+    if (!uniforms<NR>(a, tn, u)) return;
+    u.key = adamw_mix(a.seed ^ (a.sc_dev ? (uint32_t)(constant(a.ds)->t - 1) : a.t));
+    u.lrc = u.lr / u.sc.bc1;
+    u.rs = 1.0f / __builtin_sqrtf(u.sc.bc2);
     const int64_t s0 = piece * kAdamwPiece + wave * kWaveElems;
     uint8_t *scale = a.st.scale + piece * (2 * kAdamwScales) + wave * (kWaveElems / kAdamwBlock);
-#pragma unroll
-    for (int h = 0; h < 2; ++h) {
-        const int off = kQuad * (lane + h * kWave);
-        const int blk = off / kAdamwBlock;
-        // elements past the last read as zero and stay zero
-        const int64_t left = numel - (i0 + off);
-        float g[kQuad] = {0.0f, 0.0f, 0.0f, 0.0f};
-        if (left > 0) mean_quad<NR, GB>(tn, a, clip, i0 + off, left, g);
-        uint32_t *cm = reinterpret_cast<uint32_t *>(a.st.m8 + s0 + off);
-        uint32_t *cr = reinterpret_cast<uint32_t *>(a.st.r8 + s0 + off);
-        float4 *pp = reinterpret_cast<float4 *>(a.st.master + s0 + off);
-        const float4 p4 = *pp;
-        float p[kQuad] = {p4.x, p4.y, p4.z, p4.w}, m[kQuad], r[kQuad];
-        unpack4(*cm, scale_of(scale[blk]), m);
-        unpack4(*cr, scale_of(scale[kAdamwScales + blk]), r);
-        uint32_t tm = 0, tr = 0;
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-            m[e] = __builtin_fmaf(g[e], sc.c1, m[e] * sc.b1);
-            const float v = __builtin_fmaf(sc.c2 * g[e], g[e], (r[e] * r[e]) * sc.b2);
-            r[e] = __builtin_sqrtf(v);
-            p[e] = p[e] * keep - (lrc * m[e]) / (r[e] * rs + sc.eps);
-            if (e >= left) p[e] = 0.0f;                 // 0/0 where eps is 0
-            const uint32_t bm = top_bits(m[e]), br = top_bits(r[e]);
-            tm = tm > bm ? tm : bm;
-            tr = tr > br ? tr : br;
-        }
-        const uint32_t em = scale_byte(block_max(tm)), er = scale_byte(block_max(tr));
-        const int64_t q = (s0 + off) / kQuad;
-        const uint32_t x = adamw_mix((uint32_t)q + (uint32_t)(q >> 32) * 0x7F4A7C15u + key);
-        const uint32_t w[kQuad] = {x, x * 0xB5297A4Du, x * 0x68E31DA5u, x * 0x1B56C4E9u};
-        uint32_t nm[kQuad], nr[kQuad];
-#pragma unroll
-        for (int e = 0; e < kQuad; ++e) {
-            nm[e] = w[e] >> 16;
-            nr[e] = w[e] & 0xFFFFu;
-        }
-        *cm = encode4<false>(m, nm, scale_inv(em));
-        *cr = encode4<true>(r, nr, scale_inv(er));
-        *pp = make_float4(p[0], p[1], p[2], p[3]);
-        if (lane % (kAdamwBlock / kQuad) == 0) {
-            scale[blk] = (uint8_t)em;
-            scale[kAdamwScales + blk] = (uint8_t)er;
-        }
-        if (left > 0) store_quad<PB>(tn.out, i0 + off, left, p);
+    if (i0 + kWaveElems > tn.numel) {
+        last8<NR, GB, PB>(a, tn, u, i0, s0, scale, lane);
+    } else if (aligned_part<GB, PB>(tn, NR > 0 ? NR : a.n)) {
+        full8<NR, GB, PB, true>(a, tn, u, i0, s0, scale, lane);
+    } else {
+        full8<NR, GB, PB, false>(a, tn, u, i0, s0, scale, lane);
     }
 }
 
@@ -345,21 +722,17 @@ __device__ __forceinline__ void encode_nearest(const float *src, uint8_t *codes,
                                                int k) {
     float x[kQuad];
     __builtin_memcpy(x, src + kQuad * k, sizeof x);
-    uint32_t top = 0;
 #pragma unroll
-    for (int e = 0; e < kQuad; ++e) {
+    for (int e = 0; e < kQuad; ++e)
         if (ROOT) x[e] = __builtin_sqrtf(x[e]);
-        const uint32_t b = top_bits(x[e]);
-        top = top > b ? top : b;
-    }
-    const uint32_t eb = scale_byte(block_max(top));
+    const uint32_t eb = scale_byte(__float_as_uint(block_max(quad_max<true>(x))));
     const float inv = scale_inv(eb);
     float y[kQuad];
 #pragma unroll
     for (int e = 0; e < kQuad; ++e) {
         y[e] = x[e] * inv;
-        if (ROOT) y[e] = x[e] > 0.0f ? __builtin_fmaxf(y[e], 0x1p-9f) : y[e];
-        if ((__float_as_uint(x[e]) & 0x7FFFFFFFu) >= kInfBits) y[e] = __builtin_nanf("");
+        if (ROOT) y[e] = at_least_a_code(y[e], x[e]);
+        if (!finite(x[e])) y[e] = __builtin_nanf("");
     }
     *reinterpret_cast<uint32_t *>(codes + kQuad * k) = pack4(y);
     if (k % (kAdamwBlock / kQuad) == 0) scale[kQuad * k / kAdamwBlock] = (uint8_t)eb;
@@ -393,7 +766,7 @@ __global__ void __launch_bounds__(256) widen_kernel(const void *src, float *dst,
 
 // ----------------------------------------------------------- sum of squares
 // S = sum over all elements of (sum_q g_q)^2 / N^2, everything in binary64.
-// Workgroup w takes pieces w, w + G, ...; its partial sum goes to memory and
+// Wave w takes pieces w, w + W, ...; a workgroup's partial sum goes to memory and
 // the last workgroup to finish adds the partials in their order, so the
 // result does not depend on which one that is.
 constexpr int kSumsqBlock = 256;
@@ -413,25 +786,93 @@ __device__ __forceinline__ double group_sum(double x, double *lds) {
     return s;
 }
 
-template <bool GB>
+// Squares of a whole part of a tensor: element i0 on, a quad per lane and
+// turn, kTurns turns in flight together.
+template <int NR, bool GB, int TURNS, bool AL>
+__device__ __forceinline__ double squares_full(Tensor &tn, int nrep, int64_t i0,
+                                               int lane) {
+    const int n = NR > 0 ? NR : nrep;
+    constexpr int es = GB ? 2 : 4;
+    constexpr int grp = NR > 0 && NR < kGroup ? NR : kGroup;
+    double s[TURNS][kQuad];
+#pragma unroll 1
+    for (int q0 = 0; q0 < n; q0 += grp) {
+        RawQuad<GB> raw[grp][TURNS];
+#pragma unroll
+        for (int k = 0; k < grp; ++k)
+            if (NR > 0 || q0 + k < n) {
+                const char *base = static_cast<const char *>(tn.grads[q0 + k]) + i0 * es;
+#pragma unroll
+                for (int h = 0; h < TURNS; ++h)
+                    raw[k][h] = load_raw<GB, AL, kPolNT>(base, kQuad * (lane + h * kWave));
+            }
+#pragma unroll
+        for (int k = 0; k < grp; ++k)
+            if (NR > 0 || q0 + k < n) {
+#pragma unroll
+                for (int h = 0; h < TURNS; ++h) {
+                    float x[kQuad];
+                    widen(raw[k][h], x);
+#pragma unroll
+                    for (int e = 0; e < kQuad; ++e)
+                        s[h][e] = q0 + k == 0 ? (double)x[e] : s[h][e] + (double)x[e];
+                }
+            }
+    }
+    double acc = 0.0;
+#pragma unroll
+    for (int h = 0; h < TURNS; ++h)
+#pragma unroll
+        for (int e = 0; e < kQuad; ++e) acc = __builtin_fma(s[h][e], s[h][e], acc);
+    return acc;
+}
+
+template <int NR, bool GB>
 __global__ void __launch_bounds__(kSumsqBlock)
-sumsq_kernel(const AdamwTensor *__restrict__ table, const int32_t *__restrict__ map,
-             int64_t npieces, int n, double *partial, uint32_t *done, double *out) {
+sumsq_kernel(const AdamwTensor *table, const int32_t *map,
+             int64_t npieces, int nrep, double *partial, uint32_t *done, double *out) {
     __shared__ double lds[kSumsqBlock / kWave];
     __shared__ bool last;
+    const int n = NR > 0 ? NR : nrep;
+    // quads of a lane in flight together: 64 of bf16 or 32 of fp32 over the
+    // replicas, at most 8 of each (two workgroups per unit leave each wave
+    // 256 registers)
+    constexpr int width = NR == 0 || NR > kGroup ? kGroup : NR;
+    constexpr int flight = GB ? 64 : 32;
+    constexpr int turns = flight / width >= 8 ? 8 : flight / width;
+    const int lane = threadIdx.x % kWave;
+    const int64_t first = (int64_t)blockIdx.x * (kSumsqBlock / kWave) +
+                          __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     double acc = 0.0;
-    for (int64_t piece = blockIdx.x; piece < npieces; piece += gridDim.x) {
-        const AdamwTensor &tn = table[map[piece]];
-        const int64_t i0 = (piece - tn.piece0) * kAdamwPiece;
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int64_t i = i0 + kQuad * (threadIdx.x + h * kSumsqBlock);
-            const int64_t left = tn.numel - i;
-            if (left <= 0) continue;
+    for (int64_t piece = first; piece < npieces;
+         piece += (int64_t)gridDim.x * (kSumsqBlock / kWave)) {
+        Tensor &tn = constant(table)[constant(map)[piece]];
+        // The windows that waves read start `head` elements into the tensor's
+        // pieces, where all replicas are aligned if they share a phase (44 us
+        // against 36 without, three bf16 replicas of 28M elements, 3 elements
+        // off); the first wave takes the head.
+        const int head = common_head<GB>(tn, n);
+        const bool al = head >= 0;
+        int64_t i0 = (piece - tn.piece0) * kAdamwPiece;
+        if (al) {
+            if (i0 == 0 && lane < head && lane < tn.numel) {
+                double s = 0.0;
+                for (int q = 0; q < n; ++q) s += (double)elem<GB>(tn.grads[q], lane);
+                acc = __builtin_fma(s, s, acc);
+            }
+            i0 += head;
+        }
+        if (i0 + kAdamwPiece <= tn.numel) {
+            for (int h = 0; h < kAdamwPiece; h += turns * kQuad * kWave)
+                acc += al ? squares_full<NR, GB, turns, true>(tn, n, i0 + h, lane)
+                          : squares_full<NR, GB, turns, false>(tn, n, i0 + h, lane);
+            continue;
+        }
+        for (int64_t i = i0 + kQuad * lane; i < tn.numel; i += kQuad * kWave) {
             double s[kQuad] = {0.0, 0.0, 0.0, 0.0};
             for (int q = 0; q < n; ++q) {
                 float x[kQuad];
-                load_quad<GB>(tn.grads[q], i, left, x);
+                load_quad<GB>(tn.grads[q], i, tn.numel - i, x);
 #pragma unroll
                 for (int e = 0; e < kQuad; ++e) s[e] += (double)x[e];
             }
@@ -442,15 +883,27 @@ sumsq_kernel(const AdamwTensor *__restrict__ table, const int32_t *__restrict__ 
     const double s = group_sum(acc, lds);
     if (threadIdx.x == 0) {
         __hip_atomic_store(&partial[blockIdx.x], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
+        // The partial is the only thing to be ordered before the count, and
+        // an agent-scope store is acknowledged once every XCD can see it, so
+        // waiting for it is enough. A release and acquire at the counter
+        // would write back and drop the whole L2 in every workgroup: 139 us
+        // against 52 us (15.6M elements, N = 8, bf16).
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                gridDim.x - 1;
     }
     __syncthreads();
     if (!last) return;
-    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "agent");
-    double t = 0.0;
-    for (unsigned k = threadIdx.x; k < gridDim.x; k += kSumsqBlock)
-        t += __hip_atomic_load(&partial[k], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    constexpr int per = kSumsqGroups / kSumsqBlock;       // all loads in flight together
+    double x[per], t = 0.0;
+#pragma unroll
+    for (int k = 0; k < per; ++k) {
+        const unsigned i = threadIdx.x + k * kSumsqBlock;
+        x[k] = i < gridDim.x ? __hip_atomic_load(&partial[i], __ATOMIC_RELAXED,
+                                                 __HIP_MEMORY_SCOPE_AGENT) : 0.0;
+    }
+#pragma unroll
+    for (int k = 0; k < per; ++k) t += x[k];
     t = group_sum(t, lds);
     if (threadIdx.x == 0) {
         *out = t / ((double)n * (double)n);
@@ -461,13 +914,13 @@ sumsq_kernel(const AdamwTensor *__restrict__ table, const int32_t *__restrict__ 
 template <int NR, bool GB, bool PB>
 hipError_t launch_typed(const AdamwArgs &a, hipStream_t stream) {
     KernelArgs k = {a.table, a.map, a.n, a.st, a.sc, a.sc_dev, a.ds, a.seed, a.t, a.sumsq,
-                    a.max_norm};
+                    a.max_norm, a.stream_state ? 1 : 0};
     if (a.q8)
         hipLaunchKernelGGL((adamw8_kernel<NR, GB, PB>), dim3((unsigned)a.npieces),
-                           dim3(kWave * kPieceWaves), 0, stream, k);
+                           dim3(kWave * kPieceWaves), ZA_LDS8, stream, k);
     else
         hipLaunchKernelGGL((adamw32_kernel<NR, GB, PB>), dim3((unsigned)(a.npieces * kPieceWaves)),
-                           dim3(kWave), 0, stream, k);
+                           dim3(kWave), ZA_LDS32, stream, k);
     return hipGetLastError();
 }
 
@@ -479,6 +932,29 @@ hipError_t launch_replicas(const AdamwArgs &a, hipStream_t stream) {
     case 4: return launch_typed<4, GB, PB>(a, stream);
     case 8: return launch_typed<8, GB, PB>(a, stream);
     default: return launch_typed<0, GB, PB>(a, stream);
+    }
+}
+
+template <int NR, bool GB>
+hipError_t sumsq_typed(const SumsqArgs &a, hipStream_t stream) {
+    constexpr int per = kSumsqBlock / kWave;
+    const int64_t groups = (a.npieces + per - 1) / per;
+    int64_t grid = groups < kSumsqGroups ? groups : kSumsqGroups;
+    if (grid < 1) grid = 1;                     // no elements: a sum of zero
+    hipLaunchKernelGGL((sumsq_kernel<NR, GB>), dim3((unsigned)grid), dim3(kSumsqBlock), 0, stream,
+                       a.table, a.map, a.npieces, a.n, a.partial, a.done, a.out);
+    return hipGetLastError();
+}
+
+template <bool GB>
+hipError_t sumsq_replicas(const SumsqArgs &a, hipStream_t stream) {
+    switch (a.n) {
+    case 1: return sumsq_typed<1, GB>(a, stream);
+    case 2: return sumsq_typed<2, GB>(a, stream);
+    case 3: return sumsq_typed<3, GB>(a, stream);
+    case 4: return sumsq_typed<4, GB>(a, stream);
+    case 8: return sumsq_typed<8, GB>(a, stream);
+    default: return sumsq_typed<0, GB>(a, stream);
     }
 }
 
@@ -497,15 +973,7 @@ hipError_t launch_adamw(const AdamwArgs &a, hipStream_t stream) {
 
 hipError_t launch_sumsq(const SumsqArgs &a, hipStream_t stream) {
     if (a.n < 1 || a.n > kAdamwMaxReplicas) return hipErrorInvalidValue;
-    const int64_t want = a.npieces < 1 ? 1 : a.npieces;     // no elements: a sum of zero
-    const dim3 g((unsigned)(want < kSumsqGroups ? want : kSumsqGroups)), b(kSumsqBlock);
-    if (a.grad_bf16)
-        hipLaunchKernelGGL(sumsq_kernel<true>, g, b, 0, stream, a.table, a.map, a.npieces, a.n,
-                           a.partial, a.done, a.out);
-    else
-        hipLaunchKernelGGL(sumsq_kernel<false>, g, b, 0, stream, a.table, a.map, a.npieces, a.n,
-                           a.partial, a.done, a.out);
-    return hipGetLastError();
+    return a.grad_bf16 ? sumsq_replicas<true>(a, stream) : sumsq_replicas<false>(a, stream);
 }
 
 hipError_t launch_adamw_decode(const AdamwStateRef &st, int64_t npieces, float *m, float *v,
