@@ -80,11 +80,12 @@ def step32(p, m, v, g, dg, sc, factor, decay):
 def step8(p, m, r, g, dg, sc, factor, decay):
     """(p, m, r) before coding, and their bounds. r*r rounds once. The root is
     a Newton step from the hardware's: at most one ulp, 2 U, off. The step
-    (lr_k/bc1) * (m / (r/sqrt(bc2) + eps)): lr_k (2), bc1 and their quotient;
-    r's root (2), 1/sqrt(bc2) as bc2 through the root (1/2), root and
-    reciprocal, the sum in one fma, the hardware's reciprocal of it (one ulp,
-    2), the product: 12.5 U. The last product is inside the fma that _update
-    counts."""
+    (lr_k/bc1) * (m / (r/sqrt(bc2) + eps)): lr_k (2), bc1, its reciprocal from
+    the hardware (one ulp, 2) and their product; r's root (2), 1/sqrt(bc2) as
+    bc2 through the root (1/2) and the hardware's reciprocal root (one ulp,
+    2), its product with r and the sum in one fma, the hardware's reciprocal
+    of it (2), the product: 14.5 U. The last product is inside the fma that
+    _update counts."""
     mn, dm, vn, dv = moments(g, dg, m, r * r, sc)
     dv = dv + U * sc["b2"] * r * r
     rn = np.sqrt(vn)
@@ -92,7 +93,7 @@ def step8(p, m, r, g, dg, sc, factor, decay):
     den = rn / np.sqrt(sc["bc2"]) + sc["eps"]
     lr = sc["lr"] * factor
     u = _ratio(lr * mn / sc["bc1"], den)
-    du = _ratio(abs(lr) * dm / sc["bc1"], den) + np.abs(u) * (0.5 * _ratio(dv, vn) + 13 * U)
+    du = _ratio(abs(lr) * dm / sc["bc1"], den) + np.abs(u) * (0.5 * _ratio(dv, vn) + 14.5 * U)
     pn, dp = _update(p, u, SAFE * du, sc["lr"], factor, decay)
     return (pn, mn, rn), (dp, dm, dr)
 

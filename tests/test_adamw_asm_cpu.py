@@ -50,10 +50,11 @@ def test_no_loops_over_descriptors(kernels):
 
 
 def test_state_streams(kernels):
-    """Every buffer access carries the streaming hint; the 32-bit step has
-    device-scope stores beside the plain ones."""
+    """Every buffer access carries the streaming hint, and stores come plain
+    and at device scope."""
     for name, body, _ in kernels:
         if "adamw32_kernel" in name or "adamw8_kernel" in name:
             lines = re.findall(r"buffer_(?:load|store)_dword\w* [^\n]*", body)
             assert lines and all(re.search(r"\bnt\b", x) for x in lines), name
-            assert ("sc1" in " ".join(lines)) == ("adamw32" in name), name
+            stores = [x for x in lines if x.startswith("buffer_store")]
+            assert 2 * sum("sc1" in x for x in stores) == len(stores), name

@@ -33,29 +33,26 @@ constexpr int kPieceWaves = kAdamwPiece / kWaveElems;
 
 // Dynamic LDS that a workgroup reserves and does not touch, to set how many
 // share a compute unit (160 KiB each).
-// 32-bit states, one-wave workgroups, 10 per unit: 3.91-3.97 ms on the
-// Llama-7B list (rank of 8, reduced fp32 gradients) against 4.04 at 13, 3.94-
-// 3.97 at 8 and 4.34 at 6; GPT-2 small whole 538 us against 555, 543 and 607.
-#ifndef ZA_LDS32
-#define ZA_LDS32 16384
-#endif
+// 32-bit states, one-wave workgroups, 7 per unit: 3.94 ms on the Llama-7B list
+// (rank of 8, reduced fp32 gradients) and 537 us on GPT-2 small whole, against
+// 3.97 and 541 at 8, 3.98 and 550 at 10, 4.19 and 544 at 14, 3.96 and 541 at 6
+// (one state, all variants in turn).
+constexpr unsigned kLds32 = 22528;
 // 8-bit states, one piece per workgroup (so that each 128-byte line of scales
-// is one workgroup's), 4 per unit: 2.14-2.15 ms on the same list in four runs
-// against 2.15-2.33 at 6 and 2.14-2.28 uncapped; one- and two-wave workgroups
-// 2.11-2.39.
-#ifndef ZA_LDS8
-#define ZA_LDS8 40960
-#endif
+// is one workgroup's), 3 per unit: 2.16 ms on the same list wherever its
+// buffers came to lie; 4 per unit took 2.12 or 2.25 by their placement, 6 took
+// 2.15 or 2.31, 2 took 2.49, uncapped 2.14 to 2.28.
+constexpr unsigned kLds8 = 53248;
 // Cache policies of buffer instructions (gfx950: nt = 2, sc1 = 16). Loads and
 // stores stream (nt): what a step touches does not outlive the forward and
 // backward pass that follows it in the Infinity Cache. Default-policy stores
 // ran at 4.60 ms where nt ones took 4.05 (32 bits, Llama-7B) and 2.58 where
 // these took 2.38 (8 bits).
 constexpr int kPolDefault = 0, kPolNT = 2;
-// 32-bit states larger than the 256 MB Infinity Cache store at device scope as
-// well (nt sc1): 3.92-3.95 ms against 3.96-4.05 (Llama-7B), 547 us against 560
-// (GPT-2 small whole); smaller ones do not: 116 us against 110 (GPT-2 small,
-// rank 3 of 8, three states in turn).
+// A state larger than the 256 MB Infinity Cache is stored at device scope as
+// well (nt sc1): 3.92-3.95 ms against 3.96-4.05 with 32 bits and 2.09 against
+// 2.12 with 8 (Llama-7B); a smaller one is not: 116 us against 110 and 86
+// against 80 (GPT-2 small, rank 3 of 8, three states in turn).
 constexpr int kPolDevice = 18;
 
 template <int V> struct Const { static constexpr int value = V; };
@@ -459,15 +456,18 @@ __device__ __forceinline__ uint32_t scale_byte(uint32_t top) {
 __device__ __forceinline__ float scale_of(uint32_t e) { return __uint_as_float(e << 23); }
 __device__ __forceinline__ float scale_inv(uint32_t e) { return __uint_as_float((254u - e) << 23); }
 
-// Largest over the 8 lanes that hold a block (of values that are not negative).
-__device__ __forceinline__ float block_max(float x) {
-    const auto lane = [](float v, auto ctrl) {
-        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), decltype(ctrl)::value,
-                                                          0xF, 0xF, false));
+// Largest over the 8 lanes that hold a block, of magnitude bits (which order
+// as the magnitudes do; an integer maximum takes its operand across lanes in
+// the same instruction).
+__device__ __forceinline__ uint32_t block_max(uint32_t x) {
+    const auto lane = [](uint32_t v, auto ctrl) {
+        return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, 0xF, 0xF,
+                                                     false);
     };
-    x = __builtin_fmaxf(x, lane(x, Const<0xB1>()));            // 1 lane apart
-    x = __builtin_fmaxf(x, lane(x, Const<0x4E>()));            // 2 apart
-    return __builtin_fmaxf(x, lane(x, Const<0x141>()));        // the other four
+    const auto larger = [](uint32_t a, uint32_t b) { return a > b ? a : b; };
+    x = larger(x, lane(x, Const<0xB1>()));            // 1 lane apart
+    x = larger(x, lane(x, Const<0x4E>()));            // 2 apart
+    return larger(x, lane(x, Const<0x141>()));        // the other four
 }
 
 __device__ __forceinline__ bool finite(float x) {
@@ -477,12 +477,12 @@ __device__ __forceinline__ bool finite(float x) {
 // Largest magnitude of a quad. SAFE: what is not finite does not count, so
 // an infinity or NaN of one element leaves its neighbours' codes alone.
 template <bool SAFE>
-__device__ __forceinline__ float quad_max(const float (&x)[kQuad]) {
+__device__ __forceinline__ uint32_t quad_max(const float (&x)[kQuad]) {
     float t = 0.0f;
 #pragma unroll
     for (int e = 0; e < kQuad; ++e)
         t = __builtin_fmaxf(t, SAFE && !finite(x[e]) ? 0.0f : __builtin_fabsf(x[e]));
-    return t;
+    return __float_as_uint(t);
 }
 
 __device__ __forceinline__ uint32_t pack4(const float (&y)[kQuad]) {
@@ -537,14 +537,19 @@ __device__ __forceinline__ float root(float v) {
     return __builtin_fmaf(__builtin_fmaf(-s, s, v), 0.5f * y, s);
 }
 
-// Fresh moments of a quad from the old ones, and the step d they give. Only d
-// takes the hardware's reciprocal (1 ulp; its operand is 0 or at least
-// 2^-75): the codes do not depend on it.
-__device__ __forceinline__ void moments8(const float (&g)[kQuad], float (&m)[kQuad],
+// Fresh moments of a quad from the stored ones (codes cm, cr on the scales em,
+// er), and the step d they give. b1 goes into m's scale, a power of two: the
+// same bits as (code * scale) * b1 above the smallest scale. Only d takes the
+// hardware's reciprocal (1 ulp; its operand is 0 or at least 2^-75): the
+// codes do not depend on it.
+__device__ __forceinline__ void moments8(const float (&g)[kQuad], uint32_t cm, uint32_t cr,
+                                         uint32_t em, uint32_t er, float (&m)[kQuad],
                                          float (&r)[kQuad], float (&d)[kQuad], const Uniform8 &u) {
+    unpack4(cm, scale_of(em) * u.sc.b1, m);
+    unpack4(cr, scale_of(er), r);
 #pragma unroll
     for (int e = 0; e < kQuad; ++e) {
-        m[e] = __builtin_fmaf(g[e], u.sc.c1, m[e] * u.sc.b1);
+        m[e] = __builtin_fmaf(g[e], u.sc.c1, m[e]);
         r[e] = root(__builtin_fmaf(u.sc.c2 * g[e], g[e], (r[e] * r[e]) * u.sc.b2));
         d[e] = m[e] * __builtin_amdgcn_rcpf(__builtin_fmaf(r[e], u.rs, u.sc.eps));
     }
@@ -555,13 +560,16 @@ template <bool SAFE>
 __device__ __forceinline__ void encode8(const float (&m)[kQuad], const float (&r)[kQuad],
                                         const Uniform8 &u, int64_t q, uint32_t &cm, uint32_t &cr,
                                         uint32_t &em, uint32_t &er) {
-    em = scale_byte(__float_as_uint(block_max(quad_max<SAFE>(m))));
-    er = scale_byte(__float_as_uint(block_max(quad_max<SAFE>(r))));
+    em = scale_byte(block_max(quad_max<SAFE>(m)));
+    er = scale_byte(block_max(quad_max<SAFE>(r)));
     const uint32_t x = adamw_mix((uint32_t)q + (uint32_t)(q >> 32) * 0x7F4A7C15u + u.key);
-    const uint32_t w[kQuad] = {x, x * 0xB5297A4Du, x * 0x68E31DA5u, x * 0x1B56C4E9u};
+    uint32_t w[kQuad] = {x, x * 0xB5297A4Du, x * 0x68E31DA5u, x * 0x1B56C4E9u};
     uint32_t nm[kQuad], nr[kQuad];
 #pragma unroll
     for (int e = 0; e < kQuad; ++e) {
+        // opaque, or the compiler takes the low half's shift into a second
+        // product (a product costs four of the other instructions)
+        asm("" : "+v"(w[e]));
         nm[e] = w[e] >> 16;
         nr[e] = w[e] & 0xFFFFu;
     }
@@ -569,10 +577,11 @@ __device__ __forceinline__ void encode8(const float (&m)[kQuad], const float (&r
     cr = encode4<true, SAFE>(r, nr, scale_inv(er));
 }
 
-// Whether a step of the quad is NaN, as it is where a moment is not finite:
+// Lanes with a NaN step in their quad, as it is where a moment is not finite:
 // an infinite m or g comes with an infinite v, whose root is NaN.
-__device__ __forceinline__ bool nan_step(const float (&d)[kQuad]) {
-    return __builtin_isunordered(d[0], d[1]) || __builtin_isunordered(d[2], d[3]);
+__device__ __forceinline__ uint64_t nan_lanes(const float (&d)[kQuad]) {
+    return __builtin_amdgcn_ballot_w64(__builtin_isunordered(d[0], d[1])) |
+           __builtin_amdgcn_ballot_w64(__builtin_isunordered(d[2], d[3]));
 }
 
 template <int NR, bool GB, bool PB, bool AL>
@@ -596,16 +605,14 @@ __device__ __forceinline__ void full8(const KernelArgs &a, Tensor &tn,
         __builtin_amdgcn_sched_barrier(0);
     });
     float d[kSplit][kQuad];
-    bool bad = false;
+    uint64_t bad = 0;
 #pragma unroll
     for (int h = 0; h < kSplit; ++h) {
-        unpack4(cm[h], scale_of(em[h]), m[h]);
-        unpack4(cr[h], scale_of(er[h]), r[h]);
-        moments8(g[h], m[h], r[h], d[h], u);
-        bad |= nan_step(d[h]);
+        moments8(g[h], cm[h], cr[h], em[h], er[h], m[h], r[h], d[h], u);
+        bad |= nan_lanes(d[h]);
     }
     const int64_t q = s0 / kQuad + lane;
-    if (__builtin_expect(__builtin_amdgcn_ballot_w64(bad) != 0, 0)) {
+    if (__builtin_expect(bad != 0, 0)) {
 #pragma unroll
         for (int h = 0; h < kSplit; ++h)
             encode8<true>(m[h], r[h], u, q + h * kWave, cm[h], cr[h], em[h], er[h]);
@@ -616,18 +623,29 @@ __device__ __forceinline__ void full8(const KernelArgs &a, Tensor &tn,
     }
     char *out = static_cast<char *>(tn.out) + i0 * (PB ? 2 : 4);
 #pragma unroll
-    for (int h = 0; h < kSplit; ++h) {
-        const int off = kQuad * (lane + h * kWave);
+    for (int h = 0; h < kSplit; ++h)
 #pragma unroll
         for (int e = 0; e < kQuad; ++e)
             p[h][e] = __builtin_fmaf(-u.lrc, d[h][e], p[h][e] * u.keep);
-        store_f4<kPolNT>(sp, off, p[h]);
-        store_raw<PB, AL, kPolNT>(out, off, narrow<PB>(p[h]));
-        __builtin_amdgcn_raw_buffer_store_b32(cm[h], sm, off, 0, kPolNT);
-        __builtin_amdgcn_raw_buffer_store_b32(cr[h], sr, off, 0, kPolNT);
-        if (lane % (kAdamwBlock / kQuad) == 0) {
-            scale[off / kAdamwBlock] = (uint8_t)em[h];
-            scale[kAdamwScales + off / kAdamwBlock] = (uint8_t)er[h];
+    const auto store = [&](auto pol) {
+        constexpr int P = decltype(pol)::value;
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h) {
+            const int off = kQuad * (lane + h * kWave);
+            store_f4<P>(sp, off, p[h]);
+            store_raw<PB, AL, P>(out, off, narrow<PB>(p[h]));
+            __builtin_amdgcn_raw_buffer_store_b32(cm[h], sm, off, 0, P);
+            __builtin_amdgcn_raw_buffer_store_b32(cr[h], sr, off, 0, P);
+        }
+    };
+    if (a.stream_state) store(Const<kPolDevice>());
+    else store(Const<kPolNT>());
+    if (lane % (kAdamwBlock / kQuad) == 0) {
+#pragma unroll
+        for (int h = 0; h < kSplit; ++h) {
+            const int blk = kQuad * (lane + h * kWave) / kAdamwBlock;
+            scale[blk] = (uint8_t)em[h];
+            scale[kAdamwScales + blk] = (uint8_t)er[h];
         }
     }
 }
@@ -648,10 +666,8 @@ __device__ __forceinline__ void last8(const KernelArgs &a, Tensor &tn,
         uint32_t *pr = reinterpret_cast<uint32_t *>(a.st.r8 + s0 + off);
         float *pp = a.st.master + s0 + off;
         uint8_t *sc = scale + off / kAdamwBlock;
-        unpack4(*pm, scale_of(sc[0]), m);
-        unpack4(*pr, scale_of(sc[kAdamwScales]), r);
         uint32_t cm, cr, em, er;
-        moments8(g, m, r, d, u);
+        moments8(g, *pm, *pr, sc[0], sc[kAdamwScales], m, r, d, u);
         encode8<true>(m, r, u, (s0 + off) / kQuad, cm, cr, em, er);
         *pm = cm;
         *pr = cr;
@@ -679,8 +695,8 @@ __global__ void __launch_bounds__(kWave *kPieceWaves) adamw8_kernel(KernelArgs a
     Uniform8 u;
     if (!uniforms<NR>(a, tn, u)) return;
     u.key = adamw_mix(a.seed ^ (a.sc_dev ? (uint32_t)(constant(a.ds)->t - 1) : a.t));
-    u.lrc = u.lr / u.sc.bc1;
-    u.rs = 1.0f / __builtin_sqrtf(u.sc.bc2);
+    u.lrc = u.lr * __builtin_amdgcn_rcpf(u.sc.bc1);      // 1 ulp, and so is the root
+    u.rs = __builtin_amdgcn_rsqf(u.sc.bc2);
     const int64_t s0 = piece * kAdamwPiece + wave * kWaveElems;
     uint8_t *scale = a.st.scale + piece * (2 * kAdamwScales) + wave * (kWaveElems / kAdamwBlock);
     if (i0 + kWaveElems > tn.numel) {
@@ -725,7 +741,7 @@ __device__ __forceinline__ void encode_nearest(const float *src, uint8_t *codes,
 #pragma unroll
     for (int e = 0; e < kQuad; ++e)
         if (ROOT) x[e] = __builtin_sqrtf(x[e]);
-    const uint32_t eb = scale_byte(__float_as_uint(block_max(quad_max<true>(x))));
+    const uint32_t eb = scale_byte(block_max(quad_max<true>(x)));
     const float inv = scale_inv(eb);
     float y[kQuad];
 #pragma unroll
@@ -887,7 +903,7 @@ sumsq_kernel(const AdamwTensor *table, const int32_t *map,
         // an agent-scope store is acknowledged once every XCD can see it, so
         // waiting for it is enough. A release and acquire at the counter
         // would write back and drop the whole L2 in every workgroup: 139 us
-        // against 52 us (15.6M elements, N = 8, bf16).
+        // against 52 us (15.6M elements, N = 8, bf16, 2048 workgroups).
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         last = __hip_atomic_fetch_add(done, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
                gridDim.x - 1;
@@ -917,10 +933,10 @@ hipError_t launch_typed(const AdamwArgs &a, hipStream_t stream) {
                     a.max_norm, a.stream_state ? 1 : 0};
     if (a.q8)
         hipLaunchKernelGGL((adamw8_kernel<NR, GB, PB>), dim3((unsigned)a.npieces),
-                           dim3(kWave * kPieceWaves), ZA_LDS8, stream, k);
+                           dim3(kWave * kPieceWaves), kLds8, stream, k);
     else
         hipLaunchKernelGGL((adamw32_kernel<NR, GB, PB>), dim3((unsigned)(a.npieces * kPieceWaves)),
-                           dim3(kWave), ZA_LDS32, stream, k);
+                           dim3(kWave), kLds32, stream, k);
     return hipGetLastError();
 }
 
