@@ -383,8 +383,9 @@ int zero_fsdp_step_sched(zero_ctx *ctx, const void *const *grads,
  * deterministic hash of the seed, t and the element's place: the same call on
  * the same state gives the same bits). Rounding to nearest would freeze v: a
  * step moves it by about 1-b2 of itself, the codes of r are 6-12% apart. A
- * nonzero v is never stored as zero; an infinite or NaN moment is stored as
- * NaN and does not touch the scale of its neighbours.
+ * v of 2^-126 or more is never stored as zero (below, its root comes out too
+ * small); an infinite or NaN moment is stored as NaN, makes its own master
+ * NaN and does not touch its neighbours' codes.
  *
  * A context's calls read and write its state, its device table and one
  * workspace: order them among themselves (one stream, or events), replays of
@@ -401,7 +402,8 @@ int zero_fsdp_step_sched(zero_ctx *ctx, const void *const *grads,
  * apply; zero_fsdp_step does with 32 bits only. zero_get_state gives m and v
  * of 8-bit states in fp32 exactly; zero_set_state rounds them to the nearest
  * codes, which leaves values that came from zero_get_state unchanged, except
- * a v below 2^-126, which fp32 cannot square exactly.
+ * a v below 2^-126, whose root fp32 cannot hold the square of. What is behind
+ * a tensor's last element must be zero in what zero_set_state gets.
  * EINVAL: as zero_fsdp_init (but any world up to ZERO_MAX_WORLD), state_bits
  * not 8 or 32, more elements than 64 bits count. EUNSUPPORTED: more than 3.4e10
  * local elements. ENOMEM / EHIP as zero_shard_init. Synchronous. */
@@ -411,7 +413,7 @@ int zero_adamw_init(int32_t ntensors, const int64_t *dim0,
                     int32_t state_bits, uint32_t seed, zero_ctx **out);
 
 /* Weight decay and learning-rate scale per tensor (host arrays of ntensors;
- * NULL: 0, or 1, for all), rounded to fp32, for the steps after it on the
+ * NULL: 0, or 1, for all), rounded to fp32 (and finite there), for the steps after it on the
  * stream; a captured step takes what holds when it replays. EINVAL: not an
  * AdamW context, a decay that is negative or not finite, a scale that is not
  * finite. */

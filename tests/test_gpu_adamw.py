@@ -563,6 +563,35 @@ def test_another_stream(state_bits):
     b.close()
 
 
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_a_new_state_on_a_stream_of_its_own(state_bits):
+    """Everything after the constructor on a side stream that waits for
+    nothing: the constructor leaves no work behind on its own stream. Decay as
+    an array, the device without its index."""
+    side = torch.cuda.Stream()
+    g = torch.randn(10_000, device="cuda") * 1e-3
+    p = torch.randn(10_000, device="cuda") * 0.02
+    outs = [torch.zeros(10_000, device="cuda") for _ in range(2)]
+    torch.cuda.synchronize()
+    states = []
+    for k in range(2):
+        st = zero.AdamWState([(10_000,)], 1, 0, LR, weight_decay=np.array([0.3]),
+                             state_bits=state_bits, device="cuda")
+        assert st.device == torch.device("cuda", 0)
+        stream = side if k else None
+        st.load_master([p], stream=stream)
+        st.bind([[g]], [outs[k]], stream=stream)
+        for t in (1, 2):
+            st.step(t, sumsq=st.sumsq(stream=stream), max_norm=0.05, stream=stream)
+        states.append(st)
+    torch.cuda.synchronize()
+    assert torch.equal(outs[0], outs[1]) and outs[0].any()
+    (a, b) = (x.get_state() for x in states)
+    assert all(torch.equal(x, y) for x, y in zip(a, b))
+    for st in states:
+        st.close()
+
+
 def test_the_same_gradient_bound_twice():
     """One tensor as the gradient of two parameters, and as two replicas."""
     shapes = [(1000,), (1000,)]
@@ -661,7 +690,7 @@ def test_refusals():
     for bad in (0.0, -1.0, float("nan"), float("inf")):
         _einval(st.step, 1, sumsq=s, max_norm=bad)
     for kw in (dict(weight_decay=-0.1), dict(weight_decay=float("nan")),
-               dict(lr_scale=float("inf"))):
+               dict(weight_decay=1e300), dict(lr_scale=float("inf")), dict(lr_scale=-1e300)):
         _einval(st.set_groups, **kw)
     with pytest.raises(ValueError):
         st.step(1, sumsq=s)                              # no max_norm

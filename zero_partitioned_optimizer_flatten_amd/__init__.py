@@ -109,9 +109,10 @@ def _dtype_code(dt: torch.dtype) -> int:
     raise TypeError(f"only float32 and bfloat16 are supported, got {dt}")
 
 
-def _stream_handle(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+def _resolve_device(device) -> torch.device:
+    """The given device, or the current one; always with its index."""
+    d = torch.device("cuda") if device is None else torch.device(device)
+    return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
 # torch's own lookup of a device's current stream handle: 0.1 us, where building
@@ -119,10 +120,16 @@ def _stream_handle(stream: Optional[torch.cuda.Stream]) -> ctypes.c_void_p:
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _current_stream_handle(device: torch.device) -> int:
-    if _raw_stream is not None:
-        return _raw_stream(device.index)
-    return torch.cuda.current_stream(device).cuda_stream
+def _stream_handle(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
+    """The given stream, or `device`'s current one (whatever device is current
+    in the caller)."""
+    if stream is None:
+        if _raw_stream is not None:
+            return _raw_stream(device.index)
+        return torch.cuda.current_stream(device).cuda_stream
+    if stream.device != device:
+        raise ValueError(f"stream is on {stream.device}, state is on {device}")
+    return stream.cuda_stream
 
 
 def _ptr_array(ptrs: Sequence[int]):
@@ -160,8 +167,7 @@ class ShardState:
     def __init__(self, numel: int, world: int, rank: int, lr: float,
                  betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
                  device=None):
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
-            else torch.device(device)
+        self.device = _resolve_device(device)
         self.numel, self.world, self.rank = int(numel), int(world), int(rank)
         h = ctypes.c_void_p()
         with torch.cuda.device(self.device):
@@ -226,7 +232,7 @@ class ShardState:
                              f"need {off + self.shard}")
         _check(lib().zero_load_master(self._h, flat_params.data_ptr(),
                                       _dtype_code(flat_params.dtype), off,
-                                      _stream_handle(stream)))
+                                      _stream_handle(stream, self.device)))
 
     def flatten(self, tensors: Sequence[torch.Tensor], out: torch.Tensor, stream=None,
                 window: Optional[Tuple[int, int]] = None):
@@ -244,12 +250,12 @@ class ShardState:
         ptrs = _ptr_array([t.data_ptr() for t in tensors])
         if window is None:
             _check(lib().zero_flatten(self._h, ptrs, numels, len(tensors), _dtype_code(dt),
-                                      out.data_ptr(), _stream_handle(stream)))
+                                      out.data_ptr(), _stream_handle(stream, self.device)))
         else:
             b, n = window
             _check(lib().zero_flatten_range(self._h, ptrs, numels, len(tensors), _dtype_code(dt),
                                             out.data_ptr(), int(b), int(n),
-                                            _stream_handle(stream)))
+                                            _stream_handle(stream, self.device)))
 
     def unflatten(self, flat: torch.Tensor, tensors: Sequence[torch.Tensor], stream=None):
         """Copy flat[off_t : off_t + numel_t] into each tensor, in order."""
@@ -264,7 +270,7 @@ class ShardState:
         numels = (ctypes.c_int64 * max(1, len(tensors)))(*[t.numel() for t in tensors])
         ptrs = _ptr_array([t.data_ptr() for t in tensors])
         _check(lib().zero_unflatten(self._h, flat.data_ptr(), len(tensors), numels,
-                                    _dtype_code(dt), ptrs, _stream_handle(stream)))
+                                    _dtype_code(dt), ptrs, _stream_handle(stream, self.device)))
 
     def _step_args(self, replicas, param_out, grad_offset, param_offset):
         if len(replicas) != self.world:
@@ -313,7 +319,7 @@ class ShardState:
         ptrs, gdt, go, po = self._step_args(replicas, param_out, grad_offset, param_offset)
         _check(lib().zero_step(self._h, ptrs, len(replicas), _dtype_code(gdt), go,
                                param_out.data_ptr(), _dtype_code(param_out.dtype), po,
-                               int(t), _stream_handle(stream)))
+                               int(t), _stream_handle(stream, self.device)))
 
     def step_range(self, shard_begin: int, count: int, replicas: Sequence[torch.Tensor],
                    t: int, param_out: torch.Tensor, grad_offset: int = 0,
@@ -327,35 +333,37 @@ class ShardState:
         _check(lib().zero_step_range(self._h, int(shard_begin), int(count), ptrs, len(replicas),
                                      _dtype_code(gdt), int(grad_offset), param_out.data_ptr(),
                                      _dtype_code(param_out.dtype), int(param_offset), int(t),
-                                     _stream_handle(stream)))
+                                     _stream_handle(stream, self.device)))
 
     # ------------------------------------------- device-resident schedule
     def schedule(self, next_t: int = 1, stream=None):
         """Keep the step count and lr on the device (created on first use,
         outside any graph capture): the next scheduled step is next_t."""
         with torch.cuda.device(self.device):
-            _check(lib().zero_schedule_init(self._h, int(next_t), _stream_handle(stream)))
+            _check(lib().zero_schedule_init(self._h, int(next_t),
+                                            _stream_handle(stream, self.device)))
 
     def schedule_noalloc(self, next_t: int = 1, stream=None):
         """schedule() in the device's static block: allocates nothing (one
         such schedule per device at a time)."""
         with torch.cuda.device(self.device):
             _check(lib().zero_schedule_init_noalloc(self._h, int(next_t),
-                                                    _stream_handle(stream)))
+                                                    _stream_handle(stream, self.device)))
 
     def schedule_lr(self, lr: float, stream=None):
         """Learning rate of later scheduled steps (stream-ordered)."""
-        _check(lib().zero_schedule_lr(self._h, float(lr), _stream_handle(stream)))
+        _check(lib().zero_schedule_lr(self._h, float(lr), _stream_handle(stream, self.device)))
 
     def schedule_next_t(self, stream=None) -> int:
         """The next scheduled step count (waits for the stream)."""
         out = ctypes.c_int64()
-        _check(lib().zero_schedule_get(self._h, ctypes.byref(out), _stream_handle(stream)))
+        _check(lib().zero_schedule_get(self._h, ctypes.byref(out),
+                                       _stream_handle(stream, self.device)))
         return out.value
 
     def step_begin(self, stream=None):
         """Begin the next scheduled step (before step_range_sched calls)."""
-        _check(lib().zero_step_begin(self._h, _stream_handle(stream)))
+        _check(lib().zero_step_begin(self._h, _stream_handle(stream, self.device)))
 
     def step_sched(self, replicas: Sequence[torch.Tensor], param_out: torch.Tensor,
                    grad_offset: Optional[int] = None, param_offset: Optional[int] = None,
@@ -365,7 +373,7 @@ class ShardState:
         ptrs, gdt, go, po = self._step_args(replicas, param_out, grad_offset, param_offset)
         _check(lib().zero_step_sched(self._h, ptrs, len(replicas), _dtype_code(gdt), go,
                                      param_out.data_ptr(), _dtype_code(param_out.dtype), po,
-                                     _stream_handle(stream)))
+                                     _stream_handle(stream, self.device)))
 
     def step_range_sched(self, shard_begin: int, count: int, replicas: Sequence[torch.Tensor],
                          param_out: torch.Tensor, grad_offset: int = 0, param_offset: int = 0,
@@ -376,7 +384,7 @@ class ShardState:
         _check(lib().zero_step_range_sched(self._h, int(shard_begin), int(count), ptrs,
                                            len(replicas), _dtype_code(gdt), int(grad_offset),
                                            param_out.data_ptr(), _dtype_code(param_out.dtype),
-                                           int(param_offset), _stream_handle(stream)))
+                                           int(param_offset), _stream_handle(stream, self.device)))
 
     def bucket_ranges(self, bucket_bounds: Sequence[int]) -> List[Tuple[int, int, int, int]]:
         """For gradient buckets given as flat-vector boundaries
@@ -397,7 +405,7 @@ class ShardState:
         out = [torch.empty(self.shard, dtype=torch.float32, device=self.device)
                for _ in range(3)]
         _check(lib().zero_get_state(self._h, out[0].data_ptr(), out[1].data_ptr(),
-                                    out[2].data_ptr(), _stream_handle(stream)))
+                                    out[2].data_ptr(), _stream_handle(stream, self.device)))
         return out
 
     def set_state(self, master: torch.Tensor, m: torch.Tensor, v: torch.Tensor, stream=None):
@@ -406,7 +414,7 @@ class ShardState:
             if x.dtype != torch.float32 or x.numel() != self.shard:
                 raise ValueError(f"{name} must be float32 with {self.shard} elements")
         _check(lib().zero_set_state(self._h, master.data_ptr(), m.data_ptr(), v.data_ptr(),
-                                    _stream_handle(stream)))
+                                    _stream_handle(stream, self.device)))
 
 
 def dim0_split(dim0: int, world: int, rank: int) -> Tuple[int, int]:
@@ -423,8 +431,7 @@ class FsdpShardState(ShardState):
 
     def __init__(self, shapes, world: int, rank: int, lr: float,
                  betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8, device=None):
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
-            else torch.device(device)
+        self.device = _resolve_device(device)
         self.shapes = [tuple(int(d) for d in s) for s in shapes]
         self.world, self.rank = int(world), int(rank)
         n = len(self.shapes)
@@ -478,7 +485,7 @@ class FsdpShardState(ShardState):
             raise TypeError("params must share one dtype")
         ptrs = _ptr_array([p.data_ptr() if p is not None else 0 for p in params])
         _check(lib().zero_fsdp_load_master(self._h, ptrs, _dtype_code(dts.pop()),
-                                           _stream_handle(stream)))
+                                           _stream_handle(stream, self.device)))
 
     def _fsdp_args(self, replica_grads, params_out):
         if len(replica_grads) != self.world:
@@ -515,14 +522,14 @@ class FsdpShardState(ShardState):
         params_out[k]: this rank's local shard of parameter k (written)."""
         gptrs, gdt, optrs, pdt = self._fsdp_args(replica_grads, params_out)
         _check(lib().zero_fsdp_step(self._h, gptrs, self.world, _dtype_code(gdt), optrs,
-                                    _dtype_code(pdt), int(t), _stream_handle(stream)))
+                                    _dtype_code(pdt), int(t), _stream_handle(stream, self.device)))
 
     def step_sched(self, replica_grads: Sequence[Sequence[torch.Tensor]],
                    params_out: Sequence[torch.Tensor], stream=None):
         """step() at the device schedule's next step count and lr."""
         gptrs, gdt, optrs, pdt = self._fsdp_args(replica_grads, params_out)
         _check(lib().zero_fsdp_step_sched(self._h, gptrs, self.world, _dtype_code(gdt), optrs,
-                                          _dtype_code(pdt), _stream_handle(stream)))
+                                          _dtype_code(pdt), _stream_handle(stream, self.device)))
 
     def state_pieces(self, state: Sequence[torch.Tensor]):
         """Split (master, m, v) from get_state into per-parameter local pieces."""
@@ -564,10 +571,7 @@ class AdamWState(FsdpShardState):
                  betas: Tuple[float, float] = (0.9, 0.999), eps: float = 1e-8,
                  weight_decay=0.0, lr_scale=1.0, state_bits: int = 32, seed: int = 0,
                  device=None):
-        self.device = torch.device("cuda", torch.cuda.current_device()) if device is None \
-            else torch.device(device)
-        if self.device.index is None:
-            self.device = torch.device("cuda", torch.cuda.current_device())
+        self.device = _resolve_device(device)
         self.shapes = [tuple(int(d) for d in s) for s in shapes]
         self.world, self.rank, self.state_bits = int(world), int(rank), int(state_bits)
         if not 0 <= int(seed) < 1 << 32:
@@ -589,15 +593,7 @@ class AdamWState(FsdpShardState):
         self._bound = None
         self._read_layout()
         self.set_groups(weight_decay, lr_scale)
-
-    def _stream(self, stream):
-        """The given stream, or this device's current one (whatever device is
-        current in the caller)."""
-        if stream is None:
-            return _current_stream_handle(self.device)
-        if stream.device != self.device:
-            raise ValueError(f"stream is on {stream.device}, state is on {self.device}")
-        return stream.cuda_stream
+        torch.cuda.current_stream(self.device).synchronize()    # for calls on any stream
 
     def set_groups(self, weight_decay=0.0, lr_scale=1.0, stream=None):
         """Weight decay and learning-rate scale of later steps: a number for
@@ -605,11 +601,11 @@ class AdamWState(FsdpShardState):
         n = len(self.shapes)
         arrays = []
         for name, x in (("weight_decay", weight_decay), ("lr_scale", lr_scale)):
-            x = [float(v) for v in x] if isinstance(x, (list, tuple)) else [float(x)] * n
+            x = [float(v) for v in x] if hasattr(x, "__len__") else [float(x)] * n
             if len(x) != n:
                 raise ValueError(f"{name}: need {n} values, got {len(x)}")
             arrays.append((ctypes.c_double * max(1, n))(*x))
-        _check(lib().zero_adamw_groups(self._h, *arrays, self._stream(stream)))
+        _check(lib().zero_adamw_groups(self._h, *arrays, _stream_handle(stream, self.device)))
 
     def _local_ptr(self, x: Optional[torch.Tensor], k: int, what: str, whole: bool) -> int:
         """Address of this rank's elements of parameter k in x, which holds
@@ -636,7 +632,9 @@ class AdamWState(FsdpShardState):
         gradients that are reduced already). params_out[k]: this rank's rows,
         written by steps; None binds gradients alone (for sumsq). None is
         taken for parameters of which this rank holds no rows. The state
-        keeps the tensors alive until the next bind."""
+        keeps the tensors alive until the next bind; a step reads these very
+        buffers, so gradients stay in place (zero_grad(set_to_none=False)) or
+        are bound again."""
         n = len(self.shapes)
         for q, gl in enumerate(grads):
             if len(gl) != n:
@@ -656,7 +654,7 @@ class AdamWState(FsdpShardState):
         gdt = _dtype_code(gdts.pop()) if gdts else ZERO_F32
         pdt = _dtype_code(pdts.pop()) if pdts else ZERO_F32
         _check(lib().zero_adamw_bind(self._h, gptrs, len(grads), gdt, optrs, pdt,
-                                     self._stream(stream)))
+                                     _stream_handle(stream, self.device)))
         self._bound = ([list(gl) for gl in grads],
                        None if params_out is None else list(params_out))
 
@@ -675,7 +673,8 @@ class AdamWState(FsdpShardState):
         if out is None:
             with torch.cuda.device(self.device), torch.cuda.stream(stream):
                 out = torch.empty(1, dtype=torch.float64, device=self.device)
-        _check(lib().zero_adamw_sumsq(self._h, self._sum_ptr(out), self._stream(stream)))
+        _check(lib().zero_adamw_sumsq(self._h, self._sum_ptr(out),
+                                      _stream_handle(stream, self.device)))
         return out
 
     def step(self, t: int, sumsq: Optional[torch.Tensor] = None,
@@ -687,7 +686,7 @@ class AdamWState(FsdpShardState):
         if sumsq is not None and max_norm is None:
             raise ValueError("clipping needs max_norm")
         _check(lib().zero_adamw_step(self._h, int(t), self._sum_ptr(sumsq),
-                                     float(max_norm or 0.0), self._stream(stream)))
+                                     float(max_norm or 0.0), _stream_handle(stream, self.device)))
 
     def step_sched(self, sumsq: Optional[torch.Tensor] = None,
                    max_norm: Optional[float] = None, stream=None):
@@ -696,7 +695,8 @@ class AdamWState(FsdpShardState):
         if sumsq is not None and max_norm is None:
             raise ValueError("clipping needs max_norm")
         _check(lib().zero_adamw_step_sched(self._h, self._sum_ptr(sumsq),
-                                           float(max_norm or 0.0), self._stream(stream)))
+                                           float(max_norm or 0.0),
+                                           _stream_handle(stream, self.device)))
 
     def state_tensors(self) -> dict:
         """The state itself, sharing the library's memory (until close()):

@@ -196,6 +196,7 @@ __device__ __forceinline__ void store_quad(void *base, int64_t i, int64_t left,
 // to be uniform costs a loop around every access).
 #define ZK_CONSTANT __attribute__((address_space(4)))
 typedef const ZK_CONSTANT AdamwTensor Tensor;
+typedef const ZK_CONSTANT AdamwGroup Group;
 
 template <class T>
 __device__ __forceinline__ const ZK_CONSTANT T *constant(const T *p) {
@@ -204,6 +205,7 @@ __device__ __forceinline__ const ZK_CONSTANT T *constant(const T *p) {
 
 struct KernelArgs {
     const AdamwTensor *table;
+    const AdamwGroup *groups;
     const int32_t *map;
     int n;
     AdamwStateRef st;
@@ -239,7 +241,7 @@ struct Uniform {
 };
 
 template <int NR>
-__device__ __forceinline__ bool uniforms(const KernelArgs &a, Tensor &tn, Uniform &u) {
+__device__ __forceinline__ bool uniforms(const KernelArgs &a, Group &gr, Uniform &u) {
     float clip;
     if (!clip_factor(a.sumsq, a.max_norm, clip)) return false;
     u.sc = a.sc;
@@ -250,8 +252,8 @@ __device__ __forceinline__ bool uniforms(const KernelArgs &a, Tensor &tn, Unifor
     }
     u.pow2 = NR > 0 ? (NR & (NR - 1)) == 0 : a.sc.n_pow2 != 0;
     u.scale = u.pow2 ? a.sc.inv_n * clip : clip;      // a power of two: the same bits
-    u.lr = u.sc.lr * tn.factor;
-    u.keep = 1.0f - u.lr * tn.decay;
+    u.lr = u.sc.lr * gr.factor;
+    u.keep = 1.0f - u.lr * gr.decay;
     return true;
 }
 
@@ -429,11 +431,12 @@ __device__ __forceinline__ void last32(const KernelArgs &a, Tensor &tn,
 template <int NR, bool GB, bool PB>
 __global__ void __launch_bounds__(kWave) adamw32_kernel(KernelArgs a) {
     const int64_t piece = blockIdx.x / kPieceWaves;
-    Tensor &tn = constant(a.table)[constant(a.map)[piece]];
+    const int k = constant(a.map)[piece];
+    Tensor &tn = constant(a.table)[k];
     const int64_t i0 = (piece - tn.piece0) * kAdamwPiece + (blockIdx.x % kPieceWaves) * kWaveElems;
     if (i0 >= tn.numel) return;
     Uniform u;
-    if (!uniforms<NR>(a, tn, u)) return;
+    if (!uniforms<NR>(a, constant(a.groups)[k], u)) return;
     const int64_t s0 = (int64_t)blockIdx.x * kWaveElems;
     const int lane = threadIdx.x;
     if (i0 + kWaveElems > tn.numel) {
@@ -689,11 +692,12 @@ __global__ void __launch_bounds__(kWave *kPieceWaves) adamw8_kernel(KernelArgs a
     const int64_t piece = blockIdx.x;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
     const int lane = threadIdx.x % kWave;
-    Tensor &tn = constant(a.table)[constant(a.map)[piece]];
+    const int k = constant(a.map)[piece];
+    Tensor &tn = constant(a.table)[k];
     const int64_t i0 = (piece - tn.piece0) * kAdamwPiece + wave * kWaveElems;
     if (i0 >= tn.numel) return;
     Uniform8 u;
-    if (!uniforms<NR>(a, tn, u)) return;
+    if (!uniforms<NR>(a, constant(a.groups)[k], u)) return;
     u.key = adamw_mix(a.seed ^ (a.sc_dev ? (uint32_t)(constant(a.ds)->t - 1) : a.t));
     u.lrc = u.lr * __builtin_amdgcn_rcpf(u.sc.bc1);      // 1 ulp, and so is the root
     u.rs = __builtin_amdgcn_rsqf(u.sc.bc2);
@@ -929,7 +933,7 @@ sumsq_kernel(const AdamwTensor *table, const int32_t *map,
 
 template <int NR, bool GB, bool PB>
 hipError_t launch_typed(const AdamwArgs &a, hipStream_t stream) {
-    KernelArgs k = {a.table, a.map, a.n, a.st, a.sc, a.sc_dev, a.ds, a.seed, a.t, a.sumsq,
+    KernelArgs k = {a.table, a.groups, a.map, a.n, a.st, a.sc, a.sc_dev, a.ds, a.seed, a.t, a.sumsq,
                     a.max_norm, a.stream_state ? 1 : 0};
     if (a.q8)
         hipLaunchKernelGGL((adamw8_kernel<NR, GB, PB>), dim3((unsigned)a.npieces),

@@ -52,15 +52,16 @@ struct zero_ctx {
     bool begun;
     // AdamW over many tensors (zero_adamw_init): state_bits 32 or 8, 0 on
     // other contexts. With 8 the moments are m8, r8 and scale, and m, v are
-    // null. aw_mem holds the device table of tensors, the piece-to-tensor
-    // map and the workspace of the sum of squares; aw_tensors mirrors the
-    // table on the host.
+    // null. aw_mem holds the device table of tensors, their groups, the
+    // piece-to-tensor map and the workspace of the sum of squares; aw_tensors
+    // mirrors the table on the host.
     int32_t state_bits;
     uint32_t sr_seed;            // mixed seed of the stochastic rounding
     uint8_t *m8, *r8, *scale;
     int64_t npieces;
     void *aw_mem;
     zk::AdamwTensor *aw_table;
+    zk::AdamwGroup *aw_groups;
     int32_t *aw_map;
     double *aw_partial;
     uint32_t *aw_done;
@@ -1125,12 +1126,15 @@ static int64_t round_up(int64_t x, int64_t to) { return (x + to - 1) / to * to; 
 static int alloc_adamw_table(zero_ctx *c) {
     const size_t nt = c->aw_tensors.size();
     const size_t table = (size_t)round_up((int64_t)(nt * sizeof(zk::AdamwTensor)), 256);
+    const size_t groups = (size_t)round_up((int64_t)(nt * sizeof(zk::AdamwGroup)), 256);
     const size_t map = (size_t)round_up(c->npieces * (int64_t)sizeof(int32_t), 256);
     const size_t partial = zk::kSumsqGroups * sizeof(double);
-    const size_t bytes = table + map + partial + 256;
+    const size_t bytes = table + groups + map + partial + 256;
     std::vector<int32_t> host_map;
+    std::vector<zk::AdamwGroup> host_groups;
     try {
         host_map.resize((size_t)c->npieces);
+        host_groups.assign(nt, {0.0f, 1.0f});
     } catch (...) {
         return fail(ZERO_ENOMEM, "host allocation failed");
     }
@@ -1147,12 +1151,16 @@ static int alloc_adamw_table(zero_ctx *c) {
     }
     char *base = (char *)c->aw_mem;
     c->aw_table = (zk::AdamwTensor *)base;
-    c->aw_map = (int32_t *)(base + table);
-    c->aw_partial = (double *)(base + table + map);
-    c->aw_done = (uint32_t *)(base + table + map + partial);
+    c->aw_groups = (zk::AdamwGroup *)(base + table);
+    c->aw_map = (int32_t *)(base + table + groups);
+    c->aw_partial = (double *)(base + table + groups + map);
+    c->aw_done = (uint32_t *)(base + table + groups + map + partial);
     e = hipMemset(c->aw_mem, 0, bytes);
     if (e == hipSuccess)
         e = hipMemcpy(c->aw_table, c->aw_tensors.data(), nt * sizeof(zk::AdamwTensor),
+                      hipMemcpyHostToDevice);
+    if (e == hipSuccess)
+        e = hipMemcpy(c->aw_groups, host_groups.data(), nt * sizeof(zk::AdamwGroup),
                       hipMemcpyHostToDevice);
     if (e == hipSuccess && c->npieces > 0)
         e = hipMemcpy(c->aw_map, host_map.data(), (size_t)c->npieces * sizeof(int32_t),
@@ -1245,8 +1253,6 @@ int zero_adamw_init(int32_t ntensors, const int64_t *dim0, const int64_t *row_nu
         a = {};
         a.numel = t.rows * t.row_numel;
         a.piece0 = piece;
-        a.decay = 0.0f;
-        a.factor = 1.0f;
         const int64_t np = a.numel / zk::kAdamwPiece + (a.numel % zk::kAdamwPiece != 0 ? 1 : 0);
         if (np > zk::kAdamwMaxPieces - piece) {
             delete c;
@@ -1275,20 +1281,17 @@ static int need_adamw(const zero_ctx *c) {
     return ZERO_OK;
 }
 
-// The host's table to the device, stream-ordered, carried by kernel
+// `words` 32-bit words to device memory, stream-ordered, carried by kernel
 // arguments: no staging buffer that the call would have to keep.
-static int upload_table(zero_ctx *c, const std::vector<zk::AdamwTensor> &tab, hipStream_t stream) {
-    static_assert(sizeof(zk::AdamwTensor) % sizeof(uint32_t) == 0, "whole words");
+static int upload_words(const zero_ctx *c, void *dst, const void *src, size_t words,
+                        hipStream_t stream) {
     DeviceGuard g(c->device);
     if (g.error() != hipSuccess) return hip_fail(g.error(), "hipSetDevice");
-    const size_t words = tab.size() * sizeof(zk::AdamwTensor) / sizeof(uint32_t);
-    const char *src = (const char *)tab.data();
-    uint32_t *dst = (uint32_t *)c->aw_table;
     zk::WordChunk chunk;
     for (size_t done = 0; done < words; done += (size_t)chunk.n) {
         chunk.n = (int)(words - done < (size_t)zk::kWordChunk ? words - done : zk::kWordChunk);
-        std::memcpy(chunk.w, src + done * sizeof(uint32_t), (size_t)chunk.n * sizeof(uint32_t));
-        hipError_t e = zk::launch_fill_words(dst + done, chunk, stream);
+        std::memcpy(chunk.w, (const uint32_t *)src + done, (size_t)chunk.n * sizeof(uint32_t));
+        hipError_t e = zk::launch_fill_words((uint32_t *)dst + done, chunk, stream);
         if (e != hipSuccess) return hip_fail(e, "uploading the tensor table");
     }
     return ZERO_OK;
@@ -1298,24 +1301,21 @@ int zero_adamw_groups(zero_ctx *c, const double *weight_decay, const double *lr_
                       hipStream_t stream) {
     int rc = need_adamw(c);
     if (rc) return rc;
-    std::vector<zk::AdamwTensor> tab;
+    std::vector<zk::AdamwGroup> groups;
     try {
-        tab = c->aw_tensors;
+        groups.resize(c->tensors.size());
     } catch (...) {
         return fail(ZERO_ENOMEM, "host allocation failed");
     }
-    for (size_t k = 0; k < tab.size(); ++k) {
+    for (size_t k = 0; k < groups.size(); ++k) {
         const double d = weight_decay ? weight_decay[k] : 0.0, f = lr_scale ? lr_scale[k] : 1.0;
-        if (!std::isfinite(d) || d < 0.0 || !std::isfinite(f))
+        if (!std::isfinite((float)d) || d < 0.0 || !std::isfinite((float)f))
             return fail(ZERO_EINVAL, "tensor %zu: weight decay must be finite and >= 0 and the "
                                      "learning-rate scale finite (got %g, %g)", k, d, f);
-        tab[k].decay = (float)d;
-        tab[k].factor = (float)f;
+        groups[k] = {(float)d, (float)f};
     }
-    rc = upload_table(c, tab, stream);
-    if (rc) return rc;
-    c->aw_tensors.swap(tab);
-    return ZERO_OK;
+    return upload_words(c, c->aw_groups, groups.data(),
+                        groups.size() * sizeof(zk::AdamwGroup) / sizeof(uint32_t), stream);
 }
 
 int zero_adamw_bind(zero_ctx *c, const void *const *grads, int32_t n_replicas,
@@ -1365,7 +1365,8 @@ int zero_adamw_bind(zero_ctx *c, const void *const *grads, int32_t n_replicas,
         if (rc) return rc;
         t.out = params_out[k];
     }
-    rc = upload_table(c, tab, stream);
+    rc = upload_words(c, c->aw_table, tab.data(),
+                      tab.size() * sizeof(zk::AdamwTensor) / sizeof(uint32_t), stream);
     if (rc) return rc;
     c->aw_tensors.swap(tab);
     c->aw_n = n_replicas;
@@ -1423,6 +1424,7 @@ static int adamw_step(zero_ctx *c, int64_t t, StepMode mode, const double *sumsq
     }
     zk::AdamwArgs a = {};
     a.table = c->aw_table;
+    a.groups = c->aw_groups;
     a.map = c->aw_map;
     a.npieces = c->npieces;
     a.n = c->aw_n;

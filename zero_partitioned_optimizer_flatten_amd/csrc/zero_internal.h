@@ -134,6 +134,9 @@ struct AdamwTensor {
     void *out;                              // this rank's output elements
     int64_t numel;                          // local elements
     int64_t piece0;                         // first piece in the state
+};
+// Apart from the pointers, so that setting the one never rewrites the other.
+struct AdamwGroup {
     float decay;                            // decoupled weight decay
     float factor;                           // of the learning rate
 };
@@ -147,6 +150,7 @@ struct AdamwStateRef {
 
 struct AdamwArgs {
     const AdamwTensor *table;
+    const AdamwGroup *groups;
     const int32_t *map;           // piece -> tensor
     int64_t npieces;
     int n;
