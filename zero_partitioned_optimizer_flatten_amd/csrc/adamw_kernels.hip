@@ -294,9 +294,10 @@ constexpr int kGroup = 8;
 template <int NR> constexpr bool kLateMaster = NR >= 2;
 
 // Mean gradients of a lane's quads in a full part (element i0 of the tensor
-// onwards). `first` runs once the first group's loads are on their way.
+// onwards). `first` runs once the first group's loads are on their way: it
+// issues the state's, works out u, and says whether the step takes place.
 template <int NR, bool GB, bool AL, class F>
-__device__ __forceinline__ void mean_full(Tensor &tn, int nrep, const Uniform &u,
+__device__ __forceinline__ bool mean_full(Tensor &tn, int nrep, const Uniform &u,
                                           int64_t i0, int lane, float (&g)[kSplit][kQuad],
                                           F &&first) {
     const int n = NR > 0 ? NR : nrep;
@@ -314,7 +315,7 @@ __device__ __forceinline__ void mean_full(Tensor &tn, int nrep, const Uniform &u
                     raw[k][h] = load_raw<GB, AL, AL ? kPolNT : kPolDefault>(
                         base, kQuad * (lane + h * kWave));
             }
-        if (q0 == 0) first();
+        if (q0 == 0 && !first()) return false;
 #pragma unroll
         for (int k = 0; k < grp; ++k)
             if (NR > 0 || q0 + k < n) {
@@ -330,14 +331,7 @@ __device__ __forceinline__ void mean_full(Tensor &tn, int nrep, const Uniform &u
     }
 #pragma unroll
     for (int h = 0; h < kSplit; ++h) mean_clip(u, g[h]);
-}
-
-// Whether every stream of a part is aligned for whole-quad instructions.
-template <bool GB>
-__device__ __forceinline__ bool aligned_grads(Tensor &tn, int n) {
-    uintptr_t bits = 0;
-    for (int q = 0; q < n; ++q) bits |= (uintptr_t)tn.grads[q] % (GB ? 8 : 16);
-    return bits == 0;
+    return true;
 }
 
 // Elements before the first at which every replica's quads are aligned, -1
@@ -351,9 +345,19 @@ __device__ __forceinline__ int common_head(Tensor &tn, int n) {
     return (kQuad - phase) % kQuad;
 }
 
-template <bool GB, bool PB>
-__device__ __forceinline__ bool aligned_part(Tensor &tn, int n) {
-    return (uintptr_t)tn.out % (PB ? 8 : 16) == 0 && aligned_grads<GB>(tn, n);
+// Whether every stream of a part is aligned for whole-quad instructions. The
+// group's values are asked for here as well, so that everything the table
+// holds comes in one round trip: left to the branches that use it, it would
+// come in a further one before the first gradient is asked for.
+template <int NR, bool GB, bool PB>
+__device__ __forceinline__ bool aligned_part(Tensor &tn, Group &gr, int nrep) {
+    const int n = NR > 0 ? NR : nrep;
+    uint32_t bits = (uint32_t)(uintptr_t)tn.out & (PB ? 7u : 15u);
+    for (int q = 0; q < n; ++q) bits |= (uint32_t)(uintptr_t)tn.grads[q] & (GB ? 7u : 15u);
+    asm volatile(""
+                 : "+s"(bits)
+                 : "s"(gr.decay), "s"(gr.factor), "s"(tn.numel), "s"(tn.piece0));
+    return bits == 0;
 }
 
 // ------------------------------------------------------------ 32-bit states
@@ -365,13 +369,14 @@ __device__ __forceinline__ float moments32(float g, float &m, float &v, const Un
 }
 
 template <int NR, bool GB, bool PB, bool AL>
-__device__ __forceinline__ void full32(const KernelArgs &a, Tensor &tn,
-                                       const Uniform &u, int64_t i0, int64_t s0, int lane) {
+__device__ __forceinline__ void full32(const KernelArgs &a, Tensor &tn, Group &gr, int64_t i0,
+                                       int64_t s0, int lane) {
+    Uniform u;
     const span_t sp = span_of(a.st.master + s0, kWaveElems * 4);
     const span_t sm = span_of(a.st.m + s0, kWaveElems * 4);
     const span_t sv = span_of(a.st.v + s0, kWaveElems * 4);
     float g[kSplit][kQuad], p[kSplit][kQuad], m[kSplit][kQuad], v[kSplit][kQuad];
-    mean_full<NR, GB, AL>(tn, a.n, u, i0, lane, g, [&] {
+    const bool go = mean_full<NR, GB, AL>(tn, a.n, u, i0, lane, g, [&] {
 #pragma unroll
         for (int h = 0; h < kSplit; ++h) {
             const int off = kQuad * (lane + h * kWave);
@@ -380,7 +385,9 @@ __device__ __forceinline__ void full32(const KernelArgs &a, Tensor &tn,
             if (!kLateMaster<NR>) load_f4<kPolNT>(sp, off, p[h]);
         }
         __builtin_amdgcn_sched_barrier(0);
+        return uniforms<NR>(a, gr, u);
     });
+    if (!go) return;
     float d[kSplit][kQuad];
 #pragma unroll
     for (int h = 0; h < kSplit; ++h)
@@ -414,8 +421,10 @@ __device__ __forceinline__ void full32(const KernelArgs &a, Tensor &tn,
 
 // The part a tensor ends in.
 template <int NR, bool GB, bool PB>
-__device__ __forceinline__ void last32(const KernelArgs &a, Tensor &tn,
-                                       const Uniform &u, int64_t i0, int64_t s0, int lane) {
+__device__ __forceinline__ void last32(const KernelArgs &a, Tensor &tn, Group &gr, int64_t i0,
+                                       int64_t s0, int lane) {
+    Uniform u;
+    if (!uniforms<NR>(a, gr, u)) return;
 #pragma unroll 1
     for (int h = 0; h < kSplit; ++h) {
         const int off = kQuad * (lane + h * kWave);
@@ -446,19 +455,15 @@ __global__ void __launch_bounds__(kWave) adamw32_kernel(KernelArgs a) {
     const int64_t piece = blockIdx.x / kPieceWaves;
     const int k = constant(a.map)[piece];
     Tensor &tn = constant(a.table)[k];
+    Group &gr = constant(a.groups)[k];
+    const bool al = aligned_part<NR, GB, PB>(tn, gr, a.n);
     const int64_t i0 = (piece - tn.piece0) * kAdamwPiece + (blockIdx.x % kPieceWaves) * kWaveElems;
-    if (i0 >= tn.numel) return;
-    Uniform u;
-    if (!uniforms<NR>(a, constant(a.groups)[k], u)) return;
     const int64_t s0 = (int64_t)blockIdx.x * kWaveElems;
     const int lane = threadIdx.x;
-    if (i0 + kWaveElems > tn.numel) {
-        last32<NR, GB, PB>(a, tn, u, i0, s0, lane);
-    } else if (aligned_part<GB, PB>(tn, NR > 0 ? NR : a.n)) {
-        full32<NR, GB, PB, true>(a, tn, u, i0, s0, lane);
-    } else {
-        full32<NR, GB, PB, false>(a, tn, u, i0, s0, lane);
-    }
+    if (i0 >= tn.numel) return;
+    if (i0 + kWaveElems > tn.numel) last32<NR, GB, PB>(a, tn, gr, i0, s0, lane);
+    else if (al) full32<NR, GB, PB, true>(a, tn, gr, i0, s0, lane);
+    else full32<NR, GB, PB, false>(a, tn, gr, i0, s0, lane);
 }
 
 // ------------------------------------------------------------- 8-bit states
@@ -543,6 +548,15 @@ struct Uniform8 : Uniform {
     uint32_t key;
 };
 
+template <int NR>
+__device__ __forceinline__ bool uniforms8(const KernelArgs &a, Group &gr, Uniform8 &u) {
+    if (!uniforms<NR>(a, gr, u)) return false;
+    u.key = adamw_mix(a.seed ^ (a.sc_dev ? (uint32_t)(constant(a.ds)->t - 1) : a.t));
+    u.lrc = u.lr * __builtin_amdgcn_rcpf(u.sc.bc1);      // 1 ulp, and so is the root
+    u.rs = __builtin_amdgcn_rsqf(u.sc.bc2);
+    return true;
+}
+
 // sqrt(v) from the hardware's reciprocal root (1 ulp) and one Newton step whose
 // residue is exact: correctly rounded but for about one v in 2^21, off by one
 // ulp there. A v below 2^-126 (gradients under 1e-18) gives less than its
@@ -601,14 +615,14 @@ __device__ __forceinline__ uint64_t nan_lanes(const float (&d)[kQuad]) {
 }
 
 template <int NR, bool GB, bool PB, bool AL>
-__device__ __forceinline__ void full8(const KernelArgs &a, Tensor &tn,
-                                      const Uniform8 &u, int64_t i0, int64_t s0, uint8_t *scale,
-                                      int lane) {
+__device__ __forceinline__ void full8(const KernelArgs &a, Tensor &tn, Group &gr, int64_t i0,
+                                      int64_t s0, uint8_t *scale, int lane) {
+    Uniform8 u;
     const span_t sp = span_of(a.st.master + s0, kWaveElems * 4);
     const span_t sm = span_of(a.st.m8 + s0, kWaveElems), sr = span_of(a.st.r8 + s0, kWaveElems);
     float g[kSplit][kQuad], p[kSplit][kQuad], m[kSplit][kQuad], r[kSplit][kQuad];
     uint32_t cm[kSplit], cr[kSplit], em[kSplit], er[kSplit];
-    mean_full<NR, GB, AL>(tn, a.n, u, i0, lane, g, [&] {
+    const bool go = mean_full<NR, GB, AL>(tn, a.n, u, i0, lane, g, [&] {
 #pragma unroll
         for (int h = 0; h < kSplit; ++h) {
             const int off = kQuad * (lane + h * kWave);
@@ -619,7 +633,9 @@ __device__ __forceinline__ void full8(const KernelArgs &a, Tensor &tn,
             if (!kLateMaster<NR>) load_f4<kPolNT>(sp, off, p[h]);
         }
         __builtin_amdgcn_sched_barrier(0);
+        return uniforms8<NR>(a, gr, u);
     });
+    if (!go) return;
     float d[kSplit][kQuad];
     uint64_t bad = 0;
 #pragma unroll
@@ -674,9 +690,10 @@ __device__ __forceinline__ void full8(const KernelArgs &a, Tensor &tn,
 // The part a tensor ends in: what is behind the last element reads as zero
 // and stays zero.
 template <int NR, bool GB, bool PB>
-__device__ __forceinline__ void last8(const KernelArgs &a, Tensor &tn,
-                                      const Uniform8 &u, int64_t i0, int64_t s0, uint8_t *scale,
-                                      int lane) {
+__device__ __forceinline__ void last8(const KernelArgs &a, Tensor &tn, Group &gr, int64_t i0,
+                                      int64_t s0, uint8_t *scale, int lane) {
+    Uniform8 u;
+    if (!uniforms8<NR>(a, gr, u)) return;
 #pragma unroll 1
     for (int h = 0; h < kSplit; ++h) {
         const int off = kQuad * (lane + h * kWave);
@@ -712,22 +729,15 @@ __global__ void __launch_bounds__(kWave *kPieceWaves) adamw8_kernel(KernelArgs a
     const int lane = threadIdx.x % kWave;
     const int k = constant(a.map)[piece];
     Tensor &tn = constant(a.table)[k];
+    Group &gr = constant(a.groups)[k];
+    const bool al = aligned_part<NR, GB, PB>(tn, gr, a.n);
     const int64_t i0 = (piece - tn.piece0) * kAdamwPiece + wave * kWaveElems;
-    if (i0 >= tn.numel) return;
-    Uniform8 u;
-    if (!uniforms<NR>(a, constant(a.groups)[k], u)) return;
-    u.key = adamw_mix(a.seed ^ (a.sc_dev ? (uint32_t)(constant(a.ds)->t - 1) : a.t));
-    u.lrc = u.lr * __builtin_amdgcn_rcpf(u.sc.bc1);      // 1 ulp, and so is the root
-    u.rs = __builtin_amdgcn_rsqf(u.sc.bc2);
     const int64_t s0 = piece * kAdamwPiece + wave * kWaveElems;
     uint8_t *scale = a.st.scale + piece * (2 * kAdamwScales) + wave * (kWaveElems / kAdamwBlock);
-    if (i0 + kWaveElems > tn.numel) {
-        last8<NR, GB, PB>(a, tn, u, i0, s0, scale, lane);
-    } else if (aligned_part<GB, PB>(tn, NR > 0 ? NR : a.n)) {
-        full8<NR, GB, PB, true>(a, tn, u, i0, s0, scale, lane);
-    } else {
-        full8<NR, GB, PB, false>(a, tn, u, i0, s0, scale, lane);
-    }
+    if (i0 >= tn.numel) return;
+    if (i0 + kWaveElems > tn.numel) last8<NR, GB, PB>(a, tn, gr, i0, s0, scale, lane);
+    else if (al) full8<NR, GB, PB, true>(a, tn, gr, i0, s0, scale, lane);
+    else full8<NR, GB, PB, false>(a, tn, gr, i0, s0, scale, lane);
 }
 
 // m and v = r*r of a piece in fp32 (r has four significant bits, so its
