@@ -1129,7 +1129,9 @@ static int alloc_adamw_table(zero_ctx *c) {
     const size_t groups = (size_t)round_up((int64_t)(nt * sizeof(zk::AdamwGroup)), 256);
     const size_t map = (size_t)round_up(c->npieces * (int64_t)sizeof(int32_t), 256);
     const size_t partial = zk::kSumsqGroups * sizeof(double);
-    const size_t bytes = table + groups + map + partial + 256;
+    const size_t counters =
+        (zk::kSumsqCounters + 1) * zk::kSumsqCounterWords * sizeof(uint32_t);
+    const size_t bytes = table + groups + map + partial + counters;
     std::vector<int32_t> host_map;
     std::vector<zk::AdamwGroup> host_groups;
     try {

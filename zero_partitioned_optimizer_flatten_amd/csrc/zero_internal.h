@@ -172,6 +172,10 @@ hipError_t launch_adamw(const AdamwArgs &a, hipStream_t stream);
 // in flight: 480 us for 3.4 GB of fp32 gradients against 495 at three per
 // unit, 520 at four and 533 at eight.
 constexpr int kSumsqGroups = 512;
+// Finished workgroups are counted on one of kSumsqCounters counters each, and
+// full counters on one more, every one on a cache line of its own.
+constexpr int kSumsqCounters = 16;
+constexpr int kSumsqCounterWords = 32;
 struct SumsqArgs {
     const AdamwTensor *table;
     const int32_t *map;
@@ -179,7 +183,7 @@ struct SumsqArgs {
     int n;
     bool grad_bf16;
     double *partial;              // kSumsqGroups
-    uint32_t *done;               // workgroups done, 0 between launches
+    uint32_t *done;               // the counters, 0 between launches
     double *out;
 };
 hipError_t launch_sumsq(const SumsqArgs &a, hipStream_t stream);
