@@ -276,9 +276,23 @@ def test_sumsq(n, gdt, gap):
     j.close()
 
 
+@pytest.mark.parametrize("pieces", [1, 3, 4, 5, 17, 63, 64, 65, 68, 1000, 2044, 2049])
+def test_sumsq_for_every_number_of_workgroups(pieces):
+    """One to 512 workgroups of four pieces each, more than once: the last one
+    to finish is found whatever their number, and the count starts anew."""
+    j = Job([(2048 * pieces - 5,)], 1, 0, 1, torch.bfloat16, torch.float32, 32, 1, seed=pieces,
+            outs=False)
+    j.fill()
+    x = _f64(j.grads[0][0])
+    want = math.fsum(x * x)
+    for _ in range(4):
+        assert abs(j.st.sumsq().item() / want - 1) <= _sum_bound([x], x.size)
+    j.close()
+
+
 def test_sumsq_of_a_long_list_and_of_large_and_small_numbers():
     """More pieces than workgroups, and squares that leave binary32."""
-    shapes = [(2048 * 2500 + 77,), (3, 5)]
+    shapes = [(2048 * 2500 + 77,), (3, 5)]      # 2501 pieces, 2048 waves
     j = Job(shapes, 1, 0, 1, torch.float32, torch.float32, 32, 1, outs=False)
     for std in (1.0, 1e30, 1e-30):
         j.fill(std)
@@ -590,6 +604,58 @@ def test_a_new_state_on_a_stream_of_its_own(state_bits):
     assert all(torch.equal(x, y) for x, y in zip(a, b))
     for st in states:
         st.close()
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("world,rank", [(3, 1), (64, 2)])
+def test_load_master_takes_this_ranks_rows(state_bits, dtype, world, rank):
+    """From whole parameters of either dtype (and of a world past the replica
+    limit), one element off alignment; the moments start at zero again."""
+    shapes = [(130, 7), (5,), (64, 2), (2049,)]
+    st = zero.AdamWState(shapes, world, rank, LR, state_bits=state_bits)
+    p = [torch.randn(math.prod(s) + 1, device="cuda").to(dtype)[1:].view(s) for s in shapes]
+    full = torch.randn(st.shard, device="cuda")
+    keep = torch.zeros(st.shard, device="cuda")
+    for k in range(4):
+        keep[st.local[k][2]:st.local[k][2] + st.local_numel(k)] = 1
+    st.set_state(full * keep, full * keep, (full * keep).square())
+    st.load_master(p)
+    master, m, v = st.get_state()
+    for k, x in enumerate(p):
+        first, rows, off = st.local[k]
+        assert torch.equal(master[off:off + st.local_numel(k)], x[first:first + rows].float().view(-1))
+    assert not m.any() and not v.any() and not master[keep == 0].any()
+    st.close()
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
+def test_two_states_at_once(state_bits):
+    """Two contexts on two streams, their launches interleaved, against the
+    same calls one after the other."""
+    shapes = [(700_000,), (3, 1001)]
+    jobs = [Job(shapes, 1, 0, 1, torch.bfloat16, torch.bfloat16, state_bits, 1, seed=k // 2)
+            for k in range(4)]
+    for j in jobs:
+        j.fill()
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    sums = [torch.zeros(1, dtype=torch.float64, device="cuda") for _ in range(4)]
+    torch.cuda.synchronize()
+    for t in range(1, 21):
+        for k, stream in enumerate(streams):              # jobs 0 and 2 at once
+            jobs[2 * k].st.sumsq(out=sums[2 * k], stream=stream)
+            jobs[2 * k].st.step(t, sumsq=sums[2 * k], max_norm=0.1, stream=stream)
+    torch.cuda.synchronize()
+    for k in (1, 3):                                      # 1 and 3 alone
+        for t in range(1, 21):
+            jobs[k].st.sumsq(out=sums[k])
+            jobs[k].st.step(t, sumsq=sums[k], max_norm=0.1)
+        torch.cuda.synchronize()
+        assert sums[k].item() == sums[k - 1].item()
+        assert all(np.array_equal(x, y) for x, y in zip(jobs[k].raw(), jobs[k - 1].raw()))
+    for j in jobs:
+        j.close()
 
 
 def test_the_same_gradient_bound_twice():
