@@ -356,6 +356,30 @@ def test_one_bad_gradient_spoils_its_own_element_alone(state_bits, bad):
         j.close()
 
 
+def test_a_stored_moment_at_the_end_of_the_range_stays_alone():
+    """m near the largest binary32 rounds to a code whose value is infinite:
+    its neighbours keep their codes' values."""
+    st = zero.AdamWState([(4096,)], 1, 0, LR, BETAS, EPS, state_bits=8)
+    g = torch.zeros(4096, device="cuda")
+    out = torch.zeros(4096, device="cuda")
+    m = torch.full((4096,), 1e-3, device="cuda")
+    v = torch.full((4096,), 1e-6, device="cuda")
+    m[7] = torch.finfo(torch.float32).max
+    st.set_state(torch.zeros(4096, device="cuda"), m, v)
+    st.bind([[g]], [out])
+    st.state_tensors()["m"].view(torch.uint8)[:32] = 0x38          # 1.0 each
+    st.state_tensors()["m"].view(torch.uint8)[7] = 0x7E            # 448 * 2^120: infinite
+    st.state_tensors()["scale"].view(torch.uint8)[0, 0, 0] = 247
+    st.step(1)
+    _, m2, _ = st.get_state()
+    assert not math.isfinite(m2[7].item())
+    want = np.float32(2.0 ** 120) * np.float32(BETAS[0])           # the others decay
+    got = m2[:32].cpu().numpy()
+    # a code is at most a step, an eighth of its octave, off
+    assert (np.abs(np.delete(got, 7) / want - 1) <= 0.125).all()
+    st.close()
+
+
 @pytest.mark.parametrize("state_bits", [32, 8])
 def test_zero_gradients_and_large_ones(state_bits):
     """All zero (masters move by decay alone, and 8-bit blocks are zero), then
