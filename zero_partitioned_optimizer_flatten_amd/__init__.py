@@ -133,10 +133,7 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], device: torch.device) ->
 
 
 def _ptr_array(ptrs: Sequence[int]):
-    arr = (ctypes.c_void_p * max(1, len(ptrs)))()
-    for i, p in enumerate(ptrs):
-        arr[i] = p
-    return arr
+    return (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs)
 
 
 def shard_geometry(numel: int, world: int, rank: int) -> Tuple[int, int, int]:
@@ -592,6 +589,12 @@ class AdamWState(FsdpShardState):
         self._h = h
         self._bound = None
         self._read_layout()
+        # (elements of this rank, of the parameter, before this rank's first)
+        self._sizes = []
+        for k, (first, rows, _) in enumerate(self.local):
+            local = self.local_numel(k)
+            self._sizes.append((local, int(torch.Size(self.shapes[k]).numel()),
+                                first * (local // rows) if rows else 0))
         self.set_groups(weight_decay, lr_scale)
         torch.cuda.current_stream(self.device).synchronize()    # for calls on any stream
 
@@ -607,23 +610,27 @@ class AdamWState(FsdpShardState):
             arrays.append((ctypes.c_double * max(1, n))(*x))
         _check(lib().zero_adamw_groups(self._h, *arrays, _stream_handle(stream, self.device)))
 
-    def _local_ptr(self, x: Optional[torch.Tensor], k: int, what: str, whole: bool) -> int:
-        """Address of this rank's elements of parameter k in x, which holds
-        these alone or, for a gradient (`whole`), the whole parameter."""
-        local = self.local_numel(k)
-        if local == 0:
-            return 0
-        if x is None:
-            raise ValueError(f"{what} is None but this rank holds rows of it")
-        self._dev(x, what)
-        full = int(torch.Size(self.shapes[k]).numel())
-        if x.numel() == local:
-            return x.data_ptr()
-        if whole and x.numel() == full:
-            first, rows, _ = self.local[k]
-            return x.data_ptr() + first * (local // rows) * x.element_size()
-        raise ValueError(f"{what} has {x.numel()} elements, need {local}"
-                         + (f" (this rank's) or {full}" if whole else ""))
+    def _pointers(self, xs: Sequence[Optional[torch.Tensor]], what: str, whole: bool) -> list:
+        """Addresses of this rank's elements of every parameter in xs, whose
+        tensors hold these alone or, for gradients (`whole`), the parameter."""
+        ptrs = []
+        for k, (x, (local, full, first)) in enumerate(zip(xs, self._sizes)):
+            if local == 0:
+                ptrs.append(0)
+                continue
+            if x is None:
+                raise ValueError(f"{what}[{k}] is None but this rank holds rows of it")
+            if x.device != self.device or not x.is_contiguous():
+                self._dev(x, f"{what}[{k}]")
+            n = x.numel()
+            if n == local:
+                ptrs.append(x.data_ptr())
+            elif whole and n == full:
+                ptrs.append(x.data_ptr() + first * x.element_size())
+            else:
+                raise ValueError(f"{what}[{k}] has {n} elements, need {local}"
+                                 + (f" (this rank's) or {full}" if whole else ""))
+        return ptrs
 
     def bind(self, grads: Sequence[Sequence[Optional[torch.Tensor]]],
              params_out: Optional[Sequence[Optional[torch.Tensor]]] = None, stream=None):
@@ -641,16 +648,16 @@ class AdamWState(FsdpShardState):
                 raise ValueError(f"grads[{q}]: need {n} tensors, got {len(gl)}")
         if params_out is not None and len(params_out) != n:
             raise ValueError(f"params_out: need {n} tensors, got {len(params_out)}")
-        held = [k for k in range(n) if self.local_numel(k)]
+        held = [k for k in range(n) if self._sizes[k][0]]
         gdts = {gl[k].dtype for gl in grads for k in held if gl[k] is not None}
         pdts = {params_out[k].dtype for k in held if params_out[k] is not None} \
             if params_out is not None else set()
         if len(gdts) > 1 or len(pdts) > 1:
             raise TypeError("gradients must share one dtype, and outputs one")
-        gptrs = _ptr_array([self._local_ptr(gl[k], k, f"grads[{q}][{k}]", True)
-                            for q, gl in enumerate(grads) for k in range(n)])
+        gptrs = _ptr_array([p for q, gl in enumerate(grads)
+                            for p in self._pointers(gl, f"grads[{q}]", True)])
         optrs = None if params_out is None else _ptr_array(
-            [self._local_ptr(x, k, f"params_out[{k}]", False) for k, x in enumerate(params_out)])
+            self._pointers(params_out, "params_out", False))
         gdt = _dtype_code(gdts.pop()) if gdts else ZERO_F32
         pdt = _dtype_code(pdts.pop()) if pdts else ZERO_F32
         _check(lib().zero_adamw_bind(self._h, gptrs, len(grads), gdt, optrs, pdt,
