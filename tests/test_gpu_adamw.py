@@ -276,6 +276,36 @@ def test_sumsq(n, gdt, gap):
     j.close()
 
 
+@pytest.mark.parametrize("n", [1, 3, 9])
+@pytest.mark.parametrize("gdt", [torch.bfloat16, torch.float32])
+def test_sumsq_of_every_last_piece(n, gdt):
+    """Rows of 256 elements, 4, 2 and 1 at a time, and a last one in part:
+    every combination, in tensors of less and of more than a piece."""
+    ends = [256 * r + d for r in range(8) for d in (1, 3, 4, 129, 254, 255, 256)]
+    for gap in (1, 4):
+        for first in (0, 2048):
+            j = Job([(first + e,) for e in ends], 1, 0, n, gdt, torch.float32, 32, gap,
+                    seed=first + gap, outs=False)
+            j.fill()
+            for f in j.gflat:
+                f[torch.from_numpy(~j.inside).cuda()] = float("nan")
+            reps = [np.concatenate([_f64(g) for g in gl]) for gl in j.grads]
+            mean = sum(reps) / n
+            mass = sum(np.abs(r) for r in reps) / n
+            got = j.st.sumsq().item()
+            assert (abs(got - math.fsum(mean * mean))
+                    <= _sum_bound(reps, mean.size) * math.fsum(mass * mass))
+            # one tensor's elements alone, so that none hides in the others' sum
+            # (a sum of ones is exact; the mean's square rounds a few times by 2^-53)
+            for k in range(0, len(ends), 5):
+                for f in j.gflat:
+                    f[torch.from_numpy(j.inside).cuda()] = 0.0
+                for gl in j.grads:
+                    gl[k].fill_(1.0)
+                assert j.st.sumsq().item() == pytest.approx(first + ends[k], rel=1e-12)
+            j.close()
+
+
 @pytest.mark.parametrize("pieces", [1, 3, 4, 5, 17, 63, 64, 65, 68, 1000, 2044, 2049])
 def test_sumsq_for_every_number_of_workgroups(pieces):
     """One to 512 workgroups of four pieces each, more than once: the last one
