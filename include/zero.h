@@ -413,10 +413,10 @@ int zero_adamw_init(int32_t ntensors, const int64_t *dim0,
                     int32_t state_bits, uint32_t seed, zero_ctx **out);
 
 /* Weight decay and learning-rate scale per tensor (host arrays of ntensors;
- * NULL: 0, or 1, for all), rounded to fp32 (and finite there), for the steps after it on the
- * stream; a captured step takes what holds when it replays. EINVAL: not an
- * AdamW context, a decay that is negative or not finite, a scale that is not
- * finite. */
+ * NULL: 0, or 1, for all), rounded to fp32 (and finite there), for the steps
+ * after it on the stream; a captured step takes what holds when it replays.
+ * EINVAL: not an AdamW context, a decay that is negative or not finite, a
+ * scale that is not finite. */
 int zero_adamw_groups(zero_ctx *ctx, const double *weight_decay,
                       const double *lr_scale, hipStream_t stream);
 
