@@ -399,8 +399,9 @@ int zero_fsdp_step_sched(zero_ctx *ctx, const void *const *grads,
  * learning-rate scale at 1 for every tensor.
  * zero_fsdp_local, zero_fsdp_load_master, zero_set_lr, the schedule calls,
  * zero_get_state / zero_set_state, zero_shard_state_bytes and zero_destroy
- * apply; zero_fsdp_step does with 32 bits only. zero_get_state gives m and v
- * of 8-bit states in fp32 exactly; zero_set_state rounds them to the nearest
+ * apply; zero_fsdp_step and zero_fsdp_step_sched do with 32 bits and a world
+ * of up to ZERO_FSDP_MAX_WORLD (EUNSUPPORTED above). zero_get_state gives m and
+ * v of 8-bit states in fp32 exactly; zero_set_state rounds them to the nearest
  * codes, which leaves values that came from zero_get_state unchanged, except
  * a v below 2^-126, whose root fp32 cannot hold the square of. What is behind
  * a tensor's last element must be zero in what zero_set_state gets.

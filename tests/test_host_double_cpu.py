@@ -1,0 +1,62 @@
+"""The library's host side without a GPU: calls that need a context, and what
+they hand to the kernels. Each call runs in a process of its own, so that one
+that overruns its stack ends that process alone."""
+import os
+import subprocess
+import sys
+
+import pytest
+
+import host_double
+
+TESTS = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(TESTS)
+
+pytestmark = pytest.mark.skipif(not host_double.available(), reason="g++ or the HIP headers missing")
+
+
+@pytest.fixture(scope="module")
+def so(tmp_path_factory):
+    return host_double.build(str(tmp_path_factory.mktemp("host")))
+
+
+def run(so, body):
+    """The lines that `body` prints; H is the library."""
+    script = (f"import sys; sys.path[:0] = [{ROOT!r}, {TESTS!r}]\n"
+              "import ctypes, host_double\n"
+              "import zero_partitioned_optimizer_flatten_amd as zero\n"
+              f"H = host_double.Host({so!r}); L = H.L\n" + body)
+    r = subprocess.run([sys.executable, "-c", script], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, (r.returncode, r.stderr[-2000:])
+    return r.stdout.splitlines()
+
+
+# --------------------------------------- the per-parameter step on AdamW's states
+
+PER_PARAMETER_STEP = """
+world = {world}
+h = H.adamw([(2 * world, 3), (world, 5)], world=world, rank=world - 1)
+grads = H.pointers([H.malloc(4 * n) for q in range(world) for n in (6 * world, 5 * world)])
+outs = H.pointers([H.malloc(4 * n) for n in (6, 5)])
+assert L.zero_schedule_init(h, 5, None) == zero.ZERO_OK
+was = L.double_launches()
+rc = [L.zero_fsdp_step(h, grads, world, 0, outs, 0, 1, None),
+      L.zero_fsdp_step_sched(h, grads, world, 0, outs, 0, None)]
+t = ctypes.c_int64()
+assert L.zero_schedule_get(h, ctypes.byref(t), None) == zero.ZERO_OK
+print(rc[0], rc[1], L.double_launches() - was, t.value)
+"""
+
+
+@pytest.mark.parametrize("world", [17, 64, 256])
+def test_per_parameter_step_refuses_more_replicas_than_it_takes(so, world):
+    """An AdamW context may have a world of up to 256, the per-parameter step
+    takes 16 replicas: refused before anything is gathered, launched or
+    counted as a step."""
+    assert run(so, PER_PARAMETER_STEP.format(world=world)) == ["-4 -4 0 5"]
+
+
+@pytest.mark.parametrize("world", [1, 16])
+def test_per_parameter_step_takes_what_fits(so, world):
+    """One launch, then the scheduled step's two."""
+    assert run(so, PER_PARAMETER_STEP.format(world=world)) == ["0 0 3 6"]

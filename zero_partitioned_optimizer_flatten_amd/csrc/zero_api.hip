@@ -585,6 +585,10 @@ static int fsdp_step_common(zero_ctx *c, const void *const *grads, int32_t n_rep
     CaptureScope cs(stream);
     if (n_replicas != c->world)
         return fail(ZERO_EINVAL, "n_replicas (%d) must equal world (%d)", n_replicas, c->world);
+    // an AdamW context's world may be larger than a segment's replicas
+    if (n_replicas > zk::kFsdpMaxWorld)
+        return fail(ZERO_EUNSUPPORTED, "the per-parameter step takes up to %d replicas (got %d)",
+                    zk::kFsdpMaxWorld, n_replicas);
     if (mode == kHostT && t < 1)
         return fail(ZERO_EINVAL, "step t must be >= 1 (got %lld)", (long long)t);
     if (mode != kHostT) {
