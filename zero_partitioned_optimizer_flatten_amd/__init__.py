@@ -112,6 +112,8 @@ def _dtype_code(dt: torch.dtype) -> int:
 def _resolve_device(device) -> torch.device:
     """The given device, or the current one; always with its index."""
     d = torch.device("cuda") if device is None else torch.device(device)
+    if d.type != "cuda":
+        raise ValueError(f"a state lives on a cuda device, got {d}")
     return d if d.index is not None else torch.device("cuda", torch.cuda.current_device())
 
 
