@@ -6,6 +6,7 @@ Tolerances are the bounds that adamw_reference derives for the sequence of
 of 8-bit states must be those of some number within the bound."""
 import ctypes
 import math
+from types import SimpleNamespace
 
 import numpy as np
 import pytest
@@ -627,6 +628,25 @@ def test_another_stream(state_bits):
         torch.cuda.current_stream().wait_stream(side)
         assert s.item() == r.item()
         assert all(np.array_equal(x, y) for x, y in zip(a.raw(), b.raw()))
+    a.close()
+    b.close()
+
+
+def test_a_stream_that_only_carries_its_handle():
+    """Every call takes it, the sum's own output among them."""
+    a, b = _twins(8)
+    side = torch.cuda.Stream()
+    bare = SimpleNamespace(cuda_stream=side.cuda_stream)
+    a.fill()
+    for f, g in zip(b.gflat, a.gflat):
+        f.copy_(g)
+    torch.cuda.synchronize()
+    s, r = a.st.sumsq(), b.st.sumsq(stream=bare)
+    a.st.step(1, sumsq=s, max_norm=0.02)
+    b.st.step(1, sumsq=r, max_norm=0.02, stream=bare)
+    torch.cuda.synchronize()
+    assert s.item() == r.item()
+    assert all(np.array_equal(x, y) for x, y in zip(a.raw(), b.raw()))
     a.close()
     b.close()
 

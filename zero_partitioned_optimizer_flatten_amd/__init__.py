@@ -123,13 +123,14 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
 def _stream_handle(stream: Optional[torch.cuda.Stream], device: torch.device) -> int:
-    """The given stream, or `device`'s current one (whatever device is current
-    in the caller)."""
+    """The given stream (anything that carries a `cuda_stream` handle), or
+    `device`'s current one (whatever device is current in the caller)."""
     if stream is None:
         if _raw_stream is not None:
             return _raw_stream(device.index)
         return torch.cuda.current_stream(device).cuda_stream
-    if stream.device != device:
+    # other objects are taken at their word: they need not know a device
+    if isinstance(stream, torch.cuda.Stream) and stream.device != device:
         raise ValueError(f"stream is on {stream.device}, state is on {device}")
     return stream.cuda_stream
 
@@ -680,7 +681,10 @@ class AdamWState(FsdpShardState):
         one float64 on the device (its root is the norm); written to `out`,
         or to a new tensor of the call's stream."""
         if out is None:
-            with torch.cuda.device(self.device), torch.cuda.stream(stream):
+            at = stream
+            if at is not None and not isinstance(at, torch.cuda.Stream):
+                at = torch.cuda.ExternalStream(at.cuda_stream, device=self.device)
+            with torch.cuda.device(self.device), torch.cuda.stream(at):
                 out = torch.empty(1, dtype=torch.float64, device=self.device)
         _check(lib().zero_adamw_sumsq(self._h, self._sum_ptr(out),
                                       _stream_handle(stream, self.device)))
