@@ -632,6 +632,37 @@ def test_another_stream(state_bits):
     b.close()
 
 
+@pytest.mark.parametrize("by_hand", [True, False])
+def test_replaced_buffers_live_until_a_running_step_is_done(by_hand):
+    """A long step on a side stream, its gradient let go of by the next bind
+    while it runs, and the main stream asking for memory of that size and
+    overwriting it: the step sees the gradient it was bound to."""
+    n = 1 << 26
+    st = zero.AdamWState([(n,)], 1, 0, LR, BETAS, EPS)
+    out = torch.zeros(n, device="cuda")
+    other = torch.zeros(n, device="cuda")
+    g = torch.full((n,), 1e-3, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    where = side if by_hand else None
+    st.bind([[g]], [out], stream=where)
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(None if by_hand else side):
+        for t in range(1, 21):                    # about 0.3 ms each
+            st.step(t, stream=where)
+        del g
+        st.bind([[other]], [out], stream=where)
+    again = torch.full((n,), 1e3, device="cuda")  # on the main stream, at once
+    torch.cuda.synchronize()
+    assert (again == 1e3).all()
+    m = st.get_state()[1]
+    want = 1e-3 * (1.0 - BETAS[0] ** 20)
+    # 20 steps, each off by 3 roundings of m at most (beta, product, sum)
+    assert (m.double() / want - 1).abs().max().item() <= 80 * 2.0 ** -24
+    st.close()
+
+
 def test_a_stream_that_only_carries_its_handle():
     """Every call takes it, the sum's own output among them."""
     a, b = _twins(8)

@@ -135,6 +135,15 @@ def _stream_handle(stream: Optional[torch.cuda.Stream], device: torch.device) ->
     return stream.cuda_stream
 
 
+def _torch_stream(stream, device: torch.device) -> torch.cuda.Stream:
+    """The given stream, or the current one, as torch's own object."""
+    if stream is None:
+        return torch.cuda.current_stream(device)
+    if isinstance(stream, torch.cuda.Stream):
+        return stream
+    return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
+
+
 def _ptr_array(ptrs: Sequence[int]):
     return (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs)
 
@@ -591,6 +600,7 @@ class AdamWState(FsdpShardState):
                                          self.state_bits, int(seed), ctypes.byref(h)))
         self._h = h
         self._bound = None
+        self._bound_on = 0          # stream that was current at the last bind
         self._read_layout()
         # (elements of this rank, of the parameter, before this rank's first)
         self._sizes = []
@@ -642,9 +652,13 @@ class AdamWState(FsdpShardState):
         gradients that are reduced already). params_out[k]: this rank's rows,
         written by steps; None binds gradients alone (for sumsq). None is
         taken for parameters of which this rank holds no rows. The state
-        keeps the tensors alive until the next bind; a step reads these very
-        buffers, so gradients stay in place (zero_grad(set_to_none=False)) or
-        are bound again."""
+        keeps the tensors alive until the next bind, and that one on another
+        stream than the current one, or than was current when they were bound,
+        marks them as used there (Tensor.record_stream), so that calls still
+        running find them whole; other tensors that were made on yet another
+        stream are the caller's to mark, as for torch's own operations. A step
+        reads these very buffers, so gradients stay in place
+        (zero_grad(set_to_none=False)) or are bound again."""
         n = len(self.shapes)
         for q, gl in enumerate(grads):
             if len(gl) != n:
@@ -663,17 +677,28 @@ class AdamWState(FsdpShardState):
             self._pointers(params_out, "params_out", False))
         gdt = _dtype_code(gdts.pop()) if gdts else ZERO_F32
         pdt = _dtype_code(pdts.pop()) if pdts else ZERO_F32
-        _check(lib().zero_adamw_bind(self._h, gptrs, len(grads), gdt, optrs, pdt,
-                                     _stream_handle(stream, self.device)))
+        handle, current = _stream_handle(stream, self.device), _stream_handle(None, self.device)
+        _check(lib().zero_adamw_bind(self._h, gptrs, len(grads), gdt, optrs, pdt, handle))
+        if self._bound is not None and (handle != current or handle != self._bound_on):
+            # a context's calls are ordered among themselves, so what this
+            # stream has behind it includes every call that used them
+            at = _torch_stream(stream, self.device)
+            for xs in (*self._bound[0], self._bound[1] or ()):
+                for x in xs:
+                    if x is not None:
+                        x.record_stream(at)
         self._bound = ([list(gl) for gl in grads],
                        None if params_out is None else list(params_out))
+        self._bound_on = current
 
-    def _sum_ptr(self, x: Optional[torch.Tensor]):
+    def _sum_ptr(self, x: Optional[torch.Tensor], stream=None):
         if x is None:
             return None
         self._dev(x, "sumsq")
         if x.dtype != torch.float64 or x.numel() != 1:
             raise ValueError("sumsq must be one float64")
+        if stream is not None:
+            x.record_stream(_torch_stream(stream, self.device))
         return x.data_ptr()
 
     def sumsq(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
@@ -681,12 +706,10 @@ class AdamWState(FsdpShardState):
         one float64 on the device (its root is the norm); written to `out`,
         or to a new tensor of the call's stream."""
         if out is None:
-            at = stream
-            if at is not None and not isinstance(at, torch.cuda.Stream):
-                at = torch.cuda.ExternalStream(at.cuda_stream, device=self.device)
+            at = None if stream is None else _torch_stream(stream, self.device)
             with torch.cuda.device(self.device), torch.cuda.stream(at):
                 out = torch.empty(1, dtype=torch.float64, device=self.device)
-        _check(lib().zero_adamw_sumsq(self._h, self._sum_ptr(out),
+        _check(lib().zero_adamw_sumsq(self._h, self._sum_ptr(out, stream),
                                       _stream_handle(stream, self.device)))
         return out
 
@@ -698,7 +721,7 @@ class AdamWState(FsdpShardState):
         makes the step write nothing."""
         if sumsq is not None and max_norm is None:
             raise ValueError("clipping needs max_norm")
-        _check(lib().zero_adamw_step(self._h, int(t), self._sum_ptr(sumsq),
+        _check(lib().zero_adamw_step(self._h, int(t), self._sum_ptr(sumsq, stream),
                                      float(max_norm or 0.0), _stream_handle(stream, self.device)))
 
     def step_sched(self, sumsq: Optional[torch.Tensor] = None,
@@ -707,7 +730,7 @@ class AdamWState(FsdpShardState):
         the count. Capturable in a HIP graph."""
         if sumsq is not None and max_norm is None:
             raise ValueError("clipping needs max_norm")
-        _check(lib().zero_adamw_step_sched(self._h, self._sum_ptr(sumsq),
+        _check(lib().zero_adamw_step_sched(self._h, self._sum_ptr(sumsq, stream),
                                            float(max_norm or 0.0),
                                            _stream_handle(stream, self.device)))
 
