@@ -16,6 +16,7 @@ namespace {
 std::map<uintptr_t, size_t> ranges;
 bool capturing;
 int launches;                 // of any kernel
+int copies;                   // hipMemcpyAsync
 bool adamw_streams;           // of the last AdamW step
 void *symbol[1 << 18];        // what hipGetSymbolAddress gives
 
@@ -30,6 +31,7 @@ extern "C" {
 
 void double_capturing(int on) { capturing = on != 0; }
 int double_launches() { return launches; }
+int double_copies() { return copies; }
 int double_adamw_streams() { return adamw_streams; }
 
 hipError_t hipMalloc(void **p, size_t n) {
@@ -58,6 +60,7 @@ hipError_t hipMemcpy(void *d, const void *s, size_t n, hipMemcpyKind) {
     return hipSuccess;
 }
 hipError_t hipMemcpyAsync(void *d, const void *s, size_t n, hipMemcpyKind, hipStream_t) {
+    ++copies;
     std::memcpy(d, s, n);
     return hipSuccess;
 }

@@ -60,3 +60,26 @@ def test_per_parameter_step_refuses_more_replicas_than_it_takes(so, world):
 def test_per_parameter_step_takes_what_fits(so, world):
     """One launch, then the scheduled step's two."""
     assert run(so, PER_PARAMETER_STEP.format(world=world)) == ["0 0 3 6"]
+
+
+# ------------------------------------------------------------ state in and out
+
+STATE = """
+h = H.adamw([(700, 3)], bits={bits})
+n = ctypes.c_int64()
+L.zero_shard_info(h, ctypes.byref(n), None, None)
+bufs = [H.malloc(4 * n.value) for _ in range(3)]
+for call in (L.zero_get_state, L.zero_set_state):
+    was = L.double_launches(), L.double_copies()
+    for k in range(3):
+        bad = list(bufs)
+        bad[k] += 256                         # 256 bytes past the allocation's end
+        print(call(h, *bad, None), end=" ")
+    print(L.double_launches() - was[0], L.double_copies() - was[1], call(h, *bufs, None))
+"""
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_refused_state_call_has_written_nothing(so, bits):
+    """Whichever of the three buffers is too short."""
+    assert run(so, STATE.format(bits=bits)) == ["-1 -1 -1 0 0 0"] * 2

@@ -1058,16 +1058,32 @@ int zero_schedule_get(const zero_ctx *c, int64_t *next_t, hipStream_t stream) {
     return ZERO_OK;
 }
 
+// The caller's buffers of zero_get_state and zero_set_state, all of them
+// before anything is written.
+static int check_state(const zero_ctx *c, const float *master, const float *m, const float *v,
+                       hipStream_t stream) {
+    CaptureScope cs(stream);
+    DeviceGuard g(c->device);
+    if (g.error() != hipSuccess) return hip_fail(g.error(), "hipSetDevice");
+    const float *buf[3] = {master, m, v};
+    for (int k = 0; k < 3; ++k) {
+        const float *x = buf[k];
+        if (!x) continue;
+        // kernels convert the 8-bit moments; the rest are plain copies
+        if (c->state_bits == 8 && k > 0 && (uintptr_t)x % sizeof(float))
+            return fail(ZERO_EINVAL, "state buffer misaligned");
+        int rc = check_range(x, c->shard * (int64_t)sizeof(float), "state buffer");
+        if (rc) return rc;
+    }
+    return ZERO_OK;
+}
+
 static int copy_state(const zero_ctx *c, const float *const src[3], float *const dst[3],
                       hipStream_t stream, const char *what) {
-    CaptureScope cs(stream);
     DeviceGuard g(c->device);
     if (g.error() != hipSuccess) return hip_fail(g.error(), "hipSetDevice");
     for (int k = 0; k < 3; ++k) {
         if (!src[k] || !dst[k]) continue;
-        int rc = check_range(src[k], c->shard * (int64_t)sizeof(float), what);
-        if (!rc) rc = check_range(dst[k], c->shard * (int64_t)sizeof(float), what);
-        if (rc) return rc;
         hipError_t e = hipMemcpyAsync(dst[k], src[k], (size_t)c->shard * sizeof(float),
                                       hipMemcpyDeviceToDevice, stream);
         if (e != hipSuccess) return hip_fail(e, what);
@@ -1078,14 +1094,6 @@ static int copy_state(const zero_ctx *c, const float *const src[3], float *const
 // The 8-bit states as fp32 m and v, out of or into the context.
 static int convert_state(const zero_ctx *c, float *get_m, float *get_v, const float *set_m,
                          const float *set_v, hipStream_t stream) {
-    CaptureScope cs(stream);
-    const void *p[4] = {get_m, get_v, set_m, set_v};
-    for (const void *x : p) {
-        if (!x) continue;
-        if ((uintptr_t)x % sizeof(float)) return fail(ZERO_EINVAL, "state buffer misaligned");
-        int rc = check_range(x, c->shard * (int64_t)sizeof(float), "state buffer");
-        if (rc) return rc;
-    }
     DeviceGuard g(c->device);
     if (g.error() != hipSuccess) return hip_fail(g.error(), "hipSetDevice");
     hipError_t e = zk::launch_adamw_decode(adamw_state(c), c->npieces, get_m, get_v, stream);
@@ -1096,8 +1104,10 @@ static int convert_state(const zero_ctx *c, float *get_m, float *get_v, const fl
 
 int zero_get_state(const zero_ctx *c, float *master, float *m, float *v, hipStream_t stream) {
     if (!c) return fail(ZERO_EINVAL, "null context");
+    int rc = check_state(c, master, m, v, stream);
+    if (rc) return rc;
     if (c->state_bits == 8) {
-        int rc = convert_state(c, m, v, nullptr, nullptr, stream);
+        rc = convert_state(c, m, v, nullptr, nullptr, stream);
         if (rc) return rc;
         m = v = nullptr;
     }
@@ -1109,8 +1119,10 @@ int zero_get_state(const zero_ctx *c, float *master, float *m, float *v, hipStre
 int zero_set_state(zero_ctx *c, const float *master, const float *m, const float *v,
                    hipStream_t stream) {
     if (!c) return fail(ZERO_EINVAL, "null context");
+    int rc = check_state(c, master, m, v, stream);
+    if (rc) return rc;
     if (c->state_bits == 8) {
-        int rc = convert_state(c, nullptr, nullptr, m, v, stream);
+        rc = convert_state(c, nullptr, nullptr, m, v, stream);
         if (rc) return rc;
         m = v = nullptr;
     }
