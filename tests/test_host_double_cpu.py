@@ -83,3 +83,25 @@ for call in (L.zero_get_state, L.zero_set_state):
 def test_a_refused_state_call_has_written_nothing(so, bits):
     """Whichever of the three buffers is too short."""
     assert run(so, STATE.format(bits=bits)) == ["-1 -1 -1 0 0 0"] * 2
+
+
+# ---------------------------------------------------------------- store policy
+
+POLICY = """
+for n in {sizes}:
+    h = H.adamw([(n // 2048, 2048)], bits={bits})
+    ptr = H.pointers([4096])                  # no known allocation: not looked into
+    assert L.zero_adamw_bind(h, ptr, 1, 1, ptr, 1, None) == zero.ZERO_OK
+    assert L.zero_adamw_step(h, 1, None, 0.0, None) == zero.ZERO_OK
+    print(L.double_adamw_streams())
+    L.zero_destroy(h)
+"""
+
+
+@pytest.mark.parametrize("bits,per_piece", [(32, 12 * 2048), (8, 6 * 2048 + 128)])
+def test_a_state_larger_than_the_infinity_cache_streams(so, bits, per_piece):
+    """256 MiB of the state's own bytes, either kind: 12 an element, or 6 and
+    two scales per 32."""
+    pieces = (256 << 20) // per_piece
+    sizes = [2048 * pieces, 2048 * (pieces + 1)]
+    assert run(so, POLICY.format(sizes=sizes, bits=bits)) == ["0", "1"]

@@ -52,10 +52,16 @@ constexpr unsigned kLds8 = 53248;
 // ran at 4.60 ms where nt ones took 4.05 (32 bits, Llama-7B) and 2.58 where
 // these took 2.38 (8 bits).
 constexpr int kPolDefault = 0, kPolNT = 2;
-// A state larger than the 256 MB Infinity Cache is stored at device scope as
-// well (nt sc1): 3.92-3.95 ms against 3.96-4.05 with 32 bits and 2.09 against
-// 2.12 with 8 (Llama-7B); a smaller one is not: 116 us against 110 and 86
-// against 80 (GPT-2 small, rank 3 of 8, three states in turn).
+// A state larger than the 256 MB Infinity Cache (22.4M elements with 32 bits,
+// 44M with 8) is stored at device scope as well (nt sc1): 3.92-3.95 ms against
+// 3.96-4.05 with 32 bits and 2.09 against 2.12 with 8 (Llama-7B); a smaller
+// one is not: 116 us against 110 and 86 against 80 (GPT-2 small, rank 3 of 8,
+// three states in turn). Around that size the two are close, and which one
+// wins goes by the gradients too. 8 bits, three states in turn, device scope
+// against nt: reduced bf16 gradients 64.6 us against 63.5 (24M elements), 74.2
+// and 73.3 (28M), 94.5 and 93.3 (36M), 123.6 and 123.4 (48M), 243.8 and 245.9
+// (96M); two fp32 replicas 92.3 against 93.1, 107.1 and 108.4, 136.6 and 137.9,
+// 182.0 and 184.5, 361.7 and 367.6.
 constexpr int kPolDevice = 18;
 
 template <int V> struct Const { static constexpr int value = V; };

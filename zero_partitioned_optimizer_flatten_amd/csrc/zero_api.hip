@@ -138,6 +138,12 @@ zk::AdamwStateRef adamw_state(const zero_ctx *c) {
     return {c->master, c->m, c->v, c->m8, c->r8, c->scale};
 }
 
+// Bytes of master, m and v, padding included.
+int64_t state_length(const zero_ctx *c) {
+    if (c->state_bits != 8) return 3 * (int64_t)sizeof(float) * c->shard;
+    return ((int64_t)sizeof(float) + 2) * c->shard + 2 * (c->shard / zk::kAdamwBlock);
+}
+
 // Make the context's device current for the duration of a call.
 class DeviceGuard {
   public:
@@ -649,7 +655,7 @@ static int fsdp_step_common(zero_ctx *c, const void *const *grads, int32_t n_rep
     a.v = c->v;
     a.sc = make_scalars(c, mode == kHostT ? t : 1);
     a.sc_dev = mode == kHostT ? nullptr : c->sc_dev;
-    a.stream_state = zk::state_streams(c->shard);
+    a.stream_state = zk::state_streams(state_length(c));
     hipError_t e = zk::launch_fsdp_step(a, stream);
     return e == hipSuccess ? ZERO_OK : hip_fail(e, "per-parameter step launch");
 }
@@ -857,7 +863,7 @@ static int step_common(zero_ctx *c, int64_t begin, int64_t count, const void *co
     a.sc = make_scalars(c, mode == kHostT ? t : 1);
     a.sc_dev = mode == kHostT ? nullptr : c->sc_dev;
     a.num_cus = c->num_cus;
-    a.stream_state = zk::state_streams(c->shard);
+    a.stream_state = zk::state_streams(state_length(c));
     a.max_workgroups = (int64_t)c->step_wgs_per_cu * c->num_cus;
     hipError_t e = zk::launch_step(a, stream);
     return e == hipSuccess ? ZERO_OK : hip_fail(e, "step launch");
@@ -1461,7 +1467,7 @@ static int adamw_step(zero_ctx *c, int64_t t, StepMode mode, const double *sumsq
     a.t = (uint32_t)(uint64_t)t;
     a.sumsq = sumsq;
     a.max_norm = max_norm;
-    a.stream_state = zk::state_streams(c->shard);
+    a.stream_state = zk::state_streams(state_length(c));
     hipError_t e = zk::launch_adamw(a, stream);
     return e == hipSuccess ? ZERO_OK : hip_fail(e, "AdamW step launch");
 }

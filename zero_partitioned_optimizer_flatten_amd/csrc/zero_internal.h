@@ -56,8 +56,8 @@ struct StepArgs {
 };
 // MI355X's last-level (Infinity) cache in front of HBM.
 constexpr int64_t kInfinityCacheBytes = (int64_t)256 << 20;
-// Whether a state of `elems` fp32 master/m/v elements is streamed.
-inline bool state_streams(int64_t elems) { return elems * 12 > kInfinityCacheBytes; }
+// Whether a state of that many bytes is streamed.
+inline bool state_streams(int64_t bytes) { return bytes > kInfinityCacheBytes; }
 hipError_t launch_step(const StepArgs &a, hipStream_t stream);
 
 // Resolve the scalars of the schedule's current step into *out: `base`
