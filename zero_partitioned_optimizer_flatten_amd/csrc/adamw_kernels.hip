@@ -293,13 +293,19 @@ __device__ __forceinline__ void load_last(Tensor &tn, int q0, int n, int64_t i, 
     }
 }
 
-// With several replicas (their count known when compiled) the master values
-// load once the moments are done, which need everything else: Llama-7B list,
-// rank of 8, bf16 gradients, 32 bits 5.53 ms against 5.71 with eight replicas
-// and 4.46 against 4.49 with four; 8 bits 4.24 against 4.32 and 3.06 against
-// 3.14. With one replica the two are level (3.62 and 2.46 ms), with a count
-// known only at run time the late load loses (five: 4.86 against 4.68).
-template <int NR> constexpr bool kLateMaster = NR >= 2;
+// With four replicas or more (their count known when compiled) the master
+// values load once the moments are done, which need everything else. Late
+// against together with the rest, bf16 gradients, clipped:
+//                         Llama-7B list, rank 0 of 8     GPT-2 small, rank 3 of 8
+//   8 replicas, 32 bits       5.59 and 5.76 ms              109.7 and 109.2 us
+//               8 bits        4.28     4.39                  77.7     78.4
+//   4 replicas, 32 bits       4.45     4.49                  89.7     88.0
+//               8 bits        3.07     3.15                  57.6     57.4
+//   2 replicas, 32 bits       3.98     3.92                  79.6     77.8
+//               8 bits        2.49     2.49                  48.9     47.5
+// With one the two are level, with a count known only at run time the late
+// load loses (five: 4.86 ms against 4.68).
+template <int NR> constexpr bool kLateMaster = NR >= 4;
 
 // How a part of a tensor (512 elements, a wave's) is reached. The last part
 // loads all that it needs before it waits, like the others: GPT-2 small, rank
