@@ -944,7 +944,9 @@ sumsq_kernel(const AdamwTensor *table, const int32_t *map,
     // 256 registers)
     constexpr int width = NR == 0 || NR > kGroup ? kGroup : NR;
     constexpr int flight = GB ? 64 : 32;
-    constexpr int turns = flight / width >= 8 ? 8 : flight / width;
+    // three of fp32 by 4, not 8: odd widths 55.5 us against 63.0, GPT-2 small's
+    // rank 31.5 against 36.3, Llama-7B list 1.46 ms against 1.50
+    constexpr int turns = !GB && NR == 3 ? 4 : flight / width >= 8 ? 8 : flight / width;
     static_assert(kAdamwPiece % (turns * kRow) == 0, "whole rounds in a piece");
     const int lane = threadIdx.x % kWave;
     const int64_t first = (int64_t)blockIdx.x * (kSumsqBlock / kWave) +
@@ -1044,6 +1046,15 @@ hipError_t sumsq_typed(const SumsqArgs &a, hipStream_t stream) {
     return hipGetLastError();
 }
 
+// Replica counts known when compiled, against the count of the run (us; odd
+// widths, GPT-2 small's rank 3 of 8, Llama-7B list's rank 0 of 8):
+//            bf16                                        fp32
+//   1   13.1 15.6    8.7 10.4    229 279       20.2 21.7   12.6 14.2    482 471
+//   2   22.3 23.6   13.6 14.7    470 476       39.6 38.5   23.5 22.2    940 973
+//   3   31.6 32.8   18.5 19.0    723 715       55.5 56.0   31.5 31.7   1456 1459
+//   4   40.2 41.7   23.9 24.2    982 975       71.2 74.0   40.5 42.8   1925 1955
+//   8   76.2 77.9   42.4 45.8   1898 1918     144.0 143.9  81.1 81.0   3892 3883
+// Eleven tensors of 893 elements in all, four of fp32: 4.4 and 5.7.
 template <bool GB>
 hipError_t sumsq_replicas(const SumsqArgs &a, hipStream_t stream) {
     switch (a.n) {
