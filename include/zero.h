@@ -382,8 +382,14 @@ int zero_fsdp_step_sched(zero_ctx *ctx, const void *const *grads,
  * in binary32 on the fresh m and v, and rounds both stochastically (a
  * deterministic hash of the seed, t and the element's place: the same call on
  * the same state gives the same bits). Rounding to nearest would freeze v: a
- * step moves it by about 1-b2 of itself, the codes of r are 6-12% apart. A
- * v of 2^-126 or more is never stored as zero (below, its root comes out too
+ * step moves it by about 1-b2 of itself, the codes of r are 6-12% apart. That
+ * holds where e4m3 has three mantissa bits, from 2^-6 scales on (2^-14 of a
+ * block's largest or more). An r stored below is rounded to nearest after all,
+ * on steps of 2^-9 scales, and can freeze: it rises only once a step takes it
+ * 3/8 or more of such a step further, and until then stays too small by up to
+ * sqrt((121/64 - b2) / (1 - b2)) (30 with b2 = 0.999, 4.4 with 0.95), its
+ * element's steps too large by as much; one that falls may stay at up to 2^-6
+ * scales. A v of 2^-126 or more is never stored as zero (below, its root comes out too
  * small); an infinite or NaN moment is stored as NaN, makes its own master
  * NaN and does not touch its neighbours' codes.
  *
