@@ -447,8 +447,10 @@ int zero_adamw_bind(zero_ctx *ctx, const void *const *grads,
                     hipStream_t stream);
 
 /* *sumsq (device) = sum of the squares of the mean gradient over this rank's
- * elements, in binary64 throughout and in a fixed order: the same gradients
- * give the same bits. Ranks that hold different rows add theirs (one
+ * elements, in binary64 throughout and in an order that the sizes and the
+ * gradients' addresses modulo four elements fix: the same gradients at such
+ * addresses, in whatever buffers, give the same bits; at others they are added
+ * in another order and the last bits may differ. Ranks that hold different rows add theirs (one
  * all-reduce of one number); its root is the gradient's norm. One launch.
  * EINVAL: not an AdamW context, nothing bound, null or misaligned sum. */
 int zero_adamw_sumsq(zero_ctx *ctx, double *sumsq, hipStream_t stream);

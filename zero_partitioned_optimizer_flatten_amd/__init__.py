@@ -704,7 +704,9 @@ class AdamWState(FsdpShardState):
     def sumsq(self, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
         """Sum of squares of the mean gradient over this rank's elements, as
         one float64 on the device (its root is the norm); written to `out`,
-        or to a new tensor of the call's stream."""
+        or to a new tensor of the call's stream. Its last bits go by the
+        order of the additions, which the gradients' addresses modulo four
+        elements decide as well as the sizes."""
         if out is None:
             at = None if stream is None else _torch_stream(stream, self.device)
             with torch.cuda.device(self.device), torch.cuda.stream(at):

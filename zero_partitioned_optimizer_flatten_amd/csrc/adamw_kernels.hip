@@ -815,7 +815,8 @@ __global__ void __launch_bounds__(256) widen_kernel(const void *src, float *dst,
 // S = sum over all elements of (sum_q g_q)^2 / N^2, everything in binary64.
 // Wave w takes pieces w, w + W, ...; a workgroup's partial sum goes to memory and
 // the last workgroup to finish adds the partials in their order, so the
-// result does not depend on which one that is.
+// result does not depend on which one that is. Which wave and lane takes an
+// element depends on the sizes and on the replicas' common phase (common_head).
 constexpr int kSumsqBlock = 256;
 constexpr int kRow = kQuad * kWave;              // elements that a wave reads in one turn
 
