@@ -58,3 +58,20 @@ def test_state_streams(kernels):
             assert lines and all(re.search(r"\bnt\b", x) for x in lines), name
             stores = [x for x in lines if x.startswith("buffer_store")]
             assert 2 * sum("sc1" in x for x in stores) == len(stores), name
+
+
+def test_partial_sums_are_handed_over_at_device_scope(kernels):
+    """The order of a workgroup's partial sum before its count rests on these
+    instructions: the partial stored at device scope, waited for, then
+    counted; the partials loaded at device scope by the one that joins them."""
+    for name, body, _ in kernels:
+        if "sumsq_kernel" not in name:
+            continue
+        lines = [x.strip() for x in body.splitlines()]
+        count = next(i for i, x in enumerate(lines) if x.startswith("global_atomic_add"))
+        stores = [i for i, x in enumerate(lines[:count]) if x.startswith("global_store")]
+        assert len(stores) == 1 and "global_store_dwordx2" in lines[stores[0]], name
+        assert re.search(r"\bsc1\b", lines[stores[0]]), name
+        assert "s_waitcnt vmcnt(0)" in lines[stores[0]:count], name
+        loads = [x for x in lines[count:] if x.startswith("global_load")]
+        assert len(loads) >= 2 and all(re.search(r"\bsc1\b", x) for x in loads), name

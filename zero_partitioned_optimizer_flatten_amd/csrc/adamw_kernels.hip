@@ -986,11 +986,14 @@ sumsq_kernel(const AdamwTensor *table, const int32_t *map,
     const double s = group_sum(acc, lds);
     if (threadIdx.x == 0) {
         __hip_atomic_store(&partial[blockIdx.x], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-        // The partial is the only thing to be ordered before the count, and
-        // an agent-scope store is acknowledged once every XCD can see it, so
-        // waiting for it is enough. A release and acquire at the counter
-        // would write back and drop the whole L2 in every workgroup: 139 us
-        // against 52 us (15.6M elements, N = 8, bf16, 2048 workgroups).
+        // The partial is the only thing to be ordered before the count.
+        // This holds on gfx950 and leans on its instructions, not on the
+        // language's memory model: an agent-scope store (sc1) writes through
+        // and is acknowledged once every XCD can see it, so waiting for it is
+        // enough, and the joining workgroup's agent-scope loads (sc1) read
+        // past its own caches. A release and acquire at the counter would
+        // write back and drop the whole L2 in every workgroup: 139 us against
+        // 52 us (15.6M elements, N = 8, bf16, 2048 workgroups).
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
         last = last_of(done, blockIdx.x, gridDim.x);
     }
