@@ -438,7 +438,12 @@ int zero_adamw_groups(zero_ctx *ctx, const double *weight_decay,
  * may be NULL. The buffers stay the caller's and must live until the last
  * call or graph replay that uses them. A later bind may change any pointer,
  * also under graphs captured before it, but not the replica count, a dtype,
- * or whether outputs are bound (EINVAL). Other EINVAL: not an AdamW context,
+ * or whether outputs are bound (EINVAL). A captured bind takes effect when it
+ * is replayed, and again with every replay: the buffers bound before it must
+ * live until the first replay, its own as long as the graph. The first bind
+ * of gradients, or of outputs, cannot be captured (EINVAL): calls before a
+ * replay would find none. Outputs may share no element with each other, nor
+ * with another element's gradient. Other EINVAL: not an AdamW context,
  * n_replicas outside [1, ZERO_FSDP_MAX_WORLD], null or misaligned pointers,
  * ranges past their allocations. */
 int zero_adamw_bind(zero_ctx *ctx, const void *const *grads,

@@ -52,18 +52,21 @@ class _Tensor:
 @pytest.fixture
 def state(monkeypatch):
     """An AdamWState of one (2, 3) and one empty parameter whose library takes
-    every call; current[0] is the current stream."""
-    current = [0]
+    every call; current[0] is the current stream, st.capturing[0] whether a
+    call's stream is being captured."""
+    current, capturing = [0], [False]
     fake = SimpleNamespace(zero_adamw_bind=lambda *a: 0, zero_adamw_sumsq=lambda *a: 0,
                            zero_adamw_step=lambda *a: 0, zero_destroy=lambda *a: None)
     monkeypatch.setattr(zero, "lib", lambda: fake)
     monkeypatch.setattr(zero, "_raw_stream", lambda index: current[0])
+    monkeypatch.setattr(zero, "_capturing", lambda *a: capturing[0], raising=False)
     monkeypatch.setattr(zero, "_torch_stream",
                         lambda s, device: SimpleNamespace(cuda_stream=current[0]) if s is None else s,
                         raising=False)
     st = object.__new__(zero.AdamWState)
     st.device, st.shapes, st._sizes = _Tensor.device, [(2, 3), (0,)], [(6, 6, 0), (0, 0, 0)]
     st._h, st._bound, st._bound_on = SimpleNamespace(value=0), None, 0
+    st._captured, st.capturing = [], capturing
     return st, current
 
 
@@ -89,3 +92,22 @@ def test_a_rebind_keeps_replaced_tensors_for_its_stream(state, bound_on, rebound
     st.bind([[second, None]], [second, None], stream=stream)
     assert g.used_on == o.used_on == used
     assert second.used_on == []
+
+
+def test_a_captured_bind_keeps_its_tensors_and_those_before(state):
+    """Until the first replay the device holds the earlier binding, and any
+    later replay uploads the captured one again: both live as long as the
+    state."""
+    import weakref
+    st, _ = state
+    alive = []
+    for captured in (False, True, False, False):
+        st.capturing[0] = captured
+        g, o = _Tensor(), _Tensor()
+        alive.append((weakref.ref(g), weakref.ref(o)))
+        st.bind([[g, None]], [o, None])
+        del g, o
+    assert [[r() is not None for r in p] for p in alive] == [
+        [True, True], [True, True], [False, False], [True, True]]
+    st.close()
+    assert not any(r() is not None for p in alive for r in p)

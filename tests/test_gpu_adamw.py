@@ -598,6 +598,47 @@ def test_norm_clip_and_step_together_eager_and_replayed(state_bits):
 
 
 @pytest.mark.parametrize("state_bits", [32, 8])
+def test_a_captured_bind(state_bits):
+    """Bind, norm and step in one graph, against the same calls made eagerly;
+    eager steps on other gradients between the replays, each of which binds
+    the captured ones again. A first bind is not captured."""
+    a, b = _twins(state_bits)
+    st = zero.AdamWState([(40,)], 1, 0, LR, state_bits=state_bits)
+    g = torch.zeros(40, device="cuda")
+    s = torch.zeros(1, dtype=torch.float64, device="cuda")
+    b.st.schedule(1)
+    others = [[x.clone() for x in gl] for gl in a.grads]
+    graph = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph):
+        _einval(st.bind, [[g]], [g])
+        b.st.bind(b.grads, b.outs)
+        b.st.sumsq(out=s)
+        b.st.step_sched(sumsq=s, max_norm=0.02)
+    _einval(st.step, 1)
+    for k in range(4):
+        a.fill()
+        for f, x in zip(b.gflat, a.gflat):
+            f.copy_(x)
+        a.st.bind(a.grads, a.outs)
+        a.st.step(2 * k + 1, sumsq=a.st.sumsq(), max_norm=0.02)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(np.array_equal(x, y) for x, y in zip(a.raw(), b.raw())), f"replay {k}"
+        for gl in others:
+            for x in gl:
+                x.copy_(torch.randn(x.shape, device="cuda") * 1e-3)
+        a.st.bind(others, a.outs)
+        b.st.bind(others, b.outs)
+        a.st.step(2 * k + 2)
+        b.st.step_sched()
+        assert all(np.array_equal(x, y) for x, y in zip(a.raw(), b.raw())), f"eager {k}"
+    del graph
+    for x in (a, b, st):
+        x.close()
+
+
+@pytest.mark.parametrize("state_bits", [32, 8])
 def test_a_scheduled_step_means_over_what_is_bound(state_bits):
     """Reduced gradients (one replica) on a rank of a world of four."""
     j = Job(RAGGED, 4, 1, 1, torch.float32, torch.float32, state_bits, 1)

@@ -105,3 +105,30 @@ def test_a_state_larger_than_the_infinity_cache_streams(so, bits, per_piece):
     pieces = (256 << 20) // per_piece
     sizes = [2048 * pieces, 2048 * (pieces + 1)]
     assert run(so, POLICY.format(sizes=sizes, bits=bits)) == ["0", "1"]
+
+
+# ------------------------------------------------------------- a captured bind
+
+CAPTURED = """
+h = H.adamw([(700, 3)], bits={bits})
+ptr = H.pointers([4096])
+bind = lambda: L.zero_adamw_bind(h, ptr, 1, 1, ptr, 1, None)
+L.double_capturing(1)
+was = L.double_launches()
+print(bind(), L.double_launches() - was, L.zero_adamw_step(h, 1, None, 0.0, None))
+L.double_capturing(0)
+grads_only = L.zero_adamw_bind(h, ptr, 1, 1, None, 1, None)
+L.double_capturing(1)
+print(grads_only, bind())                  # its outputs would be the first
+L.double_capturing(0)
+print(bind())
+L.double_capturing(1)
+print(bind(), L.zero_adamw_step(h, 1, None, 0.0, None))
+"""
+
+
+@pytest.mark.parametrize("bits", [32, 8])
+def test_a_first_bind_is_not_captured(so, bits):
+    """Captured, it would reach the device only with a replay, and a step
+    before that would follow null pointers."""
+    assert run(so, CAPTURED.format(bits=bits)) == ["-1 0 -1", "0 -1", "0", "0 0"]

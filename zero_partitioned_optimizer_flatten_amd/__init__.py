@@ -144,6 +144,14 @@ def _torch_stream(stream, device: torch.device) -> torch.cuda.Stream:
     return torch.cuda.ExternalStream(stream.cuda_stream, device=device)
 
 
+def _capturing(stream, device: torch.device) -> bool:
+    """Whether the given stream, or the device's current one, is captured."""
+    if stream is None and torch.cuda.current_device() == device.index:
+        return torch.cuda.is_current_stream_capturing()
+    with torch.cuda.stream(_torch_stream(stream, device)):
+        return torch.cuda.is_current_stream_capturing()
+
+
 def _ptr_array(ptrs: Sequence[int]):
     return (ctypes.c_void_p * max(1, len(ptrs)))(*ptrs)
 
@@ -601,6 +609,7 @@ class AdamWState(FsdpShardState):
         self._h = h
         self._bound = None
         self._bound_on = 0          # stream that was current at the last bind
+        self._captured = []         # bindings that a captured bind keeps alive
         self._read_layout()
         # (elements of this rank, of the parameter, before this rank's first)
         self._sizes = []
@@ -656,7 +665,10 @@ class AdamWState(FsdpShardState):
         stream than the current one, or than was current when they were bound,
         marks them as used there (Tensor.record_stream), so that calls still
         running find them whole; other tensors that were made on yet another
-        stream are the caller's to mark, as for torch's own operations. A step
+        stream are the caller's to mark, as for torch's own operations. A bind
+        that is captured into a graph (never the first) uploads its pointers
+        with every replay; the state then keeps its tensors, and those bound
+        before it, alive until close(). A step
         reads these very buffers, so gradients stay in place
         (zero_grad(set_to_none=False)) or are bound again."""
         n = len(self.shapes)
@@ -679,7 +691,10 @@ class AdamWState(FsdpShardState):
         pdt = _dtype_code(pdts.pop()) if pdts else ZERO_F32
         handle, current = _stream_handle(stream, self.device), _stream_handle(None, self.device)
         _check(lib().zero_adamw_bind(self._h, gptrs, len(grads), gdt, optrs, pdt, handle))
-        if self._bound is not None and (handle != current or handle != self._bound_on):
+        bound = ([list(gl) for gl in grads], None if params_out is None else list(params_out))
+        if _capturing(stream, self.device):
+            self._captured += [self._bound, bound]
+        elif self._bound is not None and (handle != current or handle != self._bound_on):
             # a context's calls are ordered among themselves, so what this
             # stream has behind it includes every call that used them
             at = _torch_stream(stream, self.device)
@@ -687,9 +702,12 @@ class AdamWState(FsdpShardState):
                 for x in xs:
                     if x is not None:
                         x.record_stream(at)
-        self._bound = ([list(gl) for gl in grads],
-                       None if params_out is None else list(params_out))
+        self._bound = bound
         self._bound_on = current
+
+    def close(self):
+        super().close()             # waits for the device
+        self._bound, self._captured = None, []
 
     def _sum_ptr(self, x: Optional[torch.Tensor], stream=None):
         if x is None:

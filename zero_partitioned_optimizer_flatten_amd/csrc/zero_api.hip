@@ -178,6 +178,7 @@ class CaptureScope {
         g_skip_range = st == hipStreamCaptureStatusActive;
     }
     ~CaptureScope() { g_skip_range = prev_; }
+    bool capturing() const { return g_skip_range; }
 
   private:
     bool prev_;
@@ -1349,6 +1350,9 @@ int zero_adamw_bind(zero_ctx *c, const void *const *grads, int32_t n_replicas,
     if (rc) return rc;
     CaptureScope cs(stream);
     if (!grads) return fail(ZERO_EINVAL, "null gradient array");
+    // what is captured reaches the device table only with a replay
+    if (cs.capturing() && (!c->aw_n || (params_out && !c->aw_has_out)))
+        return fail(ZERO_EINVAL, "the first bind of gradients or outputs cannot be captured");
     if (n_replicas < 1 || n_replicas > ZERO_FSDP_MAX_WORLD)
         return fail(ZERO_EINVAL, "n_replicas must be in [1, %d] (got %d)", ZERO_FSDP_MAX_WORLD,
                     n_replicas);
