@@ -293,19 +293,23 @@ __device__ __forceinline__ void load_last(Tensor &tn, int q0, int n, int64_t i, 
     }
 }
 
-// With four replicas or more (their count known when compiled) the master
-// values load once the moments are done, which need everything else. Late
-// against together with the rest, bf16 gradients, clipped:
-//                         Llama-7B list, rank 0 of 8     GPT-2 small, rank 3 of 8
-//   8 replicas, 32 bits       5.59 and 5.76 ms              109.7 and 109.2 us
-//               8 bits        4.28     4.39                  77.7     78.4
-//   4 replicas, 32 bits       4.45     4.49                  89.7     88.0
-//               8 bits        3.07     3.15                  57.6     57.4
-//   2 replicas, 32 bits       3.98     3.92                  79.6     77.8
-//               8 bits        2.49     2.49                  48.9     47.5
-// With one the two are level, with a count known only at run time the late
-// load loses (five: 4.86 ms against 4.68).
-template <int NR> constexpr bool kLateMaster = NR >= 4;
+// Where an element has 8 bytes of gradients or more, of several replicas whose
+// count is known when compiled, the master values load once the moments are
+// done, which need everything else. Late against together with the rest, on
+// states that nothing keeps in a cache; us for GPT-2 small's rank 3 of 8 and
+// 27.8M elements at odd widths (six states in turn), ms for Llama-7B's rank 0
+// of 8; bf16 outputs:
+//                       32 bits                                8 bits
+//   2 bf16    79.6  77.2   144  138   3.98 3.89     48.9 47.6    90.3  86.3   2.49 2.46
+//   2 fp32    86.3  86.4   157  153   4.52 4.57     57.0 57.4   100.7 101.3   2.99 3.09
+//   4 bf16    88.8  88.0   161  158   4.44 4.49     57.9 57.8   109.3 105.7   3.05 3.14
+//   4 fp32   106.3 106.5   190  191   5.75 5.83     77.7 78.1   138.9 143.0   4.23 4.31
+//   8 bf16   108.7 108.8   198  198   5.57 5.74     77.1 77.8   147.2 146.8   4.34 4.44
+//   8 fp32   150.4 150.8   272  274   8.21 8.20    124.5 123.1  227.4 227.4   6.83 6.90
+// One replica: bf16 75 and 72, 3.82 and 3.65; 45 and 43, 2.24 and 2.13. With a
+// count known only at run time the late load loses (five: 4.86 ms against
+// 4.68).
+template <int NR, bool GB> constexpr bool kLateMaster = NR >= 2 && NR * (GB ? 2 : 4) >= 8;
 
 // How a part of a tensor (512 elements, a wave's) is reached. The last part
 // loads all that it needs before it waits, like the others: GPT-2 small, rank
@@ -446,7 +450,7 @@ __device__ __forceinline__ void part32(const KernelArgs &a, Tensor &tn, Group &g
             const int off = kQuad * (lane + h * kWave);
             load_f4<kPolNT>(sm, off, m[h]);
             load_f4<kPolNT>(sv, off, v[h]);
-            if (!kLateMaster<NR>) load_f4<kPolNT>(sp, off, p[h]);
+            if (!kLateMaster<NR, GB>) load_f4<kPolNT>(sp, off, p[h]);
         }
         __builtin_amdgcn_sched_barrier(0);
         return uniforms<NR>(a, gr, u);
@@ -457,7 +461,7 @@ __device__ __forceinline__ void part32(const KernelArgs &a, Tensor &tn, Group &g
     for (int h = 0; h < kSplit; ++h)
 #pragma unroll
         for (int e = 0; e < kQuad; ++e) d[h][e] = moments32(g[h][e], m[h][e], v[h][e], u);
-    if (kLateMaster<NR>) {
+    if (kLateMaster<NR, GB>) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int h = 0; h < kSplit; ++h) load_f4<kPolNT>(sp, kQuad * (lane + h * kWave), p[h]);
@@ -664,7 +668,7 @@ __device__ __forceinline__ void part8(const KernelArgs &a, Tensor &tn, Group &gr
             cr[h] = __builtin_amdgcn_raw_buffer_load_b32(sr, off, 0, kPolNT);
             em[h] = scale[off / kAdamwBlock];
             er[h] = scale[kAdamwScales + off / kAdamwBlock];
-            if (!kLateMaster<NR>) load_f4<kPolNT>(sp, off, p[h]);
+            if (!kLateMaster<NR, GB>) load_f4<kPolNT>(sp, off, p[h]);
         }
         __builtin_amdgcn_sched_barrier(0);
         return uniforms8<NR>(a, gr, u);
@@ -687,7 +691,7 @@ __device__ __forceinline__ void part8(const KernelArgs &a, Tensor &tn, Group &gr
         for (int h = 0; h < kSplit; ++h)
             encode8<false>(m[h], r[h], u, q + h * kWave, cm[h], cr[h], em[h], er[h]);
     }
-    if (kLateMaster<NR>) {
+    if (kLateMaster<NR, GB>) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int h = 0; h < kSplit; ++h) load_f4<kPolNT>(sp, kQuad * (lane + h * kWave), p[h]);
