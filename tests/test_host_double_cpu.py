@@ -99,10 +99,10 @@ for n in {sizes}:
 
 
 @pytest.mark.parametrize("bits,per_piece", [(32, 12 * 2048), (8, 6 * 2048 + 128)])
-def test_a_state_larger_than_the_infinity_cache_streams(so, bits, per_piece):
-    """256 MiB of the state's own bytes, either kind: 12 an element, or 6 and
+def test_a_state_larger_than_half_the_infinity_cache_streams(so, bits, per_piece):
+    """128 MiB of the state's own bytes, either kind: 12 an element, or 6 and
     two scales per 32."""
-    pieces = (256 << 20) // per_piece
+    pieces = (128 << 20) // per_piece
     sizes = [2048 * pieces, 2048 * (pieces + 1)]
     assert run(so, POLICY.format(sizes=sizes, bits=bits)) == ["0", "1"]
 

@@ -52,16 +52,20 @@ constexpr unsigned kLds8 = 53248;
 // ran at 4.60 ms where nt ones took 4.05 (32 bits, Llama-7B) and 2.58 where
 // these took 2.38 (8 bits).
 constexpr int kPolDefault = 0, kPolNT = 2;
-// A state larger than the 256 MB Infinity Cache (22.4M elements with 32 bits,
-// 44M with 8) is stored at device scope as well (nt sc1): 3.92-3.95 ms against
-// 3.96-4.05 with 32 bits and 2.09 against 2.12 with 8 (Llama-7B); a smaller
-// one is not: 116 us against 110 and 86 against 80 (GPT-2 small, rank 3 of 8,
-// three states in turn). Around that size the two are close, and which one
-// wins goes by the gradients too. 8 bits, three states in turn, device scope
-// against nt: reduced bf16 gradients 64.6 us against 63.5 (24M elements), 74.2
-// and 73.3 (28M), 94.5 and 93.3 (36M), 123.6 and 123.4 (48M), 243.8 and 245.9
-// (96M); two fp32 replicas 92.3 against 93.1, 107.1 and 108.4, 136.6 and 137.9,
-// 182.0 and 184.5, 361.7 and 367.6.
+// A state of more than half the 256 MB Infinity Cache (11M elements with 32
+// bits, 22M with 8) is stored at device scope as well (nt sc1). Device scope
+// against nt, us, on eight or ten states in turn that leave nothing in a cache:
+//   32 bits           4M           8M          12M          20M elements
+//   reduced bf16  21.3  21.0   38.1  38.3   55.2  55.6   89.9  91.5
+//   reduced fp32  24.3  23.9   43.6  43.2   63.9  63.4  103.4 103.5
+//   4 of bf16     25.7  26.1   47.4  48.0   67.7  69.5  108.9 110.3
+//   8 of bf16     31.0  30.7   56.4  56.7   82.6  83.0  133.6 134.3
+//   8 bits           12M          24M          36M          56M elements
+//   reduced bf16  34.9  34.1   64.6  64.1   94.7  95.0  144.3 145.7
+//   reduced fp32  41.7  41.4   79.4  79.4  118.2 118.6  184.0 184.1
+//   4 of bf16     45.1  45.6   85.1  86.3  126.3 128.1  195.7 197.8
+//   8 of bf16     60.6  60.5  116.9 117.2  174.0 173.7  272.0 271.5
+// and 3.92-3.95 ms against 3.96-4.05 and 2.09 against 2.12 (Llama-7B).
 constexpr int kPolDevice = 18;
 
 template <int V> struct Const { static constexpr int value = V; };

@@ -1471,7 +1471,7 @@ static int adamw_step(zero_ctx *c, int64_t t, StepMode mode, const double *sumsq
     a.t = (uint32_t)(uint64_t)t;
     a.sumsq = sumsq;
     a.max_norm = max_norm;
-    a.stream_state = zk::state_streams(state_length(c));
+    a.stream_state = state_length(c) > zk::kAdamwStreamBytes;
     hipError_t e = zk::launch_adamw(a, stream);
     return e == hipSuccess ? ZERO_OK : hip_fail(e, "AdamW step launch");
 }

@@ -128,6 +128,9 @@ constexpr int kAdamwScales = kAdamwPiece / kAdamwBlock;   // per piece and momen
 constexpr int kAdamwMaxReplicas = kFsdpMaxWorld;
 // A dispatch holds at most 2^32-1 work-items, 256 of them for a piece.
 constexpr int64_t kAdamwMaxPieces = 0xFFFFFFFFll / 256;
+// A state of more bytes than this is stored at device scope (its kernels say
+// why, with figures).
+constexpr int64_t kAdamwStreamBytes = kInfinityCacheBytes / 2;
 
 struct AdamwTensor {
     const void *grads[kAdamwMaxReplicas];   // replica q's gradient at this rank's first element
@@ -163,7 +166,7 @@ struct AdamwArgs {
     uint32_t t;                   // step, without sc_dev
     const double *sumsq;          // clip by its root, or null
     double max_norm;
-    bool stream_state;            // state larger than the Infinity Cache
+    bool stream_state;            // state larger than kAdamwStreamBytes
 };
 hipError_t launch_adamw(const AdamwArgs &a, hipStream_t stream);
 
