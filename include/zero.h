@@ -386,12 +386,12 @@ int zero_fsdp_step_sched(zero_ctx *ctx, const void *const *grads,
  * holds where e4m3 has three mantissa bits, from 2^-6 scales on (2^-14 of a
  * block's largest or more). An r stored below is rounded to nearest after all,
  * on steps of 2^-9 scales, and can freeze: it rises only once a step takes it
- * 3/8 or more of such a step further, and until then stays too small by up to
+ * far enough to round up, and until then stays too small by up to
  * sqrt((121/64 - b2) / (1 - b2)) (30 with b2 = 0.999, 4.4 with 0.95), its
  * element's steps too large by as much; one that falls may stay at up to 2^-6
- * scales. A v of 2^-126 or more is never stored as zero (below, its root comes out too
- * small); an infinite or NaN moment is stored as NaN, makes its own master
- * NaN and does not touch its neighbours' codes.
+ * scales. A v of 2^-126 or more is never stored as zero (below, its root comes
+ * out too small); an infinite or NaN moment is stored as NaN, makes its own
+ * master NaN and does not touch its neighbours' codes.
  *
  * A context's calls read and write its state, its device table and one
  * workspace: order them among themselves (one stream, or events), replays of
@@ -455,8 +455,9 @@ int zero_adamw_bind(zero_ctx *ctx, const void *const *grads,
  * elements, in binary64 throughout and in an order that the sizes and the
  * gradients' addresses modulo four elements fix: the same gradients at such
  * addresses, in whatever buffers, give the same bits; at others they are added
- * in another order and the last bits may differ. Ranks that hold different rows add theirs (one
- * all-reduce of one number); its root is the gradient's norm. One launch.
+ * in another order and the last bits may differ. Ranks that hold different
+ * rows add theirs (one all-reduce of one number); its root is the gradient's
+ * norm. One launch.
  * EINVAL: not an AdamW context, nothing bound, null or misaligned sum. */
 int zero_adamw_sumsq(zero_ctx *ctx, double *sumsq, hipStream_t stream);
 
