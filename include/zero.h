@@ -483,6 +483,125 @@ int zero_adamw_step_sched(zero_ctx *ctx, const double *sumsq, double max_norm,
 int zero_adamw_state(const zero_ctx *ctx, void **master, void **m, void **v,
                      void **scale);
 
+/* ---- Both ends of a language model -------------------------------------
+ * The operators whose gradients are a list's largest and most awkward
+ * tensors: the embedding lookup, dropout, and the softmax cross entropy of
+ * hidden states against a (vocab, width) table. Their gradients are written,
+ * or added, straight into the tensor's place in a flat gradient vector, at
+ * any alignment of its dtype, where zero_step, zero_adamw_* or a reduction
+ * reads them; with a tied table the loss writes its share and the lookup adds
+ * its own.
+ *
+ * These calls take no context. They run on the current HIP device, on which
+ * all their device pointers live, stream-ordered on `stream`, allocate
+ * nothing, and can be captured into a HIP graph. A workspace is scratch of the
+ * call: calls that may run at once, replays of two graphs included, need one
+ * each; its contents need not be kept. Tables, hidden states and activations
+ * are contiguous and row-major. Outputs may not overlap inputs, save where
+ * said. The same call on the same values gives the same bits: there are no
+ * floating-point atomics.
+ *
+ * ids are 4- or 8-byte signed integers (id_bytes). An id outside [0, rows)
+ * reads as a row of zeros and has no gradient; such a target takes its row out
+ * of the loss. Arithmetic is binary32, each output is rounded once (nearest,
+ * ties to even). */
+
+/* Dropout: an element is kept where its 16 random bits are at least
+ * round(65536 p), and multiplied by the inverse of the share kept, so p is
+ * taken to a multiple of 2^-16 and the expectation is exact; the others become
+ * 0, whatever they were. The bits are Philox4x32-10's (Salmon et al., 2011)
+ * with key = seed and counter = (element / 8, offset + *counter), 64 bits
+ * each: element 8 b + k takes the k-th 16 bits of block b, lowest first, where
+ * an element is its index in the contiguous tensor. The mask is never stored:
+ * the same drop in the backward call gives it again. Steps and layers take
+ * different offsets. counter: device pointer to a 64-bit number, read when the
+ * kernel runs (a captured graph's step count), or NULL. */
+typedef struct {
+    double p;                 /* in [0, 1] */
+    uint64_t seed, offset;
+    const uint64_t *counter;
+} zero_drop;
+
+/* out[n] = D(scale * table[ids[n]] + position_table[position_ids[n]]) for
+ * n < count, with rows of `width` elements; D is dropout over the count *
+ * width output elements (drop NULL: none). position_ids and position_table may
+ * be NULL together. Both tables have `dtype`. EINVAL: null or misaligned
+ * pointers, ranges past their allocations, unknown dtypes or id sizes, a scale
+ * not finite, p outside [0, 1], an output that overlaps an input.
+ * EUNSUPPORTED: more than 3.4e10 output elements, 2^31 ids, 2^30 rows. */
+int zero_embed(const void *ids, int32_t id_bytes, int64_t count,
+               const void *table, int64_t rows, int64_t width,
+               zero_dtype dtype, double scale, const void *position_ids,
+               const void *position_table, int64_t position_rows,
+               const zero_drop *drop, void *out, zero_dtype out_dtype,
+               hipStream_t stream);
+
+/* Bytes of workspace that zero_embed_grad needs. Host only. */
+int zero_embed_grad_workspace(int64_t count, int64_t rows, int64_t width,
+                              int64_t *bytes);
+
+/* The lookup's gradient:
+ *   grad_table[v] = scale * (sum over n with ids[n] == v of D(grad_out[n]))
+ * written for every v < rows (zeros where no id names it), or, with
+ * accumulate != 0, added to the rows that ids name; rows that none names are
+ * then not touched. D: the forward call's drop. The sum is in binary32, in an
+ * order that count alone fixes. The gradient of a position table is this call
+ * with the position ids, scale 1 and the same drop. workspace: 256-byte
+ * aligned. EINVAL, EUNSUPPORTED as zero_embed; EINVAL also for a workspace
+ * that is too small. */
+int zero_embed_grad(const void *grad_out, zero_dtype grad_dtype,
+                    const void *ids, int32_t id_bytes, int64_t count,
+                    int64_t rows, int64_t width, double scale,
+                    const zero_drop *drop, void *grad_table,
+                    zero_dtype table_dtype, int32_t accumulate,
+                    void *workspace, int64_t workspace_bytes,
+                    hipStream_t stream);
+
+/* out[i] = D(x[i]), plus add[i] where add is not NULL, for i < count. With
+ * grad_out as x it is its own backward call. out may be x or add itself.
+ * EINVAL: as zero_embed, drop NULL. */
+int zero_dropout(const void *x, const void *add, void *out, int64_t count,
+                 zero_dtype dtype, const zero_drop *drop, hipStream_t stream);
+
+/* Bytes of workspace that zero_head_loss needs for these sizes, with either
+ * gradient or not. piece_rows as there. Host only. */
+int zero_head_loss_workspace(int64_t count, int64_t vocab, int64_t width,
+                             zero_dtype dtype, int32_t grad_hidden,
+                             int32_t grad_table, zero_dtype table_grad_dtype,
+                             int64_t piece_rows, int64_t *bytes);
+
+/* Softmax cross entropy of hidden[i] (count x width) against the rows of table
+ * (vocab x width), both `dtype`, with z_iv = hidden[i] . table[v], y = targets:
+ *   losses[i] = log(sum over v of exp(z_iv)) - z_iy
+ *   loss      = sum of w_i * losses[i]  (/ sum of w_i with mean != 0)
+ *   G_iv      = grad_scale * w_i (/ sum of w_i) * (softmax(z_i)_v - [v == y_i])
+ *   grad_hidden[i] = sum over v of G_iv * table[v]                (dtype)
+ *   grad_table[v]  = sum over i of G_iv * hidden[i]   (table_grad_dtype)
+ * the last added to what grad_table holds with accumulate != 0. weights: count
+ * floats, or NULL for 1. Rows whose target lies outside [0, vocab), or whose
+ * weight is 0, take no part, whatever their hidden states hold: their loss and
+ * gradient are 0, and with mean a sum of weights of 0 counts as 1. losses,
+ * grad_hidden and grad_table may each be NULL and are then not computed.
+ *
+ * The logits are never kept: rows are worked through in pieces of piece_rows
+ * (0: as many as need a GiB for one number of `dtype` each against the whole
+ * vocabulary), whose exponentials are turned into G and multiplied before the
+ * next piece's. Products add in binary32; G is rounded to `dtype` before it is
+ * multiplied, so with bf16 operands an fp32 grad_table is a sum of products
+ * whose one factor was rounded to 8 bits. Results depend on piece_rows in
+ * their last bits. EINVAL: as above, grad_scale not finite, piece_rows < 0, a
+ * workspace too small or not 256-byte aligned, overlapping buffers.
+ * EUNSUPPORTED: rows of width or vocab elements of 4 MiB or more, pieces of
+ * that many rows. */
+int zero_head_loss(const void *hidden, const void *table, zero_dtype dtype,
+                   const void *targets, int32_t id_bytes, int64_t count,
+                   int64_t vocab, int64_t width, const float *weights,
+                   int32_t mean, double grad_scale, float *loss,
+                   float *losses, void *grad_hidden, void *grad_table,
+                   zero_dtype table_grad_dtype, int32_t accumulate,
+                   int64_t piece_rows, void *workspace,
+                   int64_t workspace_bytes, hipStream_t stream);
+
 /* Copy the fp32 state out of / into the context (checkpoint and resume):
  * the master copy of this rank's slice and the two moments that [ZeRO and
  * FSDP], ZeroAdam constructor, creates per rank (master = the slice of the

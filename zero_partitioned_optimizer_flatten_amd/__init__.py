@@ -775,3 +775,6 @@ class AdamWState(FsdpShardState):
                     m=share(ptr[1], n, "|u1").view(torch.float8_e4m3fn),
                     r=share(ptr[2], n, "|u1").view(torch.float8_e4m3fn),
                     scale=share(ptr[3], n // 16, "|u1").view(torch.float8_e8m0fnu).view(-1, 2, 64))
+
+
+from .vocab import Dropout, dropout, embed, embed_grad, head_loss  # noqa: E402,F401

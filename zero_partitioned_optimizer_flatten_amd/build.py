@@ -8,7 +8,8 @@ import sys
 HERE = os.path.dirname(os.path.abspath(__file__))
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libzero.so")
-SOURCES = ["zero_api.hip", "zero_kernels.hip", "adamw_kernels.hip"]
+SOURCES = ["zero_api.hip", "zero_kernels.hip", "adamw_kernels.hip", "vocab_api.hip",
+           "vocab_kernels.hip", "head_kernels.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 # Numerics: no implicit fusion, correctly rounded fp32 divide and sqrt,
@@ -38,7 +39,7 @@ def asm(out_dir: str) -> None:
     """Write the gfx950 assembly of the kernels (for inspection)."""
     os.makedirs(out_dir, exist_ok=True)
     flags = [f for f in FLAGS if f not in ("-shared", "-fPIC")]
-    for name in ("zero_kernels", "adamw_kernels"):
+    for name in ("zero_kernels", "adamw_kernels", "vocab_kernels", "head_kernels"):
         subprocess.check_call([HIPCC, *flags, "--cuda-device-only", "-S",
                                os.path.join(CSRC, name + ".hip"),
                                "-o", os.path.join(out_dir, name + ".s")])

@@ -1,0 +1,691 @@
+// Softmax cross entropy of hidden states against a vocabulary table, with the
+// gradients of both, for gfx950.
+//
+//   z_iv = h_i . W_v,  l_i = log sum_v exp(z_iv) - z_iy
+//   G_iv = w_i (exp(z_iv) / sum_u exp(z_iu) - [v = y]),  dh_i = s sum_v G_iv W_v,
+//   dW_v = s sum_i G_iv h_i
+//
+// Three products of rows with rows (both operands' long axis contiguous) on the
+// matrix cores, tile by tile through LDS. The first one's epilogue takes each
+// tile's maximum and sum of exponentials per row, in binary32 from the
+// accumulators, and leaves e = exp(z - its tile's maximum) instead of z: e needs
+// 2 bytes where z would need 4 for the same p, for e's relative error is p's.
+// With the row's maximum and sum known, one pass turns e into G, the operand of
+// the other two products. w are the weights over the largest, and s the rest of
+// the gradient's scale, which multiplies the products' binary32 sums: rounded to
+// bf16 with s inside, the -s of the many entries with p = 0 would all be off by
+// the same; so they are -1 and exact. Rows that take
+// no part (target outside the table, weight 0) are left out of all products.
+#include "vocab_internal.h"
+
+namespace zk {
+namespace {
+
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((address_space(3))) void lds_void;
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr double kLn2 = 0.693147180559945309417;
+// e of bf16 operands is held in fp16 as e * 2^15: 11 bits for e >= 2^-29, and
+// what is below 2^-40 of its tile's largest becomes zero.
+constexpr float kScaleLog2 = 15.0f;
+
+__host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+__host__ __device__ constexpr int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+__device__ __forceinline__ uint16_t narrow(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+__device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+
+template <bool BF16> struct Elem { using type = float; };
+template <> struct Elem<true> { using type = uint16_t; };
+
+__device__ __forceinline__ int64_t load_id(const void *ids, bool wide, int64_t i) {
+    return wide ? static_cast<const int64_t *>(ids)[i] : (int64_t) static_cast<const int32_t *>(ids)[i];
+}
+
+// Whether row i has a loss.
+__device__ __forceinline__ bool takes_part(const HeadArgs &a, int64_t i) {
+    return (uint64_t)load_id(a.targets, a.wide_ids, i) < (uint64_t)a.vocab && !(a.weights && a.weights[i] == 0.0f);
+}
+
+__device__ __forceinline__ int piece_rows(const HeadSums *s, int64_t first, int64_t piece) {
+    const int64_t n = s->rows - first;
+    return (int)(n < 0 ? 0 : n < piece ? n : piece);
+}
+
+// ------------------------------------------------------- which rows
+// One workgroup: the rows that take part, in order, and their weights' sum.
+__global__ void __launch_bounds__(1024) rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map) {
+    __shared__ int32_t found[16];
+    __shared__ double parts[16];
+    __shared__ float tops[16];
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    int64_t base = 0;
+    double weight = 0.0;
+    float most = 0.0f;
+    for (int64_t i0 = 0; i0 < a.count; i0 += 1024) {
+        const int64_t i = i0 + threadIdx.x;
+        bool on = false;
+        if (i < a.count) {
+            on = takes_part(a, i);
+            if (on) {
+                const float w = a.weights ? a.weights[i] : 1.0f;
+                weight += (double)w;
+                most = fmaxf(most, fabsf(w));
+            }
+        }
+        const uint64_t mask = __ballot(on);
+        if (lane == 0) found[wave] = __popcll(mask);
+        __syncthreads();
+        int64_t at = base;
+        for (int w = 0; w < 16; ++w) {
+            if (w < wave) at += found[w];
+            base += found[w];
+        }
+        if (on) map[at + __popcll(mask & ((1ull << lane) - 1))] = (int32_t)i;
+        __syncthreads();
+    }
+    for (int s = 32; s; s /= 2) {
+        weight += __shfl_xor(weight, s);
+        most = fmaxf(most, __shfl_xor(most, s));
+    }
+    if (lane == 0) parts[wave] = weight, tops[wave] = most;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        weight = 0.0;
+        for (int w = 0; w < 16; ++w) {
+            weight += parts[w];
+            most = fmaxf(most, tops[w]);
+        }
+        if (!(most > 0.0f)) most = 1.0f;
+        sums->weight = weight;
+        sums->rows = base;
+        sums->most = most;
+        sums->scale = (float)((double)a.grad_scale * (double)most / (a.mean && weight != 0.0 ? weight : 1.0));
+    }
+}
+
+// ------------------------------------------------------- copies
+// dst [rows_p][cols_p] = the mapped rows of src [.][cols], zeros behind them.
+// A row of threads to a destination row.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+pack_kernel(const void *src, int64_t rows, int64_t cols, const int32_t *map, const HeadSums *sums,
+            int64_t first, void *dst, int64_t rows_p, int64_t cols_p) {
+    using T = typename Elem<BF16>::type;
+    const int64_t r = blockIdx.x;
+    const int64_t n = map ? piece_rows(sums, first, rows) : rows;
+    if (r >= n && r >= round_up(n, 64)) return;
+    const int64_t from = r < n ? (map ? map[first + r] : r) : -1;
+    const T *s = static_cast<const T *>(src) + from * cols;
+    T *d = static_cast<T *>(dst) + r * cols_p;
+    constexpr int V = 16 / sizeof(T);
+    for (int64_t c = (int64_t)threadIdx.x * V; c < cols_p; c += 256 * V) {
+        T x[V];
+        if (from >= 0 && c + V <= cols) {
+            __builtin_memcpy(x, s + c, sizeof x);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[k] = from >= 0 && c + k < cols ? s[c + k] : (T)0;
+        }
+        __builtin_memcpy(__builtin_assume_aligned(d + c, 16), x, sizeof x);
+    }
+}
+
+// dst [cols][rows_p] = the transpose of the mapped rows of src [.][cols], zeros
+// behind them. 64 x 64 elements to a workgroup, through LDS.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+transpose_kernel(const void *src, int64_t rows, int64_t cols, const int32_t *map, const HeadSums *sums,
+                 int64_t first, void *dst, int64_t rows_p) {
+    using T = typename Elem<BF16>::type;
+    __shared__ T tile[64][64 + 4 / sizeof(T)];
+    const int64_t n = map ? piece_rows(sums, first, rows) : rows;
+    const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
+    if (map && r0 >= round_up(n, 64)) return;
+    const int x = threadIdx.x % 64, y = threadIdx.x / 64;
+    for (int k = y; k < 64; k += 4) {
+        const int64_t r = r0 + k, c = c0 + x;
+        T v = 0;
+        if (r < n && c < cols) v = static_cast<const T *>(src)[(map ? map[first + r] : r) * cols + c];
+        tile[k][x] = v;
+    }
+    __syncthreads();
+    for (int k = y; k < 64; k += 4)
+        if (c0 + k < cols && r0 + x < rows_p) static_cast<T *>(dst)[(c0 + k) * rows_p + r0 + x] = tile[x][k];
+}
+
+// ------------------------------------------------------- the product
+// out[q][p] = sum_k P[p][k] Q[q][k]; rows of P and Q are 16-byte aligned and
+// their long axis is a whole number of 128-byte steps. A workgroup makes BP x BQ
+// outputs with WP x WQ waves; a step of both operands' rows, 128 bytes each, goes
+// straight from memory to LDS while the step before it is multiplied.
+//
+// LDS holds a row's 128 bytes as eight 16-byte chunks, chunk c at place
+// c ^ (row % 8): then the 16 rows that a fragment reads at one chunk lie on
+// different banks. A load to LDS writes lane after lane, so the exchange is made
+// in the addresses it reads from.
+
+enum Epilogue { kLogits, kStore };
+
+struct Product {
+    const void *p, *q;
+    int64_t ldp, ldq;             // bytes
+    int64_t np, nq;               // rows
+    int64_t steps;                // of 128 bytes on the long axis
+    int tiles_p, tiles_q, splits;
+    // with sums: rows of the piece, which bound nq or the long axis
+    const HeadSums *sums;
+    int64_t first, piece;
+    bool piece_is_q, piece_is_k;
+    int esize;
+    // kLogits
+    const void *targets;
+    bool wide_ids;
+    const int32_t *map;           // also of kStore's rows, if there
+    f32x2 *stat;
+    HeadRow *row;
+    int64_t subtiles;
+    void *e;                      // null: not wanted
+    int64_t lde;                  // elements
+    // kStore: out (binary32 `f32`, or `out` in its type) = product + f32_in + old out
+    float *f32;
+    int64_t f32_split;            // elements between splits
+    const float *f32_in;
+    void *out;
+    bool out_bf16, add_out;
+    int64_t ldo;                  // elements, of f32, f32_in and out
+};
+
+template <bool BF16> struct Frag { using type = f32x4; };
+template <> struct Frag<true> { using type = bf16x8; };
+
+// 16 x 16 outputs from 16 bytes a lane: lanes 16g..16g+15 hold 16 rows' g-th
+// chunk. binary32 takes four instructions, the k-th on every chunk's k-th number.
+__device__ __forceinline__ f32x4 mma(bf16x8 p, bf16x8 q, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(p, q, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma(f32x4 p, f32x4 q, f32x4 c) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) c = __builtin_amdgcn_mfma_f32_16x16x4f32(p[k], q[k], c, 0, 0, 0);
+    return c;
+}
+
+template <bool BF16, int EPI, int BP, int BQ, int WP, int WQ>
+__device__ __forceinline__ void product(const Product &g) {
+    constexpr int kWaves = WP * WQ;
+    constexpr int kI = BP / WP / 16, kJ = BQ / WQ / 16;       // fragments of a wave
+    constexpr int kLoadsP = BP / 8 / kWaves, kLoadsQ = BQ / 8 / kWaves;
+    static_assert(kLoadsP * 8 * kWaves == BP && kLoadsQ * 8 * kWaves == BQ, "whole loads");
+    constexpr int kStage = (BP + BQ) * 128;
+    using F = typename Frag<BF16>::type;
+    __shared__ __align__(1024) char lds[2][kStage];
+
+    const int lane = threadIdx.x % 64;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    int64_t nq = g.nq, steps = g.steps;
+    if (g.sums) {
+        const int n = piece_rows(g.sums, g.first, g.piece);
+        if (g.piece_is_q) nq = n;
+        if (g.piece_is_k) steps = ceil_div((int64_t)n * g.esize, 128);
+    }
+
+    // Workgroups go round robin over the 8 XCDs: give each XCD a run of
+    // neighbouring tiles, in groups of 8 along p, so that its L2 is shared.
+    const int tiles = g.tiles_p * g.tiles_q;
+    const int split = blockIdx.x / tiles;
+    int t = blockIdx.x % tiles;
+    {
+        const int per = tiles / 8, rest = tiles % 8, x = t % 8;
+        t = x * per + (x < rest ? x : rest) + t / 8;
+    }
+    const int group = t / (8 * g.tiles_q), in = t % (8 * g.tiles_q);
+    const int gp = g.tiles_p - 8 * group < 8 ? g.tiles_p - 8 * group : 8;
+    const int64_t p0 = (int64_t)(8 * group + in % gp) * BP, q0 = (int64_t)(in / gp) * BQ;
+    if (q0 >= nq) return;
+    const int64_t per_split = ceil_div(steps, g.splits);
+    const int64_t k0 = per_split * split;
+    const int ksteps = (int)(k0 >= steps ? 0 : steps - k0 < per_split ? steps - k0 : per_split);
+
+    // Rows behind the last are read as the last: always memory of the operand.
+    int vp[kLoadsP], vq[kLoadsQ];
+    const int chunk = (lane % 8) ^ (lane / 8);
+#pragma unroll
+    for (int j = 0; j < kLoadsP; ++j) {
+        int64_t r = (wave * kLoadsP + j) * 8 + lane / 8;
+        if (p0 + r >= g.np) r = g.np - 1 - p0;
+        vp[j] = (int)(r * g.ldp) + chunk * 16;
+    }
+#pragma unroll
+    for (int j = 0; j < kLoadsQ; ++j) {
+        int64_t r = (wave * kLoadsQ + j) * 8 + lane / 8;
+        if (q0 + r >= nq) r = nq - 1 - q0;
+        vq[j] = (int)(r * g.ldq) + chunk * 16;
+    }
+    const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char *>(static_cast<const char *>(g.p) + p0 * g.ldp + k0 * 128), (short)0, 0xFFFFFFFF, 0x00027000);
+    const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
+        const_cast<char *>(static_cast<const char *>(g.q) + q0 * g.ldq + k0 * 128), (short)0, 0xFFFFFFFF, 0x00027000);
+
+    auto load = [&](int k, int buf) {
+        char *s = lds[buf];
+#pragma unroll
+        for (int j = 0; j < kLoadsP; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (lds_void *)(s + (wave * kLoadsP + j) * 1024), 16, vp[j],
+                                                     k * 128, 0, 0);
+#pragma unroll
+        for (int j = 0; j < kLoadsQ; ++j)
+            __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_void *)(s + BP * 128 + (wave * kLoadsQ + j) * 1024), 16,
+                                                     vq[j], k * 128, 0, 0);
+    };
+
+    f32x4 acc[kI][kJ];
+#pragma unroll
+    for (int i = 0; i < kI; ++i)
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+
+    const int wp = wave / WQ, wq = wave % WQ;
+    const int rowp = (wp * (BP / WP) + lane % 16) * 128, rowq = (BP + wq * (BQ / WQ) + lane % 16) * 128;
+    const int off0 = ((lane / 16) ^ (lane % 8)) * 16, off1 = ((4 + lane / 16) ^ (lane % 8)) * 16;
+
+    if (ksteps > 0) load(0, 0);
+    for (int k = 0; k < ksteps; ++k) {
+        __builtin_amdgcn_s_waitcnt(0x0F70);                   // vmcnt(0): this wave's loads
+        __syncthreads();                                      // everyone's; and step k - 1 is used up
+        if (k + 1 < ksteps) load(k + 1, (k + 1) & 1);
+        const char *s = lds[k & 1];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int off = h ? off1 : off0;
+            F fp[kI], fq[kJ];
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) fq[j] = *reinterpret_cast<const F *>(s + rowq + j * 2048 + off);
+#pragma unroll
+            for (int i = 0; i < kI; ++i) fp[i] = *reinterpret_cast<const F *>(s + rowp + i * 2048 + off);
+#pragma unroll
+            for (int i = 0; i < kI; ++i)
+#pragma unroll
+                for (int j = 0; j < kJ; ++j) acc[i][j] = mma(fp[i], fq[j], acc[i][j]);
+        }
+    }
+
+    // A lane holds outputs p = pw + 16 i + r, r < 4, of q = qw + 16 j.
+    const float scale = EPI == kStore ? g.sums->scale : 1.0f;
+    const int64_t pw = p0 + wp * (BP / WP) + lane / 16 * 4, qw = q0 + wq * (BQ / WQ) + lane % 16;
+#pragma unroll
+    for (int j = 0; j < kJ; ++j) {
+        const int64_t q = qw + 16 * j;
+        if (EPI == kLogits) {
+            const bool on = q < nq;
+            const int64_t y = on ? load_id(g.targets, g.wide_ids, g.map[g.first + q]) : -1;
+            float top = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kI; ++i)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const int64_t p = pw + 16 * i + r;
+                    const float z = p < g.np ? acc[i][j][r] * kLog2e : -INFINITY;
+                    acc[i][j][r] = z;
+                    top = fmaxf(top, z);
+                    if (p == y) g.row[q].target = z;
+                }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            const float base = top == -INFINITY ? 0.0f : top;
+            float sum = 0.0f;
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+                const int64_t p = pw + 16 * i;
+                float e[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    e[r] = __builtin_amdgcn_exp2f(acc[i][j][r] - base + (BF16 ? kScaleLog2 : 0.0f));
+                    sum += e[r];
+                }
+                if (g.e && on && p < g.lde) {
+                    if (BF16) {
+                        __attribute__((ext_vector_type(4))) _Float16 h = {(_Float16)e[0], (_Float16)e[1], (_Float16)e[2],
+                                                                          (_Float16)e[3]};
+                        *reinterpret_cast<decltype(h) *>(static_cast<_Float16 *>(g.e) + q * g.lde + p) = h;
+                    } else {
+                        *reinterpret_cast<f32x4 *>(static_cast<float *>(g.e) + q * g.lde + p) = f32x4{e[0], e[1], e[2], e[3]};
+                    }
+                }
+            }
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (on && lane < 16)
+                g.stat[q * g.subtiles + (p0 / (BP / WP) + wp)] = f32x2{top, BF16 ? sum * 0x1p-15f : sum};
+        } else {
+            if (q >= nq) continue;
+            const int64_t row = g.map && g.out && !g.f32 ? (int64_t)g.map[g.first + q] : q;
+#pragma unroll
+            for (int i = 0; i < kI; ++i) {
+                const int64_t p = pw + 16 * i;
+                if (p >= g.np) continue;
+                const int64_t left = g.np - p, at = row * g.ldo + p;
+                float v[4];
+#pragma unroll
+                for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r] * scale;
+                if (g.f32_in)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (r < left) v[r] += g.f32_in[at + r];
+                if (g.add_out)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (r < left)
+                            v[r] += g.out_bf16 ? widen(static_cast<const uint16_t *>(g.out)[at + r])
+                                               : static_cast<const float *>(g.out)[at + r];
+                if (g.f32) {
+                    float *d = g.f32 + split * g.f32_split + at;
+                    if (left >= 4) __builtin_memcpy(d, v, sizeof v);
+                    else
+                        for (int r = 0; r < 4; ++r)
+                            if (r < left) d[r] = v[r];
+                } else if (g.out_bf16) {
+                    uint16_t *d = static_cast<uint16_t *>(g.out) + at, h[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) h[r] = narrow(v[r]);
+                    if (left >= 4) __builtin_memcpy(d, h, sizeof h);
+                    else
+                        for (int r = 0; r < 4; ++r)
+                            if (r < left) d[r] = h[r];
+                } else {
+                    float *d = static_cast<float *>(g.out) + at;
+                    if (left >= 4) __builtin_memcpy(d, v, sizeof v);
+                    else
+                        for (int r = 0; r < 4; ++r)
+                            if (r < left) d[r] = v[r];
+                }
+            }
+        }
+    }
+}
+
+template <bool BF16, int EPI, int BP, int BQ, int WP, int WQ>
+__global__ void __launch_bounds__(64 * WP * WQ, 2) product_kernel(Product g) {
+    product<BF16, EPI, BP, BQ, WP, WQ>(g);
+}
+
+// ------------------------------------------------------- the softmax
+// A wave to a row: its maximum and sum from its tiles', and its loss.
+__global__ void __launch_bounds__(256)
+softmax_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t first, int64_t piece,
+               const f32x2 *stat, int64_t subtiles, HeadRow *rows, float *losses) {
+    const int lane = threadIdx.x % 64;
+    const int64_t q = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    if (q >= piece_rows(sums, first, piece)) return;
+    const f32x2 *s = stat + q * subtiles;
+    float top = -INFINITY;
+    for (int64_t k = lane; k < subtiles; k += 64) top = fmaxf(top, s[k].x);
+    for (int d = 32; d; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
+    const float base = top == -INFINITY ? 0.0f : top;
+    float sum = 0.0f;
+    for (int64_t k = lane; k < subtiles; k += 64) sum += s[k].y * __builtin_amdgcn_exp2f(s[k].x - base);
+    for (int d = 32; d; d /= 2) sum += __shfl_xor(sum, d);
+    if (lane) return;
+    const int64_t i = map[first + q];
+    const float w = a.weights ? a.weights[i] : 1.0f;
+    const float share = w / sums->most;
+    // top - target first: exact where the target is the largest, which is where
+    // the loss is small
+    losses[i] = (float)(((double)(base - rows[q].target) + (double)__builtin_amdgcn_logf(sum)) * kLn2);
+    rows[q].top = base;
+    rows[q].inv = share / sum;
+    rows[q].share = share;
+}
+
+// One workgroup: the weighted sum of the losses, in binary64.
+__global__ void __launch_bounds__(1024)
+loss_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, const float *losses) {
+    __shared__ double parts[16];
+    double sum = 0.0;
+    for (int64_t k = threadIdx.x; k < sums->rows; k += 1024) {
+        const int64_t i = map[k];
+        sum += (a.weights ? (double)a.weights[i] : 1.0) * (double)losses[i];
+    }
+    for (int s = 32; s; s /= 2) sum += __shfl_xor(sum, s);
+    if (threadIdx.x % 64 == 0) parts[threadIdx.x / 64] = sum;
+    __syncthreads();
+    if (threadIdx.x == 0) {
+        sum = 0.0;
+        for (int w = 0; w < 16; ++w) sum += parts[w];
+        *a.loss = (float)(a.mean && sums->weight != 0.0 ? sum / sums->weight : sum);
+    }
+}
+
+// losses and rows of grad_hidden that take no part: zero.
+__global__ void __launch_bounds__(256) idle_rows_kernel(HeadArgs a, float *losses) {
+    const int lane = threadIdx.x % 64;
+    const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    if (i >= a.count) return;
+    if (takes_part(a, i)) return;
+    if (lane == 0) losses[i] = 0.0f;
+    if (!a.grad_hidden) return;
+    for (int64_t c = lane; c < a.width; c += 64)
+        if (a.bf16) static_cast<uint16_t *>(a.grad_hidden)[i * a.width + c] = 0;
+        else static_cast<float *>(a.grad_hidden)[i * a.width + c] = 0.0f;
+}
+
+// ------------------------------------------------------- e to G
+// In place, [rows][vocab_p], and transposed, [vocab][piece_p], zeros behind the
+// rows. 64 rows x 64 entries to a workgroup.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t first, int64_t piece,
+                const f32x2 *stat, int64_t subtiles, int sub, const HeadRow *rows, void *e,
+                int64_t vocab_p, void *e_t, int64_t piece_p) {
+    using T = typename Elem<BF16>::type;
+    constexpr int V = 16 / sizeof(T), kPerRow = 64 / V;
+    __shared__ T tile[64][64 + 4 / sizeof(T)];
+    const int n = piece_rows(sums, first, piece);
+    const int64_t v0 = (int64_t)blockIdx.x * 64, q0 = (int64_t)blockIdx.y * 64;
+    if (q0 >= n) return;
+    for (int k = threadIdx.x; k < 64 * kPerRow; k += 256) {
+        const int r = k / kPerRow, c = k % kPerRow * V;
+        const int64_t q = q0 + r, v = v0 + c;
+        T out[V];
+        if (q < n) {
+            const HeadRow s = rows[q];
+            const int64_t y = load_id(a.targets, a.wide_ids, map[first + q]);
+            const float share = __builtin_amdgcn_exp2f(stat[q * subtiles + v / sub].x - s.top) * s.inv
+                                * (BF16 ? 0x1p-15f : 1.0f);
+            T *at = static_cast<T *>(e) + q * vocab_p + v;
+            if (BF16) {
+                _Float16 h[V];
+                __builtin_memcpy(h, __builtin_assume_aligned(at, 16), sizeof h);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float x = (float)h[j] * share;
+                    if (v + j == y) x -= s.share;
+                    out[j] = (T)narrow(v + j < a.vocab ? x : 0.0f);
+                }
+            } else {
+                float h[V];
+                __builtin_memcpy(h, __builtin_assume_aligned(at, 16), sizeof h);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    float x = h[j] * share;
+                    if (v + j == y) x -= s.share;
+                    out[j] = (T)(v + j < a.vocab ? x : 0.0f);
+                }
+            }
+            __builtin_memcpy(__builtin_assume_aligned(at, 16), out, sizeof out);
+        } else {
+#pragma unroll
+            for (int j = 0; j < V; ++j) out[j] = 0;
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) tile[r][c + j] = out[j];
+    }
+    if (!e_t) return;
+    __syncthreads();
+    const int x = threadIdx.x % 64;
+    for (int k = threadIdx.x / 64; k < 64; k += 4)
+        if (v0 + k < a.vocab) static_cast<T *>(e_t)[(v0 + k) * piece_p + q0 + x] = tile[x][k];
+}
+
+// grad_hidden from the binary32 parts of the split product.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+join_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t first, int64_t piece,
+            const float *parts, int splits, int64_t stride) {
+    const int64_t q = blockIdx.x;
+    if (q >= piece_rows(sums, first, piece)) return;
+    const int64_t row = map[first + q];
+    for (int64_t c = threadIdx.x; c < a.width; c += 256) {
+        float v = 0.0f;
+        for (int s = 0; s < splits; ++s) v += parts[s * stride + q * a.width + c];
+        if (BF16) static_cast<uint16_t *>(a.grad_hidden)[row * a.width + c] = narrow(v);
+        else static_cast<float *>(a.grad_hidden)[row * a.width + c] = v;
+    }
+}
+
+// ------------------------------------------------------- launches
+template <bool BF16, int EPI>
+void start_product(const Product &g, int shape, hipStream_t stream) {
+    const dim3 grid((unsigned)(g.tiles_p * g.tiles_q * g.splits));
+    if (shape == 0) product_kernel<BF16, EPI, 256, 256, 2, 4><<<grid, 512, 0, stream>>>(g);
+    else if (shape == 1) product_kernel<BF16, EPI, 128, 128, 2, 2><<<grid, 256, 0, stream>>>(g);
+    else product_kernel<BF16, EPI, 128, 32, 4, 1><<<grid, 256, 0, stream>>>(g);
+}
+
+void set_tiles(Product &g, int shape, int splits) {
+    g.tiles_p = (int)ceil_div(g.np, kTiles[shape].p);
+    g.tiles_q = (int)ceil_div(g.nq, kTiles[shape].q);
+    g.splits = splits;
+}
+
+template <bool BF16>
+hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
+    char *w = a.workspace;
+    const int es = BF16 ? 2 : 4;
+    auto *sums = reinterpret_cast<HeadSums *>(w + p.sum_off);
+    auto *map = reinterpret_cast<int32_t *>(w + p.map_off);
+    auto *losses = a.losses ? a.losses : reinterpret_cast<float *>(w + p.loss_off);
+    auto *rows = reinterpret_cast<HeadRow *>(w + p.row_off);
+    auto *stat = reinterpret_cast<f32x2 *>(w + p.stat_off);
+    const bool grads = a.grad_hidden || a.grad_table;
+    rows_kernel<<<1, 1024, 0, stream>>>(a, sums, map);
+    if (a.count > 0) idle_rows_kernel<<<(unsigned)ceil_div(a.count, 4), 256, 0, stream>>>(a, losses);
+    const void *table = a.table;
+    if (p.pack_table) {
+        pack_kernel<BF16><<<(unsigned)a.vocab, 256, 0, stream>>>(a.table, a.vocab, a.width, nullptr, nullptr, 0,
+                                                                 w + p.table_off, a.vocab, p.width_p);
+        table = w + p.table_off;
+    }
+    if (a.grad_hidden)
+        transpose_kernel<BF16><<<dim3((unsigned)ceil_div(p.vocab_p, 64), (unsigned)ceil_div(a.width, 64)), 256, 0, stream>>>(
+            a.table, a.vocab, a.width, nullptr, nullptr, 0, w + p.table_t_off, p.vocab_p);
+    for (int64_t k = 0; k < p.pieces; ++k) {
+        const int64_t first = k * p.piece;
+        pack_kernel<BF16><<<(unsigned)p.piece_p, 256, 0, stream>>>(a.hidden, p.piece, a.width, map, sums, first,
+                                                                   w + p.hidden_off, p.piece_p, p.width_p);
+        Product g = {};
+        g.sums = sums;
+        g.first = first;
+        g.piece = p.piece;
+        g.esize = es;
+        g.map = map;
+        g.p = table;
+        g.ldp = p.width_p * es;
+        g.np = a.vocab;
+        g.q = w + p.hidden_off;
+        g.ldq = p.width_p * es;
+        g.nq = p.piece;
+        g.piece_is_q = true;
+        g.steps = p.width_p * es / 128;
+        g.targets = a.targets;
+        g.wide_ids = a.wide_ids;
+        g.stat = stat;
+        g.row = rows;
+        g.subtiles = p.subtiles;
+        g.e = grads ? w + p.e_off : nullptr;
+        g.lde = p.vocab_p;
+        set_tiles(g, p.tile_logits, 1);
+        start_product<BF16, kLogits>(g, p.tile_logits, stream);
+        softmax_kernel<<<(unsigned)ceil_div(p.piece, 4), 256, 0, stream>>>(a, sums, map, first, p.piece, stat,
+                                                                           p.subtiles, rows, losses);
+        if (!grads) continue;
+        gradient_kernel<BF16><<<dim3((unsigned)(p.vocab_p / 64), (unsigned)ceil_div(p.piece, 64)), 256, 0, stream>>>(
+            a, sums, map, first, p.piece, stat, p.subtiles, p.sub, rows, w + p.e_off, p.vocab_p,
+            a.grad_table ? w + p.e_t_off : nullptr, p.piece_p);
+        if (a.grad_hidden) {
+            Product h = {};
+            h.sums = sums;
+            h.first = first;
+            h.piece = p.piece;
+            h.esize = es;
+            h.p = w + p.table_t_off;
+            h.ldp = p.vocab_p * es;
+            h.np = a.width;
+            h.q = w + p.e_off;
+            h.ldq = p.vocab_p * es;
+            h.nq = p.piece;
+            h.piece_is_q = true;
+            h.steps = p.vocab_p * es / 128;
+            h.ldo = a.width;
+            if (p.splits > 1) {
+                h.f32 = reinterpret_cast<float *>(w + p.split_off);
+                h.f32_split = p.piece * a.width;
+            } else {
+                h.map = map;
+                h.out = a.grad_hidden;
+                h.out_bf16 = BF16;
+            }
+            set_tiles(h, p.tile_hidden, p.splits);
+            start_product<BF16, kStore>(h, p.tile_hidden, stream);
+            if (p.splits > 1)
+                join_kernel<BF16><<<(unsigned)p.piece, 256, 0, stream>>>(a, sums, map, first, p.piece, h.f32, p.splits,
+                                                                         h.f32_split);
+        }
+        if (a.grad_table) {
+            transpose_kernel<BF16><<<dim3((unsigned)ceil_div(p.piece_p, 64), (unsigned)ceil_div(a.width, 64)), 256, 0, stream>>>(
+                a.hidden, p.piece, a.width, map, sums, first, w + p.hidden_t_off, p.piece_p);
+            Product t = {};
+            t.sums = sums;
+            t.first = first;
+            t.piece = p.piece;
+            t.esize = es;
+            t.p = w + p.hidden_t_off;
+            t.ldp = p.piece_p * es;
+            t.np = a.width;
+            t.q = w + p.e_t_off;
+            t.ldq = p.piece_p * es;
+            t.nq = a.vocab;
+            t.piece_is_k = true;
+            t.ldo = a.width;
+            const bool last = k + 1 == p.pieces;
+            float *gw = a.table_grad_bf16 ? reinterpret_cast<float *>(w + p.gw_off) : static_cast<float *>(a.grad_table);
+            if (a.table_grad_bf16 && last) {
+                t.out = a.grad_table;
+                t.out_bf16 = true;
+                t.add_out = a.accumulate;
+                t.f32_in = k > 0 ? gw : nullptr;
+            } else {
+                t.f32 = gw;
+                t.f32_in = k > 0 || (!a.table_grad_bf16 && a.accumulate) ? gw : nullptr;
+            }
+            set_tiles(t, p.tile_table, 1);
+            start_product<BF16, kStore>(t, p.tile_table, stream);
+        }
+    }
+    loss_kernel<<<1, 1024, 0, stream>>>(a, sums, map, losses);
+    return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
+    return a.bf16 ? head<true>(a, p, stream) : head<false>(a, p, stream);
+}
+
+}  // namespace zk

@@ -1,0 +1,403 @@
+// Host side of the vocabulary operators: argument checks, workspace sizes and
+// dispatch. The C ABI is declared and documented in include/zero.h.
+#include <hip/hip_runtime.h>
+
+#include <cmath>
+
+#include "../../include/zero.h"
+#include "vocab_internal.h"
+
+namespace {
+
+using zk::CaptureScope;
+using zk::check_range;
+using zk::fail;
+using zk::hip_fail;
+
+bool valid_dtype(zero_dtype d) { return d == ZERO_F32 || d == ZERO_BF16; }
+int64_t dtype_size(zero_dtype d) { return d == ZERO_BF16 ? 2 : 4; }
+
+// Rows are addressed by 32-bit offsets inside a tile of 256 of them.
+constexpr int64_t kMaxRowBytes = (int64_t)1 << 22;
+// A dispatch holds fewer than 2^32 work-items.
+constexpr int64_t kMaxUnits = 0xFFFFFF00ll;
+constexpr int64_t kMaxInt = 0x7FFFFFFF;
+constexpr int64_t kMaxRows = (int64_t)1 << 30, kMaxElements = (int64_t)1 << 42;
+
+int64_t ceil_div(int64_t a, int64_t b) { return a / b + (a % b != 0); }
+
+// A buffer of count elements of `size` bytes: there, aligned, long enough.
+int check_buffer(const void *p, int64_t count, int64_t size, const char *what) {
+    if (count == 0) return ZERO_OK;
+    if (!p) return fail(ZERO_EINVAL, "%s is null", what);
+    if ((uintptr_t)p % (uintptr_t)size)
+        return fail(ZERO_EINVAL, "%s is not %lld-byte aligned", what, (long long)size);
+    return check_range(p, count * size, what);
+}
+
+int check_ids(const void *ids, int32_t id_bytes, int64_t count, const char *what) {
+    if (id_bytes != 4 && id_bytes != 8)
+        return fail(ZERO_EINVAL, "%s: ids have 4 or 8 bytes (got %d)", what, id_bytes);
+    return check_buffer(ids, count, id_bytes, what);
+}
+
+int check_table(int64_t rows, int64_t width, const char *what) {
+    if (rows < 1 || width < 1)
+        return fail(ZERO_EINVAL, "%s must have rows and columns (got %lld x %lld)", what, (long long)rows,
+                    (long long)width);
+    if (rows > kMaxRows || width > kMaxRows || rows > kMaxElements / width)
+        return fail(ZERO_EUNSUPPORTED, "%s of %lld x %lld: more than 2^30 rows or columns, or 2^42 elements", what,
+                    (long long)rows, (long long)width);
+    return ZERO_OK;
+}
+
+int check_count(int64_t count, int64_t width) {
+    if (count < 0) return fail(ZERO_EINVAL, "count must be >= 0 (got %lld)", (long long)count);
+    if (count > kMaxInt || count * ceil_div(width, 8) > kMaxUnits)
+        return fail(ZERO_EUNSUPPORTED, "%lld rows of %lld elements are more than one call takes", (long long)count,
+                    (long long)width);
+    return ZERO_OK;
+}
+
+// Whether the `na` bytes at a and the `nb` bytes at b meet.
+bool overlap(const void *a, int64_t na, const void *b, int64_t nb) {
+    const uintptr_t x = (uintptr_t)a, y = (uintptr_t)b;
+    return a && b && na > 0 && nb > 0 && x < y + (uint64_t)nb && y < x + (uint64_t)na;
+}
+
+int check_drop(const zero_drop *d, zk::Drop *out) {
+    *out = {};
+    out->scale = 1.0f;
+    if (!d) return ZERO_OK;
+    if (!(d->p >= 0.0 && d->p <= 1.0)) return fail(ZERO_EINVAL, "dropout: p must be in [0, 1] (got %g)", d->p);
+    const int rc = d->counter ? check_buffer(d->counter, 1, 8, "dropout counter") : ZERO_OK;
+    if (rc) return rc;
+    out->key0 = (uint32_t)d->seed;
+    out->key1 = (uint32_t)(d->seed >> 32);
+    out->limit = (uint32_t)std::floor(d->p * 65536.0 + 0.5);
+    out->scale = out->limit < 65536 ? (float)(65536.0 / (double)(65536 - out->limit)) : 0.0f;
+    out->offset = d->offset;
+    out->counter = d->counter;
+    return ZERO_OK;
+}
+
+int check_scale(double scale) {
+    if (!std::isfinite((float)scale)) return fail(ZERO_EINVAL, "scale must be finite in fp32 (got %g)", scale);
+    return ZERO_OK;
+}
+
+int check_workspace(const void *workspace, int64_t have, int64_t need) {
+    if (have < need)
+        return fail(ZERO_EINVAL, "workspace has %lld bytes, the call needs %lld", (long long)have, (long long)need);
+    if (!workspace) return fail(ZERO_EINVAL, "workspace is null");
+    if ((uintptr_t)workspace % 256) return fail(ZERO_EINVAL, "workspace is not 256-byte aligned");
+    return check_range(workspace, need, "workspace");
+}
+
+int head_sizes(int64_t count, int64_t vocab, int64_t width, zero_dtype dtype, int64_t piece) {
+    int rc = check_table(vocab, width, "table");
+    if (rc) return rc;
+    if (!valid_dtype(dtype)) return fail(ZERO_EINVAL, "unknown dtype %d", (int)dtype);
+    if (count < 0) return fail(ZERO_EINVAL, "count must be >= 0 (got %lld)", (long long)count);
+    if (count > kMaxInt) return fail(ZERO_EUNSUPPORTED, "%lld rows are more than one call takes", (long long)count);
+    if (piece < 0) return fail(ZERO_EINVAL, "piece_rows must be >= 0 (got %lld)", (long long)piece);
+    const int64_t es = dtype_size(dtype);
+    if ((vocab + 128) * es > kMaxRowBytes || (width + 64) * es > kMaxRowBytes)
+        return fail(ZERO_EUNSUPPORTED, "table of %lld x %lld: a row of either length must stay under 4 MiB",
+                    (long long)vocab, (long long)width);
+    if (piece > 0 && ((piece < count ? piece : count) + 64) * es > kMaxRowBytes)
+        return fail(ZERO_EUNSUPPORTED, "pieces of %lld rows: at most 2^20 (fp32) or 2^21 (bf16), less 64",
+                    (long long)piece);
+    return ZERO_OK;
+}
+
+}  // namespace
+
+namespace zk {
+
+EmbedGradPlan plan_embed_grad(int64_t count, int64_t rows, int64_t width) {
+    EmbedGradPlan p;
+    p.sort_groups_log2 = 8;                        // one workgroup to a compute unit
+    while ((rows >> p.sort_groups_log2) >= kSortIds) ++p.sort_groups_log2;
+    p.ids_per_group = (int)ceil_div(rows, (int64_t)1 << p.sort_groups_log2);
+    // About 512 spans, and at most 256 tokens in one: few partial rows for a
+    // run that is the whole batch, enough waves for short batches.
+    int64_t span = count / 512;
+    p.span = (int)(span < 8 ? 8 : span > 256 ? 256 : span);
+    p.spans = ceil_div(count, p.span);
+    const int64_t pitch = ceil_div(width, kSpanCols) * kSpanCols;
+    p.count_off = 0;
+    p.sorted_off = 256;
+    p.partial_off = p.sorted_off + ceil_div(count * (int64_t)sizeof(SortedToken), 256) * 256;
+    p.bytes = p.partial_off + (p.spans > 1 ? 2 * p.spans * pitch * (int64_t)sizeof(float) : 0);
+    return p;
+}
+
+namespace {
+
+int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
+
+// The largest tile that still gives every compute unit one.
+int choose_tile(int64_t np, int64_t nq, int64_t splits) {
+    if (nq <= 32) return 2;
+    if (ceil_div(np, 256) * ceil_div(nq, 256) * splits >= 200) return 0;
+    return 1;
+}
+
+}  // namespace
+
+HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
+    HeadPlan p = {};
+    const int64_t es = a.bf16 ? 2 : 4, step = 128 / es;
+    p.width_p = round_up(a.width, step);
+    p.vocab_p = round_up(a.vocab, 128);
+    p.pack_table = (uintptr_t)a.table % 16 || p.width_p != a.width;
+    // a piece's e takes a GiB at most, and its transpose as much again
+    int64_t piece = rows > 0 ? rows : ((int64_t)1 << 30) / (p.vocab_p * es) / 256 * 256;
+    if (rows <= 0) piece = piece < 256 ? 256 : piece > 262144 ? 262144 : piece;
+    if (piece > a.count) piece = a.count;
+    if (piece < 1) piece = 1;
+    p.piece = piece;
+    p.pieces = a.count > 0 ? ceil_div(a.count, piece) : (a.grad_table ? 1 : 0);
+    p.piece_p = round_up(piece, 64);
+    p.tile_logits = choose_tile(a.vocab, piece, 1);
+    p.sub = kTiles[p.tile_logits].sub;
+    p.subtiles = round_up(a.vocab, kTiles[p.tile_logits].p) / p.sub;
+    p.splits = 1;
+    p.tile_hidden = choose_tile(a.width, piece, 4);
+    const TileShape s = kTiles[p.tile_hidden];
+    const int64_t tiles = ceil_div(a.width, s.p) * ceil_div(piece, s.q), steps = p.vocab_p / step;
+    // enough workgroups for every compute unit, of 16 steps at least
+    while (tiles * p.splits < 256 && steps / (p.splits + 1) >= 16) ++p.splits;
+    p.tile_table = choose_tile(a.width, a.vocab, 1);
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += round_up(bytes, 256);
+        return here;
+    };
+    const bool grads = a.grad_hidden || a.grad_table;
+    p.sum_off = take(sizeof(HeadSums));
+    p.map_off = take(4 * a.count);
+    p.loss_off = a.losses ? -1 : take(4 * a.count);
+    p.row_off = take(sizeof(HeadRow) * piece);
+    p.stat_off = take(8 * piece * p.subtiles);
+    p.hidden_off = take(p.piece_p * p.width_p * es);
+    p.hidden_t_off = a.grad_table ? take(a.width * p.piece_p * es) : -1;
+    p.table_off = p.pack_table ? take(a.vocab * p.width_p * es) : -1;
+    p.table_t_off = a.grad_hidden ? take(a.width * p.vocab_p * es) : -1;
+    p.e_off = grads ? take(piece * p.vocab_p * es) : -1;
+    p.e_t_off = a.grad_table ? take(a.vocab * p.piece_p * es) : -1;
+    p.gw_off = a.grad_table && a.table_grad_bf16 && p.pieces > 1 ? take(4 * a.vocab * a.width) : -1;
+    p.split_off = a.grad_hidden && p.splits > 1 ? take(4 * p.splits * piece * a.width) : -1;
+    p.bytes = at;
+    return p;
+}
+
+}  // namespace zk
+
+extern "C" {
+
+int zero_embed(const void *ids, int32_t id_bytes, int64_t count, const void *table, int64_t rows, int64_t width,
+               zero_dtype dtype, double scale, const void *position_ids, const void *position_table,
+               int64_t position_rows, const zero_drop *drop, void *out, zero_dtype out_dtype, hipStream_t stream) {
+    CaptureScope scope(stream);
+    zk::EmbedArgs a = {};
+    int rc = check_table(rows, width, "table");
+    if (rc) return rc;
+    if (!valid_dtype(dtype) || !valid_dtype(out_dtype)) return fail(ZERO_EINVAL, "unknown dtype");
+    if ((rc = check_count(count, width))) return rc;
+    if ((rc = check_scale(scale))) return rc;
+    if ((rc = check_drop(drop, &a.drop))) return rc;
+    if ((rc = check_ids(ids, id_bytes, count, "ids"))) return rc;
+    if ((rc = check_buffer(table, rows * width, dtype_size(dtype), "table"))) return rc;
+    if (!position_ids != !position_table)
+        return fail(ZERO_EINVAL, "position ids and a position table come together");
+    if (position_ids) {
+        if ((rc = check_table(position_rows, width, "position table"))) return rc;
+        if ((rc = check_ids(position_ids, id_bytes, count, "position ids"))) return rc;
+        if ((rc = check_buffer(position_table, position_rows * width, dtype_size(dtype), "position table"))) return rc;
+    }
+    if ((rc = check_buffer(out, count * width, dtype_size(out_dtype), "out"))) return rc;
+    const int64_t bytes = count * width * dtype_size(out_dtype);
+    if (overlap(out, bytes, table, rows * width * dtype_size(dtype)) || overlap(out, bytes, ids, count * id_bytes) ||
+        overlap(out, bytes, position_table, position_rows * width * dtype_size(dtype)) ||
+        overlap(out, bytes, position_ids, count * id_bytes))
+        return fail(ZERO_EINVAL, "out overlaps an input");
+    a.ids = ids;
+    a.pos_ids = position_ids;
+    a.wide_ids = id_bytes == 8;
+    a.count = count;
+    a.rows = rows;
+    a.pos_rows = position_rows;
+    a.width = width;
+    a.table = table;
+    a.pos_table = position_table;
+    a.table_bf16 = dtype == ZERO_BF16;
+    a.out_bf16 = out_dtype == ZERO_BF16;
+    a.scale = (float)scale;
+    a.out = out;
+    const hipError_t e = zk::launch_embed(a, stream);
+    return e == hipSuccess ? ZERO_OK : hip_fail(e, "zero_embed");
+}
+
+int zero_embed_grad_workspace(int64_t count, int64_t rows, int64_t width, int64_t *bytes) {
+    int rc = check_table(rows, width, "table");
+    if (rc) return rc;
+    if ((rc = check_count(count, width))) return rc;
+    if (!bytes) return fail(ZERO_EINVAL, "null bytes");
+    *bytes = zk::plan_embed_grad(count, rows, width).bytes;
+    return ZERO_OK;
+}
+
+int zero_embed_grad(const void *grad_out, zero_dtype grad_dtype, const void *ids, int32_t id_bytes, int64_t count,
+                    int64_t rows, int64_t width, double scale, const zero_drop *drop, void *grad_table,
+                    zero_dtype table_dtype, int32_t accumulate, void *workspace, int64_t workspace_bytes,
+                    hipStream_t stream) {
+    CaptureScope scope(stream);
+    zk::EmbedGradArgs a = {};
+    int rc = check_table(rows, width, "table");
+    if (rc) return rc;
+    if (!valid_dtype(grad_dtype) || !valid_dtype(table_dtype)) return fail(ZERO_EINVAL, "unknown dtype");
+    if ((rc = check_count(count, width))) return rc;
+    if ((rc = check_scale(scale))) return rc;
+    if ((rc = check_drop(drop, &a.drop))) return rc;
+    if ((rc = check_ids(ids, id_bytes, count, "ids"))) return rc;
+    if ((rc = check_buffer(grad_out, count * width, dtype_size(grad_dtype), "grad_out"))) return rc;
+    if ((rc = check_buffer(grad_table, rows * width, dtype_size(table_dtype), "grad_table"))) return rc;
+    const int64_t bytes = rows * width * dtype_size(table_dtype);
+    if (overlap(grad_table, bytes, grad_out, count * width * dtype_size(grad_dtype)) ||
+        overlap(grad_table, bytes, ids, count * id_bytes))
+        return fail(ZERO_EINVAL, "grad_table overlaps an input");
+    const zk::EmbedGradPlan p = zk::plan_embed_grad(count, rows, width);
+    if ((rc = check_workspace(workspace, workspace_bytes, p.bytes))) return rc;
+    if (overlap(workspace, p.bytes, grad_out, count * width * dtype_size(grad_dtype)) ||
+        overlap(workspace, p.bytes, grad_table, bytes) || overlap(workspace, p.bytes, ids, count * id_bytes))
+        return fail(ZERO_EINVAL, "workspace overlaps another buffer");
+    a.grad_out = grad_out;
+    a.grad_bf16 = grad_dtype == ZERO_BF16;
+    a.ids = ids;
+    a.wide_ids = id_bytes == 8;
+    a.count = count;
+    a.rows = rows;
+    a.width = width;
+    a.scale = (float)scale;
+    a.out = grad_table;
+    a.out_bf16 = table_dtype == ZERO_BF16;
+    a.accumulate = accumulate != 0;
+    a.workspace = static_cast<char *>(workspace);
+    const hipError_t e = zk::launch_embed_grad(a, p, stream);
+    return e == hipSuccess ? ZERO_OK : hip_fail(e, "zero_embed_grad");
+}
+
+int zero_dropout(const void *x, const void *add, void *out, int64_t count, zero_dtype dtype, const zero_drop *drop,
+                 hipStream_t stream) {
+    CaptureScope scope(stream);
+    zk::DropoutArgs a = {};
+    if (!valid_dtype(dtype)) return fail(ZERO_EINVAL, "unknown dtype %d", (int)dtype);
+    if (count < 0) return fail(ZERO_EINVAL, "count must be >= 0 (got %lld)", (long long)count);
+    if (ceil_div(count, 8) > kMaxUnits)
+        return fail(ZERO_EUNSUPPORTED, "%lld elements are more than one call takes", (long long)count);
+    if (!drop) return fail(ZERO_EINVAL, "drop is null");
+    int rc = check_drop(drop, &a.drop);
+    if (rc) return rc;
+    const int64_t es = dtype_size(dtype);
+    if ((rc = check_buffer(x, count, es, "x"))) return rc;
+    if (add && (rc = check_buffer(add, count, es, "add"))) return rc;
+    if ((rc = check_buffer(out, count, es, "out"))) return rc;
+    // in place is element by element, a shifted overlap is not
+    if ((out != x && overlap(out, count * es, x, count * es)) ||
+        (add && out != add && overlap(out, count * es, add, count * es)))
+        return fail(ZERO_EINVAL, "out overlaps an input without being it");
+    a.x = x;
+    a.add = add;
+    a.out = out;
+    a.bf16 = dtype == ZERO_BF16;
+    a.count = count;
+    const hipError_t e = zk::launch_dropout(a, stream);
+    return e == hipSuccess ? ZERO_OK : hip_fail(e, "zero_dropout");
+}
+
+int zero_head_loss_workspace(int64_t count, int64_t vocab, int64_t width, zero_dtype dtype, int32_t grad_hidden,
+                             int32_t grad_table, zero_dtype table_grad_dtype, int64_t piece_rows, int64_t *bytes) {
+    int rc = head_sizes(count, vocab, width, dtype, piece_rows);
+    if (rc) return rc;
+    if (!valid_dtype(table_grad_dtype)) return fail(ZERO_EINVAL, "unknown dtype %d", (int)table_grad_dtype);
+    if (!bytes) return fail(ZERO_EINVAL, "null bytes");
+    zk::HeadArgs a = {};
+    a.table = reinterpret_cast<const void *>(1);      // any alignment
+    a.bf16 = dtype == ZERO_BF16;
+    a.count = count;
+    a.width = width;
+    a.vocab = vocab;
+    a.grad_hidden = grad_hidden ? bytes : nullptr;
+    a.grad_table = grad_table ? bytes : nullptr;
+    a.table_grad_bf16 = table_grad_dtype == ZERO_BF16;
+    *bytes = zk::plan_head(a, piece_rows).bytes;
+    return ZERO_OK;
+}
+
+int zero_head_loss(const void *hidden, const void *table, zero_dtype dtype, const void *targets, int32_t id_bytes,
+                   int64_t count, int64_t vocab, int64_t width, const float *weights, int32_t mean, double grad_scale,
+                   float *loss, float *losses, void *grad_hidden, void *grad_table, zero_dtype table_grad_dtype,
+                   int32_t accumulate, int64_t piece_rows, void *workspace, int64_t workspace_bytes,
+                   hipStream_t stream) {
+    CaptureScope scope(stream);
+    int rc = head_sizes(count, vocab, width, dtype, piece_rows);
+    if (rc) return rc;
+    if (!valid_dtype(table_grad_dtype)) return fail(ZERO_EINVAL, "unknown dtype %d", (int)table_grad_dtype);
+    if (!std::isfinite((float)grad_scale))
+        return fail(ZERO_EINVAL, "grad_scale must be finite in fp32 (got %g)", grad_scale);
+    const int64_t es = dtype_size(dtype), gs = dtype_size(table_grad_dtype);
+    if ((rc = check_ids(targets, id_bytes, count, "targets"))) return rc;
+    if ((rc = check_buffer(hidden, count * width, es, "hidden"))) return rc;
+    if ((rc = check_buffer(table, vocab * width, es, "table"))) return rc;
+    if (weights && (rc = check_buffer(weights, count, 4, "weights"))) return rc;
+    if ((rc = check_buffer(loss, 1, 4, "loss"))) return rc;
+    if (losses && (rc = check_buffer(losses, count, 4, "losses"))) return rc;
+    if (grad_hidden && (rc = check_buffer(grad_hidden, count * width, es, "grad_hidden"))) return rc;
+    if (grad_table && (rc = check_buffer(grad_table, vocab * width, gs, "grad_table"))) return rc;
+    zk::HeadArgs a = {};
+    a.hidden = hidden;
+    a.table = table;
+    a.bf16 = dtype == ZERO_BF16;
+    a.targets = targets;
+    a.wide_ids = id_bytes == 8;
+    a.count = count;
+    a.width = width;
+    a.vocab = vocab;
+    a.weights = weights;
+    a.mean = mean != 0;
+    a.grad_scale = (float)grad_scale;
+    a.loss = loss;
+    a.losses = losses;
+    a.grad_hidden = grad_hidden;
+    a.grad_table = grad_table;
+    a.table_grad_bf16 = table_grad_dtype == ZERO_BF16;
+    a.accumulate = accumulate != 0;
+    a.workspace = static_cast<char *>(workspace);
+    const zk::HeadPlan p = zk::plan_head(a, piece_rows);
+    if ((rc = check_workspace(workspace, workspace_bytes, p.bytes))) return rc;
+    // every output and the workspace apart from everything else
+    const struct {
+        const void *p;
+        int64_t bytes;
+        bool written;
+    } all[] = {{loss, 4, true},
+               {losses, 4 * count, true},
+               {grad_hidden, count * width * es, true},
+               {grad_table, vocab * width * gs, true},
+               {workspace, p.bytes, true},
+               {hidden, count * width * es, false},
+               {table, vocab * width * es, false},
+               {targets, count * id_bytes, false},
+               {weights, 4 * count, false}};
+    for (const auto &x : all)
+        for (const auto &y : all)
+            if (&x != &y && x.written && overlap(x.p, x.bytes, y.p, y.bytes))
+                return fail(ZERO_EINVAL, "an output or the workspace overlaps another buffer");
+    const hipError_t e = zk::launch_head(a, p, stream);
+    return e == hipSuccess ? ZERO_OK : hip_fail(e, "zero_head_loss");
+}
+
+}  // extern "C"

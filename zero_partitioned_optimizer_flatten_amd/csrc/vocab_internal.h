@@ -1,0 +1,143 @@
+// Internal interface between the host API of the vocabulary operators
+// (vocab_api.hip) and their gfx950 kernels (vocab_kernels.hip,
+// head_kernels.hip). Callers use include/zero.h.
+#pragma once
+
+#include "zero_internal.h"
+
+namespace zk {
+
+// Host checks that zero_api.hip implements (they set the thread's last error).
+int fail(int code, const char *fmt, ...);
+int hip_fail(hipError_t e, const char *what);
+int check_range(const void *p, int64_t nbytes, const char *what);
+// Skips check_range while `stream` is captured, for the scope's life.
+class CaptureScope {
+  public:
+    explicit CaptureScope(hipStream_t stream);
+    ~CaptureScope();
+    CaptureScope(const CaptureScope &) = delete;
+    CaptureScope &operator=(const CaptureScope &) = delete;
+    bool capturing() const;
+
+  private:
+    bool prev_;
+};
+
+// Dropout: an element is kept where its 16 random bits are >= limit, and then
+// multiplied by scale. limit == 0 means none.
+struct Drop {
+    uint32_t key0, key1;
+    uint32_t limit;               // 0..65536
+    float scale;
+    uint64_t offset;
+    const uint64_t *counter;      // device, added to offset; or null
+};
+
+struct EmbedArgs {
+    const void *ids, *pos_ids;    // pos_ids null: no position table
+    bool wide_ids;                // 64-bit ids
+    int64_t count, rows, pos_rows, width;
+    const void *table, *pos_table;
+    bool table_bf16, out_bf16;
+    float scale;
+    Drop drop;
+    void *out;
+};
+hipError_t launch_embed(const EmbedArgs &a, hipStream_t stream);
+
+// One sorted token: its id, its row of grad_out, and the run of equal ids it
+// is in, as [begin, end) of the sorted list.
+struct SortedToken {
+    int32_t id, row, begin, end;
+};
+// Ids are spread over the sorting workgroups by their remainder, at most
+// kSortIds to each.
+constexpr int kSortIds = 512;
+constexpr int kSortWaves = 16;
+struct EmbedGradPlan {
+    int sort_groups_log2;         // workgroups of the sort
+    int ids_per_group;
+    int span;                     // sorted tokens one wave adds up
+    int64_t spans;
+    int64_t sorted_off, count_off, partial_off, bytes;   // workspace layout
+};
+// Columns of one wave in the sums.
+constexpr int kSpanCols = 512;
+EmbedGradPlan plan_embed_grad(int64_t count, int64_t rows, int64_t width);
+struct EmbedGradArgs {
+    const void *grad_out;
+    bool grad_bf16;
+    const void *ids;
+    bool wide_ids;
+    int64_t count, rows, width;
+    float scale;
+    Drop drop;
+    void *out;
+    bool out_bf16, accumulate;
+    char *workspace;
+};
+hipError_t launch_embed_grad(const EmbedGradArgs &a, const EmbedGradPlan &p, hipStream_t stream);
+
+struct DropoutArgs {
+    const void *x, *add;          // add null: none
+    void *out;
+    bool bf16;
+    int64_t count;
+    Drop drop;
+};
+hipError_t launch_dropout(const DropoutArgs &a, hipStream_t stream);
+
+// ---- softmax cross entropy against a table (head_kernels.hip)
+// What the call finds out first: how many rows take part, their weights' sum
+// and the largest, and what both gradients are multiplied by.
+struct HeadSums {
+    double weight;
+    int64_t rows;
+    float most;                   // largest |weight|
+    float scale;                  // grad_scale * most (/ the weights' sum)
+};
+// Of each row that takes part, in the order of the piece.
+struct HeadRow {
+    float top;                    // largest z * log2(e)
+    float inv;                    // share / sum of exponentials
+    float share;                  // weight / most
+    float target;                 // z_y * log2(e)
+};
+// Tiles of the products: rows of P and of Q, waves, rows of P to a wave.
+struct TileShape {
+    int p, q, waves, sub;
+};
+constexpr TileShape kTiles[] = {{256, 256, 8, 128}, {128, 128, 4, 64}, {128, 32, 4, 32}};
+
+struct HeadPlan {
+    int64_t piece, pieces;        // rows of hidden in a piece
+    int64_t width_p, vocab_p, piece_p;   // extents padded for the products' long axes
+    bool pack_table;              // table copied to aligned, padded rows
+    int tile_logits, tile_hidden, tile_table;   // shapes of the three products' tiles
+    int sub;                      // vocabulary entries that share a statistic
+    int64_t subtiles;             // statistics of a row
+    int splits;                   // of the vocabulary axis in grad_hidden's product
+    // workspace offsets in bytes; -1: not there
+    int64_t sum_off, map_off, loss_off, row_off, stat_off, hidden_off, hidden_t_off, table_off,
+        table_t_off, e_off, e_t_off, gw_off, split_off, bytes;
+};
+struct HeadArgs {
+    const void *hidden, *table;
+    bool bf16;
+    const void *targets;
+    bool wide_ids;
+    int64_t count, width, vocab;
+    const float *weights;
+    bool mean;
+    float grad_scale;
+    float *loss, *losses;
+    void *grad_hidden, *grad_table;
+    bool table_grad_bf16, accumulate;
+    char *workspace;
+};
+// rows: the most rows of hidden in one piece (0: by the memory of a piece).
+HeadPlan plan_head(const HeadArgs &a, int64_t rows);
+hipError_t launch_head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream);
+
+}  // namespace zk

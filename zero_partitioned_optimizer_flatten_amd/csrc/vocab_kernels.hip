@@ -1,0 +1,494 @@
+// Embedding lookup, its gradient by sorted tokens, and dropout, for gfx950.
+//
+// Arithmetic is binary32; every output is rounded once (nearest, ties to
+// even). No floating-point atomics: the same call gives the same bits.
+#include "vocab_internal.h"
+
+namespace zk {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kVec = 8;           // elements of one vector, one Philox block
+
+// ------------------------------------------------------------ elements
+
+__device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
+
+__device__ __forceinline__ uint16_t narrow(float f) {
+    const uint32_t u = __float_as_uint(f);
+    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
+    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+}
+
+// Eight elements at any alignment of their type; `left` of them exist.
+template <bool BF16>
+__device__ __forceinline__ void load8(const void *base, int64_t at, int64_t left, float *v) {
+    if (BF16) {
+        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+        if (left >= kVec) {
+            uint16_t h[kVec];
+            __builtin_memcpy(h, p, sizeof h);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[k] = widen(h[k]);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[k] = k < left ? widen(p[k]) : 0.0f;
+        }
+    } else {
+        const float *p = static_cast<const float *>(base) + at;
+        if (left >= kVec) {
+            __builtin_memcpy(v, p, kVec * sizeof(float));
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[k] = k < left ? p[k] : 0.0f;
+        }
+    }
+}
+
+template <bool BF16>
+__device__ __forceinline__ void store8(void *base, int64_t at, int64_t left, const float *v) {
+    if (BF16) {
+        uint16_t *p = static_cast<uint16_t *>(base) + at;
+        uint16_t h[kVec];
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) h[k] = narrow(v[k]);
+        if (left >= kVec) {
+            __builtin_memcpy(p, h, sizeof h);
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                if (k < left) p[k] = h[k];
+        }
+    } else {
+        float *p = static_cast<float *>(base) + at;
+        if (left >= kVec) {
+            __builtin_memcpy(p, v, kVec * sizeof(float));
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; ++k)
+                if (k < left) p[k] = v[k];
+        }
+    }
+}
+
+// ------------------------------------------------------------- dropout
+// Philox4x32-10 (Salmon, Moraes, Dror and Shaw, "Parallel random numbers: as
+// easy as 1, 2, 3", 2011): 128 bits for each counter (block, offset), used as
+// eight 16-bit numbers. With 16 bits an element instead of 32 the ten rounds'
+// 20 wide products, which issue at a quarter of the rate, serve twice as many
+// elements; p is then a multiple of 2^-16, and the scale is the inverse of the
+// share that this p keeps, so the expectation stays exact.
+
+struct Bits8 {
+    uint32_t w[4];                // element k: the k-th 16 bits
+};
+
+__device__ __forceinline__ Bits8 philox(uint64_t block, uint64_t offset, uint32_t k0, uint32_t k1) {
+    uint32_t c0 = (uint32_t)block, c1 = (uint32_t)(block >> 32);
+    uint32_t c2 = (uint32_t)offset, c3 = (uint32_t)(offset >> 32);
+#pragma unroll
+    for (int r = 0; r < 10; ++r) {
+        const uint64_t a = (uint64_t)0xD2511F53u * c0, b = (uint64_t)0xCD9E8D57u * c2;
+        c0 = (uint32_t)(b >> 32) ^ c1 ^ k0;
+        c1 = (uint32_t)b;
+        c2 = (uint32_t)(a >> 32) ^ c3 ^ k1;
+        c3 = (uint32_t)a;
+        k0 += 0x9E3779B9u;
+        k1 += 0xBB67AE85u;
+    }
+    return {{c0, c1, c2, c3}};
+}
+
+__device__ __forceinline__ uint64_t drop_offset(const Drop &d) {
+    return d.offset + (d.limit && d.counter ? *d.counter : 0);
+}
+
+// v[k] = keep(first + k) ? v[k] * scale : 0 for eight elements from any place.
+// A dropped element is a selected zero, so NaN and infinity there vanish.
+template <bool ALIGNED>
+__device__ __forceinline__ void drop8(const Drop &d, uint64_t offset, uint64_t first, float *v) {
+    const Bits8 x = philox(first / kVec, offset, d.key0, d.key1);
+    if (ALIGNED || first % kVec == 0) {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            const uint32_t u = (x.w[k / 2] >> (16 * (k % 2))) & 0xFFFFu;
+            v[k] = u >= d.limit ? v[k] * d.scale : 0.0f;
+        }
+    } else {
+        const Bits8 y = philox(first / kVec + 1, offset, d.key0, d.key1);
+        const int s = (int)(first % kVec);
+        uint32_t keep = 0;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) {
+            keep |= (uint32_t)(((x.w[k / 2] >> (16 * (k % 2))) & 0xFFFFu) >= d.limit) << k;
+            keep |= (uint32_t)(((y.w[k / 2] >> (16 * (k % 2))) & 0xFFFFu) >= d.limit) << (k + kVec);
+        }
+        keep >>= s;
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) v[k] = (keep >> k) & 1u ? v[k] * d.scale : 0.0f;
+    }
+}
+
+template <bool BF16, bool ADD>
+__global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutArgs a) {
+    const int64_t block = (int64_t)blockIdx.x * kThreads + threadIdx.x;
+    const int64_t at = block * kVec, left = a.count - at;
+    if (left <= 0) return;
+    const uint64_t offset = drop_offset(a.drop);
+    float v[kVec];
+    load8<BF16>(a.x, at, left, v);
+    drop8<true>(a.drop, offset, (uint64_t)at, v);
+    if (ADD) {
+        float r[kVec];
+        load8<BF16>(a.add, at, left, r);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) v[k] += r[k];
+    }
+    store8<BF16>(a.out, at, left, v);
+}
+
+// -------------------------------------------------------------- lookup
+
+__device__ __forceinline__ int64_t load_id(const void *ids, bool wide, int64_t i) {
+    return wide ? static_cast<const int64_t *>(ids)[i] : (int64_t) static_cast<const int32_t *>(ids)[i];
+}
+
+// A vector of eight columns of one output row to a thread.
+template <bool TBF, bool OBF, bool POS, bool DROP, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a, uint32_t per_row) {
+    const uint32_t unit = blockIdx.x * kThreads + threadIdx.x;   // a dispatch has fewer than 2^32
+    const int64_t row = unit / per_row;
+    if (row >= a.count) return;
+    const int64_t col = (int64_t)(unit % per_row) * kVec, left = a.width - col;
+    const uint64_t offset = DROP ? drop_offset(a.drop) : 0;
+    const int64_t id = load_id(a.ids, a.wide_ids, row);
+    float v[kVec];
+    if ((uint64_t)id < (uint64_t)a.rows) {
+        load8<TBF>(a.table, id * a.width + col, left, v);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) v[k] *= a.scale;
+    } else {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) v[k] = 0.0f;
+    }
+    if (POS) {
+        const int64_t pos = load_id(a.pos_ids, a.wide_ids, row);
+        if ((uint64_t)pos < (uint64_t)a.pos_rows) {
+            float r[kVec];
+            load8<TBF>(a.pos_table, pos * a.width + col, left, r);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) v[k] += r[k];
+        }
+    }
+    if (DROP) drop8<ALIGNED>(a.drop, offset, (uint64_t)(row * a.width + col), v);
+    store8<OBF>(a.out, row * a.width + col, left, v);
+}
+
+// ------------------------------------------- gradient: tokens, sorted
+// The tokens are grouped by id in one launch with no traffic between its
+// workgroups. Workgroup g owns the ids that are g modulo the workgroup count
+// (a power of two; neighbouring ids, which frequencies go by, end up in
+// different ones) and reads every token: it counts its own ids, and how many
+// tokens belong to the workgroups before it, which is where its share of the
+// sorted list begins. A second reading places its tokens, each wave its own
+// stretch of the batch in order, so equal ids keep the order they came in and
+// their sum is always added up the same way. When the gradient is written and
+// not added to, the rows of ids that no token names are set to zero here.
+
+__device__ __forceinline__ void zero_row(char *p, int64_t bytes, int lane) {
+    // 2-byte elements up to a 16-byte line, whole vectors, the rest
+    int64_t head = (16 - ((uintptr_t)p & 15)) & 15;
+    if (head > bytes) head = bytes;
+    for (int64_t k = 2 * lane; k < head; k += 128) *reinterpret_cast<uint16_t *>(p + k) = 0;
+    const int64_t vecs = (bytes - head) / 16;
+    const uint4 z = {0, 0, 0, 0};
+    for (int64_t k = lane; k < vecs; k += 64) *reinterpret_cast<uint4 *>(p + head + 16 * k) = z;
+    for (int64_t k = head + 16 * vecs + 2 * lane; k < bytes; k += 128)
+        *reinterpret_cast<uint16_t *>(p + k) = 0;
+}
+
+__global__ void __launch_bounds__(64 * kSortWaves)
+sort_kernel(EmbedGradArgs a, int log2_groups, int per_group, SortedToken *sorted, int32_t *total) {
+    extern __shared__ int32_t counts[];            // [kSortWaves][per_group], then places
+    __shared__ int32_t before[kSortWaves], sums[kSortWaves];
+    int32_t *begin = counts + kSortWaves * per_group, *end = begin + per_group;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const uint32_t group = blockIdx.x, mask = (1u << log2_groups) - 1;
+    for (int k = threadIdx.x; k < kSortWaves * per_group; k += 64 * kSortWaves) counts[k] = 0;
+    __syncthreads();
+    const int64_t stretch = (a.count + 64 * kSortWaves - 1) / (64 * kSortWaves) * 64;
+    const int64_t first = stretch * wave;
+    const int64_t last = first + stretch < a.count ? first + stretch : a.count;
+    int32_t *mine = counts + wave * per_group;
+    int32_t lower = 0, all = 0;
+    for (int64_t i = first + lane; i < last; i += 64) {
+        const int64_t id = load_id(a.ids, a.wide_ids, i);
+        if ((uint64_t)id < (uint64_t)a.rows) {
+            const uint32_t g = (uint32_t)id & mask;
+            lower += g < group;
+            ++all;
+            if (g == group) atomicAdd(&mine[(uint32_t)id >> log2_groups], 1);
+        }
+    }
+    for (int s = 32; s; s /= 2) {
+        lower += __shfl_xor(lower, s);
+        all += __shfl_xor(all, s);
+    }
+    if (lane == 0) before[wave] = lower, sums[wave] = all;
+    __syncthreads();
+    int32_t base = 0;
+    all = 0;
+    for (int w = 0; w < kSortWaves; ++w) {
+        base += before[w];
+        all += sums[w];
+    }
+    if (group == 0 && threadIdx.x == 0) *total = all;
+    __syncthreads();
+    // one id to a thread (per_group <= kSortIds): an exclusive sum over the ids
+    int32_t own = 0;
+    if ((int)threadIdx.x < per_group)
+        for (int w = 0; w < kSortWaves; ++w) own += counts[w * per_group + threadIdx.x];
+    int32_t upto = own;
+    for (int s = 1; s < 64; s *= 2) {
+        const int32_t x = __shfl_up(upto, s);
+        if (lane >= s) upto += x;
+    }
+    if (lane == 63) sums[wave] = upto;
+    __syncthreads();
+    for (int w = 0; w < wave; ++w) base += sums[w];
+    if ((int)threadIdx.x < per_group) {
+        int32_t at = base + upto - own;
+        begin[threadIdx.x] = at;
+        end[threadIdx.x] = at + own;
+        for (int w = 0; w < kSortWaves; ++w) {
+            const int32_t c = counts[w * per_group + threadIdx.x];
+            counts[w * per_group + threadIdx.x] = at;
+            at += c;
+        }
+    }
+    __syncthreads();
+    for (int64_t i0 = first; i0 < last; i0 += 64) {
+        const int64_t i = i0 + lane;
+        const int64_t id = i < last ? load_id(a.ids, a.wide_ids, i) : -1;
+        const bool here = (uint64_t)id < (uint64_t)a.rows && ((uint32_t)id & mask) == group;
+        const int32_t k = here ? (int32_t)((uint32_t)id >> log2_groups) : -1;
+        uint64_t todo = __ballot(here);
+        while (todo) {                             // the ids among these 64, one by one
+            const int leader = __builtin_ctzll(todo);
+            const uint64_t same = __ballot(k == __shfl(k, leader));
+            int32_t at = 0;
+            if (lane == leader) at = atomicAdd(&mine[k], (int32_t)__popcll(same));
+            at = __shfl(at, leader) + __popcll(same & ((1ull << lane) - 1));
+            if ((same >> lane) & 1) sorted[at] = {(int32_t)id, (int32_t)i, begin[k], end[k]};
+            todo &= ~same;
+        }
+    }
+    if (a.accumulate) return;
+    const int64_t row_bytes = a.width * (a.out_bf16 ? 2 : 4);
+    for (int k = wave; k < per_group; k += kSortWaves) {
+        const int64_t id = ((int64_t)k << log2_groups) + group;
+        if (id < a.rows && begin[k] == end[k])
+            zero_row(static_cast<char *>(a.out) + id * row_bytes, row_bytes, lane);
+    }
+}
+
+// ------------------------------------------- gradient: runs added up
+// A wave adds up `span` sorted tokens, 512 columns of them, in order. A run of
+// equal ids inside the span is one row of the gradient and written at once. Of
+// a run that goes over the span's end or came in over its start the wave
+// leaves a partial row: slot 2s where it came in, else slot 2s + 1. The joining
+// kernel adds a run's partial rows in the order of the spans. So the work is
+// even whatever the tokens are, one padding token a million times included.
+
+template <bool OBF>
+__device__ __forceinline__ void write_row(const EmbedGradArgs &a, int32_t id, int64_t col,
+                                          const float *sum) {
+    const int64_t left = a.width - col, at = (int64_t)id * a.width + col;
+    if (left <= 0) return;
+    float v[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) v[k] = sum[k] * a.scale;
+    if (a.accumulate) {
+        float old[kVec];
+        load8<OBF>(a.out, at, left, old);
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) v[k] += old[k];
+    }
+    store8<OBF>(a.out, at, left, v);
+}
+
+template <bool GBF, bool OBF, bool DROP, bool ALIGNED>
+__global__ void __launch_bounds__(kThreads)
+span_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, int span,
+            int64_t spans, int col_chunks, float *partial, int64_t pitch) {
+    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+    const int lane = threadIdx.x % 64;
+    const int64_t s = unit / col_chunks;
+    const int64_t col = (unit - s * col_chunks) * kSpanCols + lane * kVec;
+    const int32_t n = *total;
+    const int64_t lo = s * span, hi = lo + span < n ? lo + span : n;
+    if (s >= spans || lo >= n) return;
+    const int64_t left = a.width - col;
+    const uint64_t offset = DROP ? drop_offset(a.drop) : 0;
+    float sum[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) sum[k] = 0.0f;
+    for (int64_t i = lo; i < hi; ++i) {
+        const SortedToken t = sorted[i];
+        if (left > 0) {
+            float v[kVec];
+            load8<GBF>(a.grad_out, (int64_t)t.row * a.width + col, left, v);
+            if (DROP) drop8<ALIGNED>(a.drop, offset, (uint64_t)t.row * a.width + col, v);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) sum[k] += v[k];
+        }
+        if (i + 1 == t.end || i + 1 == hi) {
+            if (t.begin >= lo && t.end <= hi) {
+                write_row<OBF>(a, t.id, col, sum);
+            } else if (left > 0) {
+                float *p = partial + (2 * s + (t.begin >= lo)) * pitch + col;
+                __builtin_memcpy(__builtin_assume_aligned(p, 16), sum, sizeof sum);
+            }
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) sum[k] = 0.0f;
+        }
+    }
+}
+
+// Workgroup (span, columns): the run that begins in the span and goes over its
+// end. Its spans are dealt to the workgroup's waves in stretches, joined in order.
+constexpr int kJoinWaves = 4;
+
+template <bool OBF>
+__global__ void __launch_bounds__(64 * kJoinWaves)
+join_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, int span,
+            int col_chunks, const float *partial, int64_t pitch) {
+    __shared__ __align__(16) float sums[kJoinWaves][kSpanCols];
+    const int64_t s = blockIdx.x / col_chunks;
+    const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+    const int64_t col = (int64_t)(blockIdx.x % col_chunks) * kSpanCols + lane * kVec;
+    const int32_t n = *total;
+    const int64_t hi = (s + 1) * span;
+    if (hi >= n) return;                           // the whole workgroup
+    const SortedToken t = sorted[hi - 1];
+    if (t.end <= hi || t.begin < hi - span) return;
+    const int64_t last = (t.end - 1) / span;       // the run's last span
+    const int64_t more = last - s;                 // slots 2(s+1), 2(s+2), ...
+    const int64_t each = (more + kJoinWaves - 1) / kJoinWaves;
+    const int64_t b = s + 1 + each * wave, e = b + each < last + 1 ? b + each : last + 1;
+    float sum[kVec], v[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) sum[k] = 0.0f;
+    if (col < a.width) {
+        if (wave == 0) __builtin_memcpy(sum, partial + (2 * s + 1) * pitch + col, sizeof sum);
+#pragma unroll 4
+        for (int64_t q = b; q < e; ++q) {
+            __builtin_memcpy(v, partial + 2 * q * pitch + col, sizeof v);
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) sum[k] += v[k];
+        }
+    }
+    __builtin_memcpy(&sums[wave][lane * kVec], sum, sizeof sum);
+    __syncthreads();
+    if (wave != 0) return;
+    for (int w = 1; w < kJoinWaves; ++w)
+#pragma unroll
+        for (int k = 0; k < kVec; ++k) sum[k] += sums[w][lane * kVec + k];
+    write_row<OBF>(a, t.id, col, sum);
+}
+
+static_assert(kSpanCols == 64 * kVec, "a vector to a lane");
+
+int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+template <bool TBF, bool OBF, bool POS>
+void start_embed(const EmbedArgs &a, hipStream_t stream) {
+    const uint32_t per_row = (uint32_t)ceil_div(a.width, kVec);
+    const dim3 grid((unsigned)ceil_div(a.count * per_row, kThreads));
+    const bool aligned = a.width % kVec == 0;
+    if (a.drop.limit == 0)
+        embed_kernel<TBF, OBF, POS, false, true><<<grid, kThreads, 0, stream>>>(a, per_row);
+    else if (aligned)
+        embed_kernel<TBF, OBF, POS, true, true><<<grid, kThreads, 0, stream>>>(a, per_row);
+    else
+        embed_kernel<TBF, OBF, POS, true, false><<<grid, kThreads, 0, stream>>>(a, per_row);
+}
+
+template <bool GBF, bool OBF>
+void start_spans(const EmbedGradArgs &a, const EmbedGradPlan &p, const SortedToken *sorted,
+                 const int32_t *total, float *partial, hipStream_t stream) {
+    const int chunks = (int)ceil_div(a.width, kSpanCols);
+    const int64_t pitch = (int64_t)chunks * kSpanCols;
+    const dim3 grid((unsigned)ceil_div(p.spans * chunks, kThreads / 64));
+    if (a.drop.limit == 0)
+        span_kernel<GBF, OBF, false, true><<<grid, kThreads, 0, stream>>>(
+            a, sorted, total, p.span, p.spans, chunks, partial, pitch);
+    else if (a.width % kVec == 0)
+        span_kernel<GBF, OBF, true, true><<<grid, kThreads, 0, stream>>>(
+            a, sorted, total, p.span, p.spans, chunks, partial, pitch);
+    else
+        span_kernel<GBF, OBF, true, false><<<grid, kThreads, 0, stream>>>(
+            a, sorted, total, p.span, p.spans, chunks, partial, pitch);
+    if (p.spans > 1)
+        join_kernel<OBF><<<dim3((unsigned)((p.spans - 1) * chunks)), 64 * kJoinWaves, 0, stream>>>(
+            a, sorted, total, p.span, chunks, partial, pitch);
+}
+
+}  // namespace
+
+hipError_t launch_dropout(const DropoutArgs &a, hipStream_t stream) {
+    if (a.count == 0) return hipSuccess;
+    const dim3 grid((unsigned)ceil_div(a.count, (int64_t)kThreads * kVec));
+    if (a.bf16) {
+        if (a.add) dropout_kernel<true, true><<<grid, kThreads, 0, stream>>>(a);
+        else dropout_kernel<true, false><<<grid, kThreads, 0, stream>>>(a);
+    } else {
+        if (a.add) dropout_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
+        else dropout_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_embed(const EmbedArgs &a, hipStream_t stream) {
+    if (a.count == 0) return hipSuccess;
+    if (a.table_bf16) {
+        if (a.out_bf16) {
+            if (a.pos_ids) start_embed<true, true, true>(a, stream);
+            else start_embed<true, true, false>(a, stream);
+        } else {
+            if (a.pos_ids) start_embed<true, false, true>(a, stream);
+            else start_embed<true, false, false>(a, stream);
+        }
+    } else {
+        if (a.out_bf16) {
+            if (a.pos_ids) start_embed<false, true, true>(a, stream);
+            else start_embed<false, true, false>(a, stream);
+        } else {
+            if (a.pos_ids) start_embed<false, false, true>(a, stream);
+            else start_embed<false, false, false>(a, stream);
+        }
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_embed_grad(const EmbedGradArgs &a, const EmbedGradPlan &p, hipStream_t stream) {
+    if (a.count == 0 && a.accumulate) return hipSuccess;
+    auto *sorted = reinterpret_cast<SortedToken *>(a.workspace + p.sorted_off);
+    auto *total = reinterpret_cast<int32_t *>(a.workspace + p.count_off);
+    auto *partial = reinterpret_cast<float *>(a.workspace + p.partial_off);
+    const size_t lds = (size_t)(kSortWaves + 2) * p.ids_per_group * sizeof(int32_t);
+    sort_kernel<<<dim3(1u << p.sort_groups_log2), 64 * kSortWaves, lds, stream>>>(
+        a, p.sort_groups_log2, p.ids_per_group, sorted, total);
+    if (a.count > 0) {
+        if (a.grad_bf16) {
+            if (a.out_bf16) start_spans<true, true>(a, p, sorted, total, partial, stream);
+            else start_spans<true, false>(a, p, sorted, total, partial, stream);
+        } else {
+            if (a.out_bf16) start_spans<false, true>(a, p, sorted, total, partial, stream);
+            else start_spans<false, false>(a, p, sorted, total, partial, stream);
+        }
+    }
+    return hipGetLastError();
+}
+
+}  // namespace zk

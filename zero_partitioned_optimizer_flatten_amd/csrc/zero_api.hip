@@ -13,7 +13,7 @@
 #include <vector>
 
 #include "../../include/zero.h"
-#include "zero_internal.h"
+#include "vocab_internal.h"
 
 // One parameter of a per-parameter (dim-0) layout context.
 struct zero_fsdp_tensor {
@@ -83,6 +83,16 @@ namespace {
 
 thread_local std::string g_last_error;
 
+// Range checks query the runtime's allocation table, which a stream
+// capture in global mode may not allow. While the caller's stream is being
+// captured they are skipped (every other argument check still runs); the
+// buffers of a captured call are normally those of an earlier eager call.
+thread_local bool g_skip_range = false;
+
+}  // namespace
+
+namespace zk {
+
 int fail(int code, const char *fmt, ...) {
     char buf[512];
     va_list ap;
@@ -100,6 +110,45 @@ int fail(int code, const char *fmt, ...) {
 int hip_fail(hipError_t e, const char *what) {
     return fail(ZERO_EHIP, "%s: %s (%d)", what, hipGetErrorString(e), (int)e);
 }
+
+CaptureScope::CaptureScope(hipStream_t s) : prev_(g_skip_range) {
+    hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
+    if (hipStreamIsCapturing(s, &st) != hipSuccess) {
+        (void)hipGetLastError();
+        st = hipStreamCaptureStatusNone;
+    }
+    g_skip_range = st == hipStreamCaptureStatusActive;
+}
+CaptureScope::~CaptureScope() { g_skip_range = prev_; }
+bool CaptureScope::capturing() const { return g_skip_range; }
+
+// Reject a device range that runs past the allocation holding its first
+// byte (an undersized buffer would otherwise fault on the GPU). Memory the
+// runtime cannot describe (e.g. imported or virtually mapped) is accepted.
+int check_range(const void *p, int64_t nbytes, const char *what) {
+    if (nbytes <= 0 || g_skip_range) return ZERO_OK;
+    hipDeviceptr_t base = nullptr;
+    size_t size = 0;
+    hipError_t e = hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)p);
+    if (e != hipSuccess) {
+        (void)hipGetLastError();
+        return ZERO_OK;
+    }
+    const uintptr_t b = (uintptr_t)base, q = (uintptr_t)p;
+    if (q < b || q - b + (uint64_t)nbytes > (uint64_t)size)
+        return fail(ZERO_EINVAL, "%s: %lld bytes at %p run past the end of its allocation "
+                    "(%zu bytes at %p)", what, (long long)nbytes, p, size, (void *)base);
+    return ZERO_OK;
+}
+
+}  // namespace zk
+
+namespace {
+
+using zk::CaptureScope;
+using zk::check_range;
+using zk::fail;
+using zk::hip_fail;
 
 bool valid_dtype(zero_dtype d) { return d == ZERO_F32 || d == ZERO_BF16; }
 size_t dtype_size(zero_dtype d) { return d == ZERO_BF16 ? 2 : 4; }
@@ -160,48 +209,6 @@ class DeviceGuard {
     int prev_ = -1;
     hipError_t err_ = hipSuccess;
 };
-
-// Range checks query the runtime's allocation table, which a stream
-// capture in global mode may not allow. While the caller's stream is being
-// captured they are skipped (every other argument check still runs); the
-// buffers of a captured call are normally those of an earlier eager call.
-thread_local bool g_skip_range = false;
-
-class CaptureScope {
-  public:
-    explicit CaptureScope(hipStream_t s) : prev_(g_skip_range) {
-        hipStreamCaptureStatus st = hipStreamCaptureStatusNone;
-        if (hipStreamIsCapturing(s, &st) != hipSuccess) {
-            (void)hipGetLastError();
-            st = hipStreamCaptureStatusNone;
-        }
-        g_skip_range = st == hipStreamCaptureStatusActive;
-    }
-    ~CaptureScope() { g_skip_range = prev_; }
-    bool capturing() const { return g_skip_range; }
-
-  private:
-    bool prev_;
-};
-
-// Reject a device range that runs past the allocation holding its first
-// byte (an undersized buffer would otherwise fault on the GPU). Memory the
-// runtime cannot describe (e.g. imported or virtually mapped) is accepted.
-int check_range(const void *p, int64_t nbytes, const char *what) {
-    if (nbytes <= 0 || g_skip_range) return ZERO_OK;
-    hipDeviceptr_t base = nullptr;
-    size_t size = 0;
-    hipError_t e = hipMemGetAddressRange(&base, &size, (hipDeviceptr_t)p);
-    if (e != hipSuccess) {
-        (void)hipGetLastError();
-        return ZERO_OK;
-    }
-    const uintptr_t b = (uintptr_t)base, q = (uintptr_t)p;
-    if (q < b || q - b + (uint64_t)nbytes > (uint64_t)size)
-        return fail(ZERO_EINVAL, "%s: %lld bytes at %p run past the end of its allocation "
-                    "(%zu bytes at %p)", what, (long long)nbytes, p, size, (void *)base);
-    return ZERO_OK;
-}
 
 zk::StepScalars make_scalars(const zero_ctx *c, int64_t t) {
     zk::StepScalars sc;
