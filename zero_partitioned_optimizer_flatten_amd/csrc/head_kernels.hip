@@ -138,29 +138,6 @@ pack_kernel(const void *src, int64_t rows, int64_t cols, const int32_t *map, con
     }
 }
 
-// dst [cols][rows_p] = the transpose of the mapped rows of src [.][cols], zeros
-// behind them. 64 x 64 elements to a workgroup, through LDS.
-template <bool BF16>
-__global__ void __launch_bounds__(256)
-transpose_kernel(const void *src, int64_t rows, int64_t cols, const int32_t *map, const HeadSums *sums,
-                 int64_t first, void *dst, int64_t rows_p) {
-    using T = typename Elem<BF16>::type;
-    __shared__ T tile[64][64 + 4 / sizeof(T)];
-    const int64_t n = map ? piece_rows(sums, first, rows) : rows;
-    const int64_t r0 = (int64_t)blockIdx.x * 64, c0 = (int64_t)blockIdx.y * 64;
-    if (map && r0 >= round_up(n, 64)) return;
-    const int x = threadIdx.x % 64, y = threadIdx.x / 64;
-    for (int k = y; k < 64; k += 4) {
-        const int64_t r = r0 + k, c = c0 + x;
-        T v = 0;
-        if (r < n && c < cols) v = static_cast<const T *>(src)[(map ? map[first + r] : r) * cols + c];
-        tile[k][x] = v;
-    }
-    __syncthreads();
-    for (int k = y; k < 64; k += 4)
-        if (c0 + k < cols && r0 + x < rows_p) static_cast<T *>(dst)[(c0 + k) * rows_p + r0 + x] = tile[x][k];
-}
-
 // ------------------------------------------------------- the product
 // out[q][p] = sum_k P[p][k] Q[q][k]; rows of P and Q are 16-byte aligned and
 // their long axis is a whole number of 128-byte steps. A workgroup makes BP x BQ
@@ -184,7 +161,7 @@ struct Product {
     const HeadSums *sums;
     int64_t first, piece;
     bool piece_is_q, piece_is_k;
-    int esize;
+    int64_t kp;                   // lines of a P across the long axis
     // kLogits
     const void *targets;
     bool wide_ids;
@@ -217,7 +194,95 @@ __device__ __forceinline__ f32x4 mma(f32x4 p, f32x4 q, f32x4 c) {
     return c;
 }
 
-template <bool BF16, int EPI, int BP, int BQ, int WP, int WQ>
+// 16 bytes a lane, from base + from, to LDS at `lds` + 16 * lane. In assembly,
+// since the compiler would otherwise wait for all such loads before it reads LDS
+// across lanes (ds_read_b64_tr_b16); the waits are the loop's own. No register is
+// written.
+__device__ __forceinline__ void load_to_lds(const char *base, int from, uint32_t lds) {
+    typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+    const u32x4 r = {(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32) & 0xFFFFu, 0xFFFFFFFFu, 0x00027000u};
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+                 :
+                 : "s"(lds), "v"(from), "s"(r)
+                 : "memory");
+}
+
+// One operand's tile of a stage: B rows and 128 bytes of the long axis, from
+// rows along it ([row][k], T false) or across it ([k][row], T true).
+template <bool BF16, bool T, int B, int LOADS>
+struct Operand {
+    static constexpr int kEs = BF16 ? 2 : 4, kSteps = 128 / kEs;
+    static constexpr int kLine = T ? B * kEs : 128;           // bytes of a line in LDS
+    int at[LOADS];                                            // what each load's lane reads
+    int64_t step;                                             // bytes from stage to stage
+
+    // Where the 16-byte chunk at place c of line k comes from.
+    static __device__ __forceinline__ int source(int k, int c) {
+        if (!T) return c ^ (k % 8);
+        if (BF16) return c ^ ((((k & 3) | ((k >> 1) & 4)) << 1) & (kLine / 16 - 1));
+        return c ^ (((k >> 2) & 3) << 2 & (kLine / 16 - 1));
+    }
+    // Rows (T: 16-byte columns) behind the operand's last are read as the last:
+    // always memory of the operand.
+    __device__ __forceinline__ void init(int wave, int lane, int64_t first, int64_t n, int64_t ld) {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+            const int byte = (wave * LOADS + j) * 1024 + lane * 16;
+            const int line = byte / kLine, chunk = source(line, byte % kLine / 16);
+            if (T) {
+                int64_t col = first * kEs + chunk * 16;
+                if (col > ld - 16) col = ld - 16;
+                at[j] = (int)(line * ld + (col - first * kEs));
+            } else {
+                int64_t r = line;
+                if (first + r >= n) r = n - 1 - first;
+                at[j] = (int)(r * ld) + chunk * 16;
+            }
+        }
+        step = T ? kSteps * ld : 128;
+    }
+    // lds: the operand's place in the stage. T: of a stage with fewer than
+    // kSteps lines (`left` >= 1) those behind are read as the last.
+    template <bool LAST>
+    __device__ __forceinline__ void load(const char *base, uint32_t lds, int wave, int lane, int left, int ld) const {
+#pragma unroll
+        for (int j = 0; j < LOADS; ++j) {
+            int from = at[j];
+            if (LAST) {
+                const int line = ((wave * LOADS + j) * 1024 + lane * 16) / kLine;
+                if (line >= left) from -= (line - (left - 1)) * ld;
+            }
+            load_to_lds(base, from, lds + (wave * LOADS + j) * 1024);
+        }
+    }
+    // Fragment: 16 rows from row0 (a multiple of 16), half h of the stage.
+    static __device__ __forceinline__ typename Frag<BF16>::type read(const char *lds, int row0, int h, int lane) {
+        const int g = lane / 16, s = lane % 16;
+        if constexpr (!T) {
+            const int r = row0 + s;
+            return *reinterpret_cast<const typename Frag<BF16>::type *>(lds + r * 128 + (((4 * h + g) ^ (lane % 8)) * 16));
+        } else if constexpr (BF16) {
+            // 16 lanes bring 4 lines of 16 numbers and get 4 lines' numbers of one row each
+            typedef __attribute__((ext_vector_type(4))) short s16x4;
+            typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+            const int k = 32 * h + 8 * g + s / 4;
+            const int c = row0 / 8 + s % 4 / 2;                // chunk of the four numbers
+            const char *p = lds + k * kLine + source(k, c) * 16 + (s % 2) * 8;
+            const s16x4 lo = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)p);
+            const s16x4 hi = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4 *)(p + 4 * kLine));
+            return __builtin_bit_cast(bf16x8, __builtin_shufflevector(lo, hi, 0, 1, 2, 3, 4, 5, 6, 7));
+        } else {
+            f32x4 v;
+            const int k = 16 * h + 4 * g;
+            const char *p = lds + k * kLine + source(k, row0 / 4 + s / 4) * 16 + (s % 4) * 4;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = *reinterpret_cast<const float *>(p + e * kLine);
+            return v;
+        }
+    }
+};
+
+template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ>
 __device__ __forceinline__ void product(const Product &g) {
     constexpr int kWaves = WP * WQ;
     constexpr int kI = BP / WP / 16, kJ = BQ / WQ / 16;       // fragments of a wave
@@ -225,6 +290,8 @@ __device__ __forceinline__ void product(const Product &g) {
     static_assert(kLoadsP * 8 * kWaves == BP && kLoadsQ * 8 * kWaves == BQ, "whole loads");
     constexpr int kStage = (BP + BQ) * 128;
     using F = typename Frag<BF16>::type;
+    using OpP = Operand<BF16, TP, BP, kLoadsP>;
+    using OpQ = Operand<BF16, TQ, BQ, kLoadsQ>;
     __shared__ __align__(1024) char lds[2][kStage];
 
     const int lane = threadIdx.x % 64;
@@ -233,7 +300,7 @@ __device__ __forceinline__ void product(const Product &g) {
     if (g.sums) {
         const int n = piece_rows(g.sums, g.first, g.piece);
         if (g.piece_is_q) nq = n;
-        if (g.piece_is_k) steps = ceil_div((int64_t)n * g.esize, 128);
+        if (g.piece_is_k) steps = ceil_div((int64_t)n * OpP::kEs, 128);
     }
 
     // Workgroups go round robin over the 8 XCDs: give each XCD a run of
@@ -253,36 +320,24 @@ __device__ __forceinline__ void product(const Product &g) {
     const int64_t k0 = per_split * split;
     const int ksteps = (int)(k0 >= steps ? 0 : steps - k0 < per_split ? steps - k0 : per_split);
 
-    // Rows behind the last are read as the last: always memory of the operand.
-    int vp[kLoadsP], vq[kLoadsQ];
-    const int chunk = (lane % 8) ^ (lane / 8);
-#pragma unroll
-    for (int j = 0; j < kLoadsP; ++j) {
-        int64_t r = (wave * kLoadsP + j) * 8 + lane / 8;
-        if (p0 + r >= g.np) r = g.np - 1 - p0;
-        vp[j] = (int)(r * g.ldp) + chunk * 16;
-    }
-#pragma unroll
-    for (int j = 0; j < kLoadsQ; ++j) {
-        int64_t r = (wave * kLoadsQ + j) * 8 + lane / 8;
-        if (q0 + r >= nq) r = nq - 1 - q0;
-        vq[j] = (int)(r * g.ldq) + chunk * 16;
-    }
-    const __amdgpu_buffer_rsrc_t rp = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char *>(static_cast<const char *>(g.p) + p0 * g.ldp + k0 * 128), (short)0, 0xFFFFFFFF, 0x00027000);
-    const __amdgpu_buffer_rsrc_t rq = __builtin_amdgcn_make_buffer_rsrc(
-        const_cast<char *>(static_cast<const char *>(g.q) + q0 * g.ldq + k0 * 128), (short)0, 0xFFFFFFFF, 0x00027000);
+    OpP op;
+    OpQ oq;
+    op.init(wave, lane, p0, g.np, g.ldp);
+    oq.init(wave, lane, q0, nq, g.ldq);
+    const char *bp = static_cast<const char *>(g.p) + (TP ? p0 * OpP::kEs : p0 * g.ldp) + k0 * op.step;
+    const char *bq = static_cast<const char *>(g.q) + (TQ ? q0 * OpQ::kEs : q0 * g.ldq) + k0 * oq.step;
+    // lines of P that are left (TP: the table's rows are not padded)
+    int64_t lines = TP ? g.kp - k0 * OpP::kSteps : 0;
+    const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
 
-    auto load = [&](int k, int buf) {
-        char *s = lds[buf];
-#pragma unroll
-        for (int j = 0; j < kLoadsP; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rp, (lds_void *)(s + (wave * kLoadsP + j) * 1024), 16, vp[j],
-                                                     k * 128, 0, 0);
-#pragma unroll
-        for (int j = 0; j < kLoadsQ; ++j)
-            __builtin_amdgcn_raw_ptr_buffer_load_lds(rq, (lds_void *)(s + BP * 128 + (wave * kLoadsQ + j) * 1024), 16,
-                                                     vq[j], k * 128, 0, 0);
+    auto load = [&](int buf) {
+        const uint32_t s = lds0 + buf * kStage;
+        if (TP && lines < OpP::kSteps) op.template load<true>(bp, s, wave, lane, (int)lines, (int)g.ldp);
+        else op.template load<false>(bp, s, wave, lane, 0, 0);
+        oq.template load<false>(bq, s + BP * 128, wave, lane, 0, 0);
+        bp += op.step;
+        bq += oq.step;
+        lines -= OpP::kSteps;
     };
 
     f32x4 acc[kI][kJ];
@@ -291,29 +346,56 @@ __device__ __forceinline__ void product(const Product &g) {
 #pragma unroll
         for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
 
+    // A stage is multiplied in four parts: part c takes half c / 2 of the long axis
+    // and half c % 2 of the wave's rows of P.
     const int wp = wave / WQ, wq = wave % WQ;
-    const int rowp = (wp * (BP / WP) + lane % 16) * 128, rowq = (BP + wq * (BQ / WQ) + lane % 16) * 128;
-    const int off0 = ((lane / 16) ^ (lane % 8)) * 16, off1 = ((4 + lane / 16) ^ (lane % 8)) * 16;
+    F fp[2][kI / 2], fq[2][kJ];
+    auto read = [&](int buf, int c) {
+        const char *s = lds[buf];
+        if (c % 2 == 0)
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) fq[c / 2][j] = OpQ::read(s + BP * 128, wq * (BQ / WQ) + 16 * j, c / 2, lane);
+#pragma unroll
+        for (int i = 0; i < kI / 2; ++i)
+            fp[c % 2][i] = OpP::read(s, wp * (BP / WP) + 16 * (c % 2 * (kI / 2) + i), c / 2, lane);
+    };
+    auto multiply = [&](int c) {
+#pragma unroll
+        for (int i = 0; i < kI / 2; ++i)
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                f32x4 &x = acc[c % 2 * (kI / 2) + i][j];
+                x = mma(fp[c % 2][i], fq[c / 2][j], x);
+            }
+    };
 
-    if (ksteps > 0) load(0, 0);
+    // Each part is read while the one before is multiplied. When the last part of a
+    // stage has been read by all, the loads of the stage after the next go to its
+    // place, so a load has nearly a stage's time to arrive and a wave meets one
+    // barrier a stage, with products still to do.
+    if (ksteps > 0) load(0);
+    if (ksteps > 1) load(1);
+    if (ksteps > 1) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(kLoadsP + kLoadsQ) : "memory");
+    else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+    if (ksteps > 0) read(0, 0);
     for (int k = 0; k < ksteps; ++k) {
-        __builtin_amdgcn_s_waitcnt(0x0F70);                   // vmcnt(0): this wave's loads
-        __syncthreads();                                      // everyone's; and step k - 1 is used up
-        if (k + 1 < ksteps) load(k + 1, (k + 1) & 1);
-        const char *s = lds[k & 1];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            const int off = h ? off1 : off0;
-            F fp[kI], fq[kJ];
-#pragma unroll
-            for (int j = 0; j < kJ; ++j) fq[j] = *reinterpret_cast<const F *>(s + rowq + j * 2048 + off);
-#pragma unroll
-            for (int i = 0; i < kI; ++i) fp[i] = *reinterpret_cast<const F *>(s + rowp + i * 2048 + off);
-#pragma unroll
-            for (int i = 0; i < kI; ++i)
-#pragma unroll
-                for (int j = 0; j < kJ; ++j) acc[i][j] = mma(fp[i], fq[j], acc[i][j]);
-        }
+        const int buf = k & 1;
+        read(buf, 1);
+        __builtin_amdgcn_sched_barrier(0);        // the reads go first, whatever the scheduler thinks
+        multiply(0);
+        __builtin_amdgcn_sched_barrier(0);
+        read(buf, 2);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(1);
+        __builtin_amdgcn_sched_barrier(0);
+        read(buf, 3);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(2);
+        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (k + 2 < ksteps) load(buf);
+        if (k + 1 < ksteps) read(buf ^ 1, 0);
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(3);
     }
 
     // A lane holds outputs p = pw + 16 i + r, r < 4, of q = qw + 16 j.
@@ -410,9 +492,9 @@ __device__ __forceinline__ void product(const Product &g) {
     }
 }
 
-template <bool BF16, int EPI, int BP, int BQ, int WP, int WQ>
+template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ>
 __global__ void __launch_bounds__(64 * WP * WQ, 2) product_kernel(Product g) {
-    product<BF16, EPI, BP, BQ, WP, WQ>(g);
+    product<BF16, EPI, TP, TQ, BP, BQ, WP, WQ>(g);
 }
 
 // ------------------------------------------------------- the softmax
@@ -476,61 +558,47 @@ __global__ void __launch_bounds__(256) idle_rows_kernel(HeadArgs a, float *losse
 }
 
 // ------------------------------------------------------- e to G
-// In place, [rows][vocab_p], and transposed, [vocab][piece_p], zeros behind the
-// rows. 64 rows x 64 entries to a workgroup.
+// In place, [rows][vocab_p]; zeros behind the last row up to a whole stage of the
+// product across the rows, and behind the vocabulary. Eight (four) numbers to a
+// thread, grid (columns, rows).
 template <bool BF16>
 __global__ void __launch_bounds__(256)
 gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t first, int64_t piece,
                 const f32x2 *stat, int64_t subtiles, int sub, const HeadRow *rows, void *e,
-                int64_t vocab_p, void *e_t, int64_t piece_p) {
+                int64_t vocab_p) {
     using T = typename Elem<BF16>::type;
-    constexpr int V = 16 / sizeof(T), kPerRow = 64 / V;
-    __shared__ T tile[64][64 + 4 / sizeof(T)];
+    constexpr int V = 16 / sizeof(T);
     const int n = piece_rows(sums, first, piece);
-    const int64_t v0 = (int64_t)blockIdx.x * 64, q0 = (int64_t)blockIdx.y * 64;
-    if (q0 >= n) return;
-    for (int k = threadIdx.x; k < 64 * kPerRow; k += 256) {
-        const int r = k / kPerRow, c = k % kPerRow * V;
-        const int64_t q = q0 + r, v = v0 + c;
-        T out[V];
-        if (q < n) {
-            const HeadRow s = rows[q];
-            const int64_t y = load_id(a.targets, a.wide_ids, map[first + q]);
-            const float share = __builtin_amdgcn_exp2f(stat[q * subtiles + v / sub].x - s.top) * s.inv
-                                * (BF16 ? 0x1p-15f : 1.0f);
-            T *at = static_cast<T *>(e) + q * vocab_p + v;
-            if (BF16) {
-                _Float16 h[V];
-                __builtin_memcpy(h, __builtin_assume_aligned(at, 16), sizeof h);
+    const int64_t q = blockIdx.y, v = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
+    if (q >= round_up(n, 64) || v >= vocab_p) return;
+    T *at = static_cast<T *>(e) + q * vocab_p + v, out[V];
+    if (q < n) {
+        const HeadRow s = rows[q];
+        const int64_t y = load_id(a.targets, a.wide_ids, map[first + q]);
+        const float share = __builtin_amdgcn_exp2f(stat[q * subtiles + v / sub].x - s.top) * s.inv
+                            * (BF16 ? 0x1p-15f : 1.0f);
+        float x[V];
+        if (BF16) {
+            _Float16 h[V];
+            __builtin_memcpy(h, __builtin_assume_aligned(at, 16), sizeof h);
 #pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float x = (float)h[j] * share;
-                    if (v + j == y) x -= s.share;
-                    out[j] = (T)narrow(v + j < a.vocab ? x : 0.0f);
-                }
-            } else {
-                float h[V];
-                __builtin_memcpy(h, __builtin_assume_aligned(at, 16), sizeof h);
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    float x = h[j] * share;
-                    if (v + j == y) x -= s.share;
-                    out[j] = (T)(v + j < a.vocab ? x : 0.0f);
-                }
-            }
-            __builtin_memcpy(__builtin_assume_aligned(at, 16), out, sizeof out);
+            for (int j = 0; j < V; ++j) x[j] = (float)h[j];
         } else {
-#pragma unroll
-            for (int j = 0; j < V; ++j) out[j] = 0;
+            __builtin_memcpy(x, __builtin_assume_aligned(at, 16), sizeof x);
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) tile[r][c + j] = out[j];
+        for (int j = 0; j < V; ++j) {
+            float d = x[j] * share;
+            if (v + j == y) d -= s.share;
+            if (v + j >= a.vocab) d = 0.0f;
+            if constexpr (BF16) out[j] = narrow(d);
+            else out[j] = d;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) out[j] = 0;
     }
-    if (!e_t) return;
-    __syncthreads();
-    const int x = threadIdx.x % 64;
-    for (int k = threadIdx.x / 64; k < 64; k += 4)
-        if (v0 + k < a.vocab) static_cast<T *>(e_t)[(v0 + k) * piece_p + q0 + x] = tile[x][k];
+    __builtin_memcpy(__builtin_assume_aligned(at, 16), out, sizeof out);
 }
 
 // grad_hidden from the binary32 parts of the split product.
@@ -550,12 +618,12 @@ join_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t first,
 }
 
 // ------------------------------------------------------- launches
-template <bool BF16, int EPI>
+template <bool BF16, int EPI, bool TP, bool TQ>
 void start_product(const Product &g, int shape, hipStream_t stream) {
     const dim3 grid((unsigned)(g.tiles_p * g.tiles_q * g.splits));
-    if (shape == 0) product_kernel<BF16, EPI, 256, 256, 2, 4><<<grid, 512, 0, stream>>>(g);
-    else if (shape == 1) product_kernel<BF16, EPI, 128, 128, 2, 2><<<grid, 256, 0, stream>>>(g);
-    else product_kernel<BF16, EPI, 128, 32, 4, 1><<<grid, 256, 0, stream>>>(g);
+    if (shape == 0) product_kernel<BF16, EPI, TP, TQ, 256, 256, 2, 4><<<grid, 512, 0, stream>>>(g);
+    else if (shape == 1) product_kernel<BF16, EPI, TP, TQ, 128, 128, 2, 2><<<grid, 256, 0, stream>>>(g);
+    else product_kernel<BF16, EPI, TP, TQ, 128, 32, 4, 1><<<grid, 256, 0, stream>>>(g);
 }
 
 void set_tiles(Product &g, int shape, int splits) {
@@ -582,9 +650,6 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
                                                                  w + p.table_off, a.vocab, p.width_p);
         table = w + p.table_off;
     }
-    if (a.grad_hidden)
-        transpose_kernel<BF16><<<dim3((unsigned)ceil_div(p.vocab_p, 64), (unsigned)ceil_div(a.width, 64)), 256, 0, stream>>>(
-            a.table, a.vocab, a.width, nullptr, nullptr, 0, w + p.table_t_off, p.vocab_p);
     for (int64_t k = 0; k < p.pieces; ++k) {
         const int64_t first = k * p.piece;
         pack_kernel<BF16><<<(unsigned)p.piece_p, 256, 0, stream>>>(a.hidden, p.piece, a.width, map, sums, first,
@@ -593,7 +658,6 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
         g.sums = sums;
         g.first = first;
         g.piece = p.piece;
-        g.esize = es;
         g.map = map;
         g.p = table;
         g.ldp = p.width_p * es;
@@ -611,27 +675,26 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
         g.e = grads ? w + p.e_off : nullptr;
         g.lde = p.vocab_p;
         set_tiles(g, p.tile_logits, 1);
-        start_product<BF16, kLogits>(g, p.tile_logits, stream);
+        start_product<BF16, kLogits, false, false>(g, p.tile_logits, stream);
         softmax_kernel<<<(unsigned)ceil_div(p.piece, 4), 256, 0, stream>>>(a, sums, map, first, p.piece, stat,
                                                                            p.subtiles, rows, losses);
         if (!grads) continue;
-        gradient_kernel<BF16><<<dim3((unsigned)(p.vocab_p / 64), (unsigned)ceil_div(p.piece, 64)), 256, 0, stream>>>(
-            a, sums, map, first, p.piece, stat, p.subtiles, p.sub, rows, w + p.e_off, p.vocab_p,
-            a.grad_table ? w + p.e_t_off : nullptr, p.piece_p);
+        gradient_kernel<BF16><<<dim3((unsigned)ceil_div(p.vocab_p * es, 256 * 16), (unsigned)p.piece_p), 256, 0, stream>>>(
+            a, sums, map, first, p.piece, stat, p.subtiles, p.sub, rows, w + p.e_off, p.vocab_p);
         if (a.grad_hidden) {
             Product h = {};
             h.sums = sums;
             h.first = first;
             h.piece = p.piece;
-            h.esize = es;
-            h.p = w + p.table_t_off;
-            h.ldp = p.vocab_p * es;
+            h.p = table;
+            h.ldp = p.width_p * es;
+            h.kp = a.vocab;
             h.np = a.width;
             h.q = w + p.e_off;
             h.ldq = p.vocab_p * es;
             h.nq = p.piece;
             h.piece_is_q = true;
-            h.steps = p.vocab_p * es / 128;
+            h.steps = ceil_div(a.vocab * es, 128);    // every stage has a row of the table
             h.ldo = a.width;
             if (p.splits > 1) {
                 h.f32 = reinterpret_cast<float *>(w + p.split_off);
@@ -642,24 +705,22 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
                 h.out_bf16 = BF16;
             }
             set_tiles(h, p.tile_hidden, p.splits);
-            start_product<BF16, kStore>(h, p.tile_hidden, stream);
+            start_product<BF16, kStore, true, false>(h, p.tile_hidden, stream);
             if (p.splits > 1)
                 join_kernel<BF16><<<(unsigned)p.piece, 256, 0, stream>>>(a, sums, map, first, p.piece, h.f32, p.splits,
                                                                          h.f32_split);
         }
         if (a.grad_table) {
-            transpose_kernel<BF16><<<dim3((unsigned)ceil_div(p.piece_p, 64), (unsigned)ceil_div(a.width, 64)), 256, 0, stream>>>(
-                a.hidden, p.piece, a.width, map, sums, first, w + p.hidden_t_off, p.piece_p);
             Product t = {};
             t.sums = sums;
             t.first = first;
             t.piece = p.piece;
-            t.esize = es;
-            t.p = w + p.hidden_t_off;
-            t.ldp = p.piece_p * es;
+            t.p = w + p.hidden_off;
+            t.ldp = p.width_p * es;
+            t.kp = p.piece_p;
             t.np = a.width;
-            t.q = w + p.e_t_off;
-            t.ldq = p.piece_p * es;
+            t.q = w + p.e_off;
+            t.ldq = p.vocab_p * es;
             t.nq = a.vocab;
             t.piece_is_k = true;
             t.ldo = a.width;
@@ -675,7 +736,7 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
                 t.f32_in = k > 0 || (!a.table_grad_bf16 && a.accumulate) ? gw : nullptr;
             }
             set_tiles(t, p.tile_table, 1);
-            start_product<BF16, kStore>(t, p.tile_table, stream);
+            start_product<BF16, kStore, true, true>(t, p.tile_table, stream);
         }
     }
     loss_kernel<<<1, 1024, 0, stream>>>(a, sums, map, losses);

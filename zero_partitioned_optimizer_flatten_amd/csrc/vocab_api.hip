@@ -152,7 +152,7 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     p.width_p = round_up(a.width, step);
     p.vocab_p = round_up(a.vocab, 128);
     p.pack_table = (uintptr_t)a.table % 16 || p.width_p != a.width;
-    // a piece's e takes a GiB at most, and its transpose as much again
+    // a piece's e takes a GiB at most
     int64_t piece = rows > 0 ? rows : ((int64_t)1 << 30) / (p.vocab_p * es) / 256 * 256;
     if (rows <= 0) piece = piece < 256 ? 256 : piece > 262144 ? 262144 : piece;
     if (piece > a.count) piece = a.count;
@@ -166,7 +166,7 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     p.splits = 1;
     p.tile_hidden = choose_tile(a.width, piece, 4);
     const TileShape s = kTiles[p.tile_hidden];
-    const int64_t tiles = ceil_div(a.width, s.p) * ceil_div(piece, s.q), steps = p.vocab_p / step;
+    const int64_t tiles = ceil_div(a.width, s.p) * ceil_div(piece, s.q), steps = ceil_div(a.vocab, step);
     // enough workgroups for every compute unit, of 16 steps at least
     while (tiles * p.splits < 256 && steps / (p.splits + 1) >= 16) ++p.splits;
     p.tile_table = choose_tile(a.width, a.vocab, 1);
@@ -183,11 +183,8 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     p.row_off = take(sizeof(HeadRow) * piece);
     p.stat_off = take(8 * piece * p.subtiles);
     p.hidden_off = take(p.piece_p * p.width_p * es);
-    p.hidden_t_off = a.grad_table ? take(a.width * p.piece_p * es) : -1;
     p.table_off = p.pack_table ? take(a.vocab * p.width_p * es) : -1;
-    p.table_t_off = a.grad_hidden ? take(a.width * p.vocab_p * es) : -1;
-    p.e_off = grads ? take(piece * p.vocab_p * es) : -1;
-    p.e_t_off = a.grad_table ? take(a.vocab * p.piece_p * es) : -1;
+    p.e_off = grads ? take(p.piece_p * p.vocab_p * es) : -1;
     p.gw_off = a.grad_table && a.table_grad_bf16 && p.pieces > 1 ? take(4 * a.vocab * a.width) : -1;
     p.split_off = a.grad_hidden && p.splits > 1 ? take(4 * p.splits * piece * a.width) : -1;
     p.bytes = at;

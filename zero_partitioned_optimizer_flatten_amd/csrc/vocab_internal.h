@@ -119,8 +119,8 @@ struct HeadPlan {
     int64_t subtiles;             // statistics of a row
     int splits;                   // of the vocabulary axis in grad_hidden's product
     // workspace offsets in bytes; -1: not there
-    int64_t sum_off, map_off, loss_off, row_off, stat_off, hidden_off, hidden_t_off, table_off,
-        table_t_off, e_off, e_t_off, gw_off, split_off, bytes;
+    int64_t sum_off, map_off, loss_off, row_off, stat_off, hidden_off, table_off, e_off, gw_off,
+        split_off, bytes;
 };
 struct HeadArgs {
     const void *hidden, *table;
