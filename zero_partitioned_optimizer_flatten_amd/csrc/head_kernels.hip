@@ -60,8 +60,9 @@ __device__ __forceinline__ int piece_rows(const HeadSums *s, int64_t first, int6
 }
 
 // ------------------------------------------------------- which rows
-// One workgroup: the rows that take part, in order, and their weights' sum.
-__global__ void __launch_bounds__(1024) rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map) {
+// One workgroup: the rows that take part, in order, with their targets, and
+// their weights' sum.
+__global__ void __launch_bounds__(1024) rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target) {
     __shared__ int32_t found[16];
     __shared__ double parts[16];
     __shared__ float tops[16];
@@ -88,7 +89,11 @@ __global__ void __launch_bounds__(1024) rows_kernel(HeadArgs a, HeadSums *sums, 
             if (w < wave) at += found[w];
             base += found[w];
         }
-        if (on) map[at + __popcll(mask & ((1ull << lane) - 1))] = (int32_t)i;
+        if (on) {
+            at += __popcll(mask & ((1ull << lane) - 1));
+            map[at] = (int32_t)i;
+            target[at] = (int32_t)load_id(a.targets, a.wide_ids, i);
+        }
         __syncthreads();
     }
     for (int s = 32; s; s /= 2) {
@@ -149,7 +154,7 @@ pack_kernel(const void *src, int64_t rows, int64_t cols, const int32_t *map, con
 // different banks. A load to LDS writes lane after lane, so the exchange is made
 // in the addresses it reads from.
 
-enum Epilogue { kLogits, kStore };
+enum Epilogue { kLogits, kBf16, kF32 };
 
 struct Product {
     const void *p, *q;
@@ -163,20 +168,19 @@ struct Product {
     bool piece_is_q, piece_is_k;
     int64_t kp;                   // lines of a P across the long axis
     // kLogits
-    const void *targets;
-    bool wide_ids;
-    const int32_t *map;           // also of kStore's rows, if there
+    const int32_t *target;        // of the rows of Q
     f32x2 *stat;
     HeadRow *row;
     int64_t subtiles;
     void *e;                      // null: not wanted
     int64_t lde;                  // elements
-    // kStore: out (binary32 `f32`, or `out` in its type) = product + f32_in + old out
+    const int32_t *map;           // rows of the output, if they are others
+    // kBf16: out = scaled product + f32_in + old out; kF32: f32 = scaled product + f32_in
     float *f32;
     int64_t f32_split;            // elements between splits
-    const float *f32_in;
+    const float *f32_in;          // or null
     void *out;
-    bool out_bf16, add_out;
+    bool add_out;
     int64_t ldo;                  // elements, of f32, f32_in and out
 };
 
@@ -292,7 +296,8 @@ __device__ __forceinline__ void product(const Product &g) {
     using F = typename Frag<BF16>::type;
     using OpP = Operand<BF16, TP, BP, kLoadsP>;
     using OpQ = Operand<BF16, TQ, BQ, kLoadsQ>;
-    __shared__ __align__(1024) char lds[2][kStage];
+    constexpr int kOut = EPI != kF32 ? BQ * (2 * BP + 16) : 0;
+    __shared__ __align__(1024) char lds[2 * kStage > kOut ? 2 * kStage : kOut];
 
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -340,6 +345,14 @@ __device__ __forceinline__ void product(const Product &g) {
         lines -= OpP::kSteps;
     };
 
+    int target[kJ];
+    if constexpr (EPI == kLogits)
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+            const int64_t q = q0 + wave % WQ * (BQ / WQ) + lane % 16 + 16 * j;
+            target[j] = q < nq ? g.target[g.first + q] : -1;
+        }
+
     f32x4 acc[kI][kJ];
 #pragma unroll
     for (int i = 0; i < kI; ++i)
@@ -351,7 +364,7 @@ __device__ __forceinline__ void product(const Product &g) {
     const int wp = wave / WQ, wq = wave % WQ;
     F fp[2][kI / 2], fq[2][kJ];
     auto read = [&](int buf, int c) {
-        const char *s = lds[buf];
+        const char *s = lds + buf * kStage;
         if (c % 2 == 0)
 #pragma unroll
             for (int j = 0; j < kJ; ++j) fq[c / 2][j] = OpQ::read(s + BP * 128, wq * (BQ / WQ) + 16 * j, c / 2, lane);
@@ -399,95 +412,129 @@ __device__ __forceinline__ void product(const Product &g) {
     }
 
     // A lane holds outputs p = pw + 16 i + r, r < 4, of q = qw + 16 j.
-    const float scale = EPI == kStore ? g.sums->scale : 1.0f;
-    const int64_t pw = p0 + wp * (BP / WP) + lane / 16 * 4, qw = q0 + wq * (BQ / WQ) + lane % 16;
+    const int pl = wp * (BP / WP) + lane / 16 * 4, ql = wq * (BQ / WQ) + lane % 16;
+    const int64_t pw = p0 + pl, qw = q0 + ql;
+    const bool whole = p0 + BP <= g.np;
+    // Numbers of two bytes go out through LDS, [q][p], for whole lines: a lane's
+    // four are 8 bytes of a line, 16 lines to an instruction. 16 bytes between
+    // rows keep the 16 on different banks.
+    constexpr int kPitch = 2 * BP + 16;
+    auto put = [&](int i, int j, const uint16_t *h) {
+        __builtin_memcpy(__builtin_assume_aligned(lds + (ql + 16 * j) * kPitch + (pl + 16 * i) * 2, 8), h, 8);
+    };
+    if constexpr (EPI == kLogits) {
 #pragma unroll
-    for (int j = 0; j < kJ; ++j) {
-        const int64_t q = qw + 16 * j;
-        if (EPI == kLogits) {
+        for (int j = 0; j < kJ; ++j) {
+            const int64_t q = qw + 16 * j;
             const bool on = q < nq;
-            const int64_t y = on ? load_id(g.targets, g.wide_ids, g.map[g.first + q]) : -1;
+            if (!whole)
+#pragma unroll
+                for (int i = 0; i < kI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (pw + 16 * i + r >= g.np) acc[i][j][r] = -INFINITY;
+            const int yl = target[j] - (int)pw;
+            if (__ballot(yl >= 0 && yl < BP / WP && yl % 16 < 4))
+#pragma unroll
+                for (int i = 0; i < kI; ++i)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        if (yl == 16 * i + r) g.row[q].target = acc[i][j][r] * kLog2e;
             float top = -INFINITY;
 #pragma unroll
             for (int i = 0; i < kI; ++i)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    const int64_t p = pw + 16 * i + r;
-                    const float z = p < g.np ? acc[i][j][r] * kLog2e : -INFINITY;
-                    acc[i][j][r] = z;
-                    top = fmaxf(top, z);
-                    if (p == y) g.row[q].target = z;
-                }
+                for (int r = 0; r < 4; ++r) top = fmaxf(top, acc[i][j][r]);
             top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            const float base = top == -INFINITY ? 0.0f : top;
+            top = fmaxf(top, __shfl_xor(top, 32)) * kLog2e;
+            const float base = (BF16 ? kScaleLog2 : 0.0f) - (top == -INFINITY ? 0.0f : top);
             float sum = 0.0f;
 #pragma unroll
             for (int i = 0; i < kI; ++i) {
-                const int64_t p = pw + 16 * i;
                 float e[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    e[r] = __builtin_amdgcn_exp2f(acc[i][j][r] - base + (BF16 ? kScaleLog2 : 0.0f));
+                    e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, base));
                     sum += e[r];
                 }
-                if (g.e && on && p < g.lde) {
-                    if (BF16) {
-                        __attribute__((ext_vector_type(4))) _Float16 h = {(_Float16)e[0], (_Float16)e[1], (_Float16)e[2],
-                                                                          (_Float16)e[3]};
-                        *reinterpret_cast<decltype(h) *>(static_cast<_Float16 *>(g.e) + q * g.lde + p) = h;
-                    } else {
-                        *reinterpret_cast<f32x4 *>(static_cast<float *>(g.e) + q * g.lde + p) = f32x4{e[0], e[1], e[2], e[3]};
-                    }
+                if (!g.e) continue;
+                if constexpr (BF16) {
+                    const _Float16 h[4] = {(_Float16)e[0], (_Float16)e[1], (_Float16)e[2], (_Float16)e[3]};
+                    put(i, j, reinterpret_cast<const uint16_t *>(h));
+                } else if (on && pw + 16 * i < g.lde) {
+                    *reinterpret_cast<f32x4 *>(static_cast<float *>(g.e) + q * g.lde + pw + 16 * i) = f32x4{e[0], e[1], e[2], e[3]};
                 }
             }
             sum += __shfl_xor(sum, 16);
             sum += __shfl_xor(sum, 32);
             if (on && lane < 16)
                 g.stat[q * g.subtiles + (p0 / (BP / WP) + wp)] = f32x2{top, BF16 ? sum * 0x1p-15f : sum};
-        } else {
-            if (q >= nq) continue;
-            const int64_t row = g.map && g.out && !g.f32 ? (int64_t)g.map[g.first + q] : q;
+        }
+    } else {
+        const float scale = g.sums->scale;
+#pragma unroll
+        for (int j = 0; j < kJ; ++j) {
+            const int64_t q = qw + 16 * j;
+            if (EPI == kF32 && q >= nq) continue;
+            const int64_t row = q < nq ? (g.map ? (int64_t)g.map[g.first + q] : q) : -1, at = row * g.ldo + pw;
+            float *f = g.f32 + split * g.f32_split + at;
+            const float *fi = g.f32_in + at;
+            const uint16_t *old = static_cast<const uint16_t *>(g.out) + at;
 #pragma unroll
             for (int i = 0; i < kI; ++i) {
-                const int64_t p = pw + 16 * i;
-                if (p >= g.np) continue;
-                const int64_t left = g.np - p, at = row * g.ldo + p;
+                const int64_t left = row < 0 ? 0 : whole ? 4 : g.np - pw - 16 * i;
                 float v[4];
 #pragma unroll
                 for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r] * scale;
-                if (g.f32_in)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (r < left) v[r] += g.f32_in[at + r];
-                if (g.add_out)
-#pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (r < left)
-                            v[r] += g.out_bf16 ? widen(static_cast<const uint16_t *>(g.out)[at + r])
-                                               : static_cast<const float *>(g.out)[at + r];
-                if (g.f32) {
-                    float *d = g.f32 + split * g.f32_split + at;
-                    if (left >= 4) __builtin_memcpy(d, v, sizeof v);
+                if (g.f32_in) {
+                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (left >= 4) __builtin_memcpy(x, fi + 16 * i, sizeof x);
                     else
-                        for (int r = 0; r < 4; ++r)
-                            if (r < left) d[r] = v[r];
-                } else if (g.out_bf16) {
-                    uint16_t *d = static_cast<uint16_t *>(g.out) + at, h[4];
+                        for (int r = 0; r < 3; ++r)
+                            if (r < left) x[r] = fi[16 * i + r];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] += x[r];
+                }
+                if constexpr (EPI == kF32) {
+                    if (left >= 4) __builtin_memcpy(f + 16 * i, v, sizeof v);
+                    else
+                        for (int r = 0; r < 3; ++r)
+                            if (r < left) f[16 * i + r] = v[r];
+                } else {
+                    uint16_t h[4] = {0, 0, 0, 0};
+                    if (g.add_out) {
+                        if (left >= 4) __builtin_memcpy(h, old + 16 * i, sizeof h);
+                        else
+                            for (int r = 0; r < 3; ++r)
+                                if (r < left) h[r] = old[16 * i + r];
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] += widen(h[r]);
+                    }
 #pragma unroll
                     for (int r = 0; r < 4; ++r) h[r] = narrow(v[r]);
-                    if (left >= 4) __builtin_memcpy(d, h, sizeof h);
-                    else
-                        for (int r = 0; r < 4; ++r)
-                            if (r < left) d[r] = h[r];
-                } else {
-                    float *d = static_cast<float *>(g.out) + at;
-                    if (left >= 4) __builtin_memcpy(d, v, sizeof v);
-                    else
-                        for (int r = 0; r < 4; ++r)
-                            if (r < left) d[r] = v[r];
+                    put(i, j, h);
                 }
             }
+        }
+    }
+    if constexpr (EPI == kBf16 || (EPI == kLogits && BF16)) {
+        if (EPI == kLogits && !g.e) return;
+        __syncthreads();
+        constexpr int kAcross = BP / 8, kDown = 64 * kWaves / kAcross;    // 16-byte chunks of a line; lines at a time
+        const int64_t p = p0 + threadIdx.x % kAcross * 8;
+        const int64_t np = EPI == kLogits ? g.lde : g.np, ld = EPI == kLogits ? g.lde : g.ldo;
+        uint16_t *out = static_cast<uint16_t *>(EPI == kLogits ? g.e : g.out);
+        if (p >= np) return;
+#pragma unroll 4
+        for (int r = threadIdx.x / kAcross; r < BQ; r += kDown) {
+            if (q0 + r >= nq) break;
+            const int64_t row = EPI == kBf16 && g.map ? (int64_t)g.map[g.first + q0 + r] : q0 + r;
+            uint16_t h[8], *d = out + row * ld + p;
+            __builtin_memcpy(h, __builtin_assume_aligned(lds + r * kPitch + threadIdx.x % kAcross * 16, 16), sizeof h);
+            if (p + 8 <= np) __builtin_memcpy(d, h, sizeof h);
+            else
+                for (int k = 0; k < 7; ++k)
+                    if (p + k < np) d[k] = h[k];
         }
     }
 }
@@ -563,7 +610,7 @@ __global__ void __launch_bounds__(256) idle_rows_kernel(HeadArgs a, float *losse
 // thread, grid (columns, rows).
 template <bool BF16>
 __global__ void __launch_bounds__(256)
-gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t first, int64_t piece,
+gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *target, int64_t first, int64_t piece,
                 const f32x2 *stat, int64_t subtiles, int sub, const HeadRow *rows, void *e,
                 int64_t vocab_p) {
     using T = typename Elem<BF16>::type;
@@ -574,7 +621,7 @@ gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t fi
     T *at = static_cast<T *>(e) + q * vocab_p + v, out[V];
     if (q < n) {
         const HeadRow s = rows[q];
-        const int64_t y = load_id(a.targets, a.wide_ids, map[first + q]);
+        const int64_t y = target[first + q];
         const float share = __builtin_amdgcn_exp2f(stat[q * subtiles + v / sub].x - s.top) * s.inv
                             * (BF16 ? 0x1p-15f : 1.0f);
         float x[V];
@@ -637,12 +684,12 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
     char *w = a.workspace;
     const int es = BF16 ? 2 : 4;
     auto *sums = reinterpret_cast<HeadSums *>(w + p.sum_off);
-    auto *map = reinterpret_cast<int32_t *>(w + p.map_off);
+    auto *map = reinterpret_cast<int32_t *>(w + p.map_off), *target = map + a.count;
     auto *losses = a.losses ? a.losses : reinterpret_cast<float *>(w + p.loss_off);
     auto *rows = reinterpret_cast<HeadRow *>(w + p.row_off);
     auto *stat = reinterpret_cast<f32x2 *>(w + p.stat_off);
     const bool grads = a.grad_hidden || a.grad_table;
-    rows_kernel<<<1, 1024, 0, stream>>>(a, sums, map);
+    rows_kernel<<<1, 1024, 0, stream>>>(a, sums, map, target);
     if (a.count > 0) idle_rows_kernel<<<(unsigned)ceil_div(a.count, 4), 256, 0, stream>>>(a, losses);
     const void *table = a.table;
     if (p.pack_table) {
@@ -658,7 +705,6 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
         g.sums = sums;
         g.first = first;
         g.piece = p.piece;
-        g.map = map;
         g.p = table;
         g.ldp = p.width_p * es;
         g.np = a.vocab;
@@ -667,8 +713,7 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
         g.nq = p.piece;
         g.piece_is_q = true;
         g.steps = p.width_p * es / 128;
-        g.targets = a.targets;
-        g.wide_ids = a.wide_ids;
+        g.target = target;
         g.stat = stat;
         g.row = rows;
         g.subtiles = p.subtiles;
@@ -680,7 +725,7 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
                                                                            p.subtiles, rows, losses);
         if (!grads) continue;
         gradient_kernel<BF16><<<dim3((unsigned)ceil_div(p.vocab_p * es, 256 * 16), (unsigned)p.piece_p), 256, 0, stream>>>(
-            a, sums, map, first, p.piece, stat, p.subtiles, p.sub, rows, w + p.e_off, p.vocab_p);
+            a, sums, target, first, p.piece, stat, p.subtiles, p.sub, rows, w + p.e_off, p.vocab_p);
         if (a.grad_hidden) {
             Product h = {};
             h.sums = sums;
@@ -696,16 +741,17 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
             h.piece_is_q = true;
             h.steps = ceil_div(a.vocab * es, 128);    // every stage has a row of the table
             h.ldo = a.width;
+            set_tiles(h, p.tile_hidden, p.splits);
             if (p.splits > 1) {
                 h.f32 = reinterpret_cast<float *>(w + p.split_off);
                 h.f32_split = p.piece * a.width;
+                start_product<BF16, kF32, true, false>(h, p.tile_hidden, stream);
             } else {
                 h.map = map;
                 h.out = a.grad_hidden;
-                h.out_bf16 = BF16;
+                h.f32 = static_cast<float *>(a.grad_hidden);
+                start_product<BF16, BF16 ? kBf16 : kF32, true, false>(h, p.tile_hidden, stream);
             }
-            set_tiles(h, p.tile_hidden, p.splits);
-            start_product<BF16, kStore, true, false>(h, p.tile_hidden, stream);
             if (p.splits > 1)
                 join_kernel<BF16><<<(unsigned)p.piece, 256, 0, stream>>>(a, sums, map, first, p.piece, h.f32, p.splits,
                                                                          h.f32_split);
@@ -726,17 +772,16 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
             t.ldo = a.width;
             const bool last = k + 1 == p.pieces;
             float *gw = a.table_grad_bf16 ? reinterpret_cast<float *>(w + p.gw_off) : static_cast<float *>(a.grad_table);
+            set_tiles(t, p.tile_table, 1);
+            t.f32_in = k > 0 || (!a.table_grad_bf16 && a.accumulate) ? gw : nullptr;
             if (a.table_grad_bf16 && last) {
                 t.out = a.grad_table;
-                t.out_bf16 = true;
                 t.add_out = a.accumulate;
-                t.f32_in = k > 0 ? gw : nullptr;
+                start_product<BF16, kBf16, true, true>(t, p.tile_table, stream);
             } else {
                 t.f32 = gw;
-                t.f32_in = k > 0 || (!a.table_grad_bf16 && a.accumulate) ? gw : nullptr;
+                start_product<BF16, kF32, true, true>(t, p.tile_table, stream);
             }
-            set_tiles(t, p.tile_table, 1);
-            start_product<BF16, kStore, true, true>(t, p.tile_table, stream);
         }
     }
     loss_kernel<<<1, 1024, 0, stream>>>(a, sums, map, losses);

@@ -178,7 +178,7 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     };
     const bool grads = a.grad_hidden || a.grad_table;
     p.sum_off = take(sizeof(HeadSums));
-    p.map_off = take(4 * a.count);
+    p.map_off = take(8 * a.count);           // and their targets
     p.loss_off = a.losses ? -1 : take(4 * a.count);
     p.row_off = take(sizeof(HeadRow) * piece);
     p.stat_off = take(8 * piece * p.subtiles);
