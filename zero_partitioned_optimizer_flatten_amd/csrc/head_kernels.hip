@@ -56,7 +56,7 @@ __device__ __forceinline__ bool takes_part(const HeadArgs &a, int64_t i) {
 
 __device__ __forceinline__ int piece_rows(const HeadSums *s, int64_t first, int64_t piece) {
     const int64_t n = s->rows - first;
-    return (int)(n < 0 ? 0 : n < piece ? n : piece);
+    return __builtin_amdgcn_readfirstlane((int)(n < 0 ? 0 : n < piece ? n : piece));
 }
 
 // ------------------------------------------------------- which rows
@@ -160,13 +160,14 @@ struct Product {
     const void *p, *q;
     int64_t ldp, ldq;             // bytes
     int64_t np, nq;               // rows
+    int64_t kp, kq;               // lines of operands across the long axis
     int64_t steps;                // of 128 bytes on the long axis
-    int tiles_p, tiles_q, splits;
+    int slots;                    // room for parts of tiles (0: tiles are not cut)
+    float *parts;
     // with sums: rows of the piece, which bound nq or the long axis
     const HeadSums *sums;
     int64_t first, piece;
     bool piece_is_q, piece_is_k;
-    int64_t kp;                   // lines of a P across the long axis
     // kLogits
     const int32_t *target;        // of the rows of Q
     f32x2 *stat;
@@ -174,15 +175,92 @@ struct Product {
     int64_t subtiles;
     void *e;                      // null: not wanted
     int64_t lde;                  // elements
-    const int32_t *map;           // rows of the output, if they are others
     // kBf16: out = scaled product + f32_in + old out; kF32: f32 = scaled product + f32_in
+    const int32_t *map;           // rows of the output, if they are others
     float *f32;
-    int64_t f32_split;            // elements between splits
     const float *f32_in;          // or null
     void *out;
     bool add_out;
     int64_t ldo;                  // elements, of f32, f32_in and out
 };
+
+// Which workgroup makes what. Tiles are dealt to `at_once` workgroups, as many as
+// run at a time; those of a last, incomplete round are cut along the long axis
+// into parts, whose sums go to slots and are joined by another kernel. 7B list's
+// grad_hidden of 6553 rows: 416 tiles on 256 compute units, 160 of them in three
+// parts, took 1.45 ms where two whole rounds took 1.68.
+struct Schedule {
+    int tiles_p, tiles_q, whole, cut, parts, units;
+    int steps, per;               // of a whole tile, of a part
+};
+
+// Every lane has the same value; the compiler is not always aware of it.
+__device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
+
+__device__ __forceinline__ Schedule schedule(const Product &g, int bp, int bq, int es, int at_once) {
+    Schedule s;
+    int nq = (int)g.nq;
+    s.steps = (int)g.steps;
+    if (g.sums) {
+        const int n = piece_rows(g.sums, g.first, g.piece);
+        if (g.piece_is_q) nq = n;
+        if (g.piece_is_k) s.steps = (n * es + 127) / 128;
+    }
+    s.tiles_p = ((int)g.np + bp - 1) / bp;
+    s.tiles_q = (nq + bq - 1) / bq;
+    const int tiles = s.tiles_p * s.tiles_q;
+    s.cut = uniform(tiles % at_once);
+    s.whole = tiles - s.cut;
+    s.parts = 1;
+    s.per = s.steps;
+    // in steps: rounds of parts with what a part costs besides, and the joining
+    int best = s.steps + 8;
+    for (int k = 2; k <= 8 && s.cut > 0; ++k) {
+        if (s.steps < 16 * k || s.cut * k > g.slots) break;
+        const int per = uniform((s.steps + k - 1) / k);
+        const int cost = uniform((s.cut * k + at_once - 1) / at_once) * (per + 8) + s.cut * k / 11;
+        if (cost < best) best = cost, s.parts = k, s.per = per;
+    }
+    s.units = s.whole + s.cut * s.parts;
+    return s;
+}
+
+// The tile at place t of n: workgroups go round robin over the 8 XCDs, so each
+// XCD gets a run of neighbouring tiles, in groups of 8 along p, to share its L2.
+__device__ __forceinline__ void place(const Schedule &s, int t, int n, int first, int *p, int *q) {
+    const int per = n / 8, rest = n % 8, x = t % 8;
+    t = first + x * per + (x < rest ? x : rest) + t / 8;
+    const int group = t / (8 * s.tiles_q), in = t % (8 * s.tiles_q);
+    const int gp = s.tiles_p - 8 * group < 8 ? s.tiles_p - 8 * group : 8;
+    *p = uniform(8 * group + in % gp);
+    *q = uniform(in / gp);
+}
+
+struct Unit {
+    int64_t p0, q0;
+    int k0, steps, slot;          // slot < 0: a whole tile
+};
+
+__device__ __forceinline__ Unit unit_of(const Schedule &s, int u, int bp, int bq) {
+    Unit r;
+    int p, q;
+    r.k0 = 0;
+    r.steps = s.steps;
+    r.slot = -1;
+    if (u < s.whole || s.parts == 1) {
+        if (u < s.whole) place(s, u, s.whole, 0, &p, &q);
+        else place(s, u - s.whole, s.cut, s.whole, &p, &q);
+    } else {
+        const int part = uniform((u - s.whole) / s.cut), t = u - s.whole - part * s.cut;
+        place(s, t, s.cut, s.whole, &p, &q);
+        r.k0 = s.per * part;
+        r.steps = s.steps - r.k0 < s.per ? s.steps - r.k0 : s.per;
+        r.slot = t * s.parts + part;
+    }
+    r.p0 = (int64_t)p * bp;
+    r.q0 = (int64_t)q * bq;
+    return r;
+}
 
 template <bool BF16> struct Frag { using type = f32x4; };
 template <> struct Frag<true> { using type = bf16x8; };
@@ -198,13 +276,13 @@ __device__ __forceinline__ f32x4 mma(f32x4 p, f32x4 q, f32x4 c) {
     return c;
 }
 
-// 16 bytes a lane, from base + from, to LDS at `lds` + 16 * lane. In assembly,
-// since the compiler would otherwise wait for all such loads before it reads LDS
-// across lanes (ds_read_b64_tr_b16); the waits are the loop's own. No register is
-// written.
-__device__ __forceinline__ void load_to_lds(const char *base, int from, uint32_t lds) {
+// 16 bytes a lane, from base + from, to LDS at `lds` + 16 * lane; nothing from
+// base + bytes on is read. In assembly, since the compiler would otherwise wait
+// for all such loads before it reads LDS across lanes (ds_read_b64_tr_b16); the
+// waits are the loop's own. No register is written.
+__device__ __forceinline__ void load_to_lds(const char *base, uint32_t bytes, int from, uint32_t lds) {
     typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
-    const u32x4 r = {(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32) & 0xFFFFu, 0xFFFFFFFFu, 0x00027000u};
+    const u32x4 r = {(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32) & 0xFFFFu, bytes, 0x00027000u};
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(from), "s"(r)
@@ -218,7 +296,9 @@ struct Operand {
     static constexpr int kEs = BF16 ? 2 : 4, kSteps = 128 / kEs;
     static constexpr int kLine = T ? B * kEs : 128;           // bytes of a line in LDS
     int at[LOADS];                                            // what each load's lane reads
-    int64_t step;                                             // bytes from stage to stage
+    int step;                                                 // bytes from stage to stage
+    const char *base;                                         // of the next stage
+    int64_t room;                                             // bytes from there to the operand's end
 
     // Where the 16-byte chunk at place c of line k comes from.
     static __device__ __forceinline__ int source(int k, int c) {
@@ -226,29 +306,27 @@ struct Operand {
         if (BF16) return c ^ ((((k & 3) | ((k >> 1) & 4)) << 1) & (kLine / 16 - 1));
         return c ^ (((k >> 2) & 3) << 2 & (kLine / 16 - 1));
     }
-    // Rows (T: 16-byte columns) behind the operand's last are read as the last:
-    // always memory of the operand.
-    __device__ __forceinline__ void init(int wave, int lane, int64_t first, int64_t n, int64_t ld) {
+    __device__ __forceinline__ void init(int wave, int lane, int ld) {
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
-            const int byte = (wave * LOADS + j) * 1024 + lane * 16;
-            const int line = byte / kLine, chunk = source(line, byte % kLine / 16);
-            if (T) {
-                int64_t col = first * kEs + chunk * 16;
-                if (col > ld - 16) col = ld - 16;
-                at[j] = (int)(line * ld + (col - first * kEs));
-            } else {
-                int64_t r = line;
-                if (first + r >= n) r = n - 1 - first;
-                at[j] = (int)(r * ld) + chunk * 16;
-            }
+            const int byte = (wave * LOADS + j) * 1024 + lane * 16, line = byte / kLine;
+            at[j] = line * ld + source(line, byte % kLine / 16) * 16;
         }
         step = T ? kSteps * ld : 128;
     }
-    // lds: the operand's place in the stage. T: of a stage with fewer than
-    // kSteps lines (`left` >= 1) those behind are read as the last.
+    // Rows behind the operand's last, and columns behind a line's (T), bring
+    // whatever is there or nothing: they make outputs that are not stored.
+    __device__ __forceinline__ void begin(const void *operand, int64_t first, int64_t ld, int64_t lines, int k0) {
+        const int64_t off = (T ? first * kEs : first * ld) + (int64_t)k0 * step;
+        base = static_cast<const char *>(operand) + off;
+        room = lines * ld - off;
+    }
+    // lds: the operand's place in the stage. LAST (T): of a stage with fewer than
+    // kSteps lines (`left` >= 1) those behind are read as the last; they meet zeros
+    // of the other operand, and LDS might hold a NaN.
     template <bool LAST>
-    __device__ __forceinline__ void load(const char *base, uint32_t lds, int wave, int lane, int left, int ld) const {
+    __device__ __forceinline__ void load(uint32_t lds, int wave, int lane, int left, int ld) {
+        const uint32_t bytes = room < 0xFFFFFFFFll ? (uint32_t)room : 0xFFFFFFFFu;
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
             int from = at[j];
@@ -256,8 +334,10 @@ struct Operand {
                 const int line = ((wave * LOADS + j) * 1024 + lane * 16) / kLine;
                 if (line >= left) from -= (line - (left - 1)) * ld;
             }
-            load_to_lds(base, from, lds + (wave * LOADS + j) * 1024);
+            load_to_lds(base, bytes, from, lds + (wave * LOADS + j) * 1024);
         }
+        base += step;
+        room -= step;
     }
     // Fragment: 16 rows from row0 (a multiple of 16), half h of the stage.
     static __device__ __forceinline__ typename Frag<BF16>::type read(const char *lds, int row0, int h, int lane) {
@@ -286,91 +366,69 @@ struct Operand {
     }
 };
 
-template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ>
+template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE>
 __device__ __forceinline__ void product(const Product &g) {
     constexpr int kWaves = WP * WQ;
-    constexpr int kI = BP / WP / 16, kJ = BQ / WQ / 16;       // fragments of a wave
+    constexpr int kP = BP / WP, kQ = BQ / WQ;                 // outputs of a wave
+    constexpr int kI = kP / 16, kJ = kQ / 16;                 // its fragments
     constexpr int kLoadsP = BP / 8 / kWaves, kLoadsQ = BQ / 8 / kWaves;
     static_assert(kLoadsP * 8 * kWaves == BP && kLoadsQ * 8 * kWaves == BQ, "whole loads");
     constexpr int kStage = (BP + BQ) * 128;
     using F = typename Frag<BF16>::type;
     using OpP = Operand<BF16, TP, BP, kLoadsP>;
     using OpQ = Operand<BF16, TQ, BQ, kLoadsQ>;
-    constexpr int kOut = EPI != kF32 ? BQ * (2 * BP + 16) : 0;
-    __shared__ __align__(1024) char lds[2 * kStage > kOut ? 2 * kStage : kOut];
+    // Outputs of two bytes are turned in LDS, 16 rows of q at a time, a wave its own.
+    constexpr bool kTurned = EPI == kBf16 || (EPI == kLogits && BF16);
+    constexpr int kTurn = kTurned ? 16 * kP * 2 : 0;
+    __shared__ __align__(1024) char lds[2 * kStage + kWaves * kTurn];
 
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-    int64_t nq = g.nq, steps = g.steps;
-    if (g.sums) {
-        const int n = piece_rows(g.sums, g.first, g.piece);
-        if (g.piece_is_q) nq = n;
-        if (g.piece_is_k) steps = ceil_div((int64_t)n * OpP::kEs, 128);
-    }
+    const int wp = wave / WQ, wq = wave % WQ;
+    const Schedule sc = schedule(g, BP, BQ, OpP::kEs, AT_ONCE);
+    const int64_t nq = g.sums && g.piece_is_q ? piece_rows(g.sums, g.first, g.piece) : g.nq;
+    if ((int)blockIdx.x >= sc.units) return;
 
-    // Workgroups go round robin over the 8 XCDs: give each XCD a run of
-    // neighbouring tiles, in groups of 8 along p, so that its L2 is shared.
-    const int tiles = g.tiles_p * g.tiles_q;
-    const int split = blockIdx.x / tiles;
-    int t = blockIdx.x % tiles;
-    {
-        const int per = tiles / 8, rest = tiles % 8, x = t % 8;
-        t = x * per + (x < rest ? x : rest) + t / 8;
-    }
-    const int group = t / (8 * g.tiles_q), in = t % (8 * g.tiles_q);
-    const int gp = g.tiles_p - 8 * group < 8 ? g.tiles_p - 8 * group : 8;
-    const int64_t p0 = (int64_t)(8 * group + in % gp) * BP, q0 = (int64_t)(in / gp) * BQ;
-    if (q0 >= nq) return;
-    const int64_t per_split = ceil_div(steps, g.splits);
-    const int64_t k0 = per_split * split;
-    const int ksteps = (int)(k0 >= steps ? 0 : steps - k0 < per_split ? steps - k0 : per_split);
-
+    // The loads run two stages ahead of the products, over the ends of units.
     OpP op;
     OpQ oq;
-    op.init(wave, lane, p0, g.np, g.ldp);
-    oq.init(wave, lane, q0, nq, g.ldq);
-    const char *bp = static_cast<const char *>(g.p) + (TP ? p0 * OpP::kEs : p0 * g.ldp) + k0 * op.step;
-    const char *bq = static_cast<const char *>(g.q) + (TQ ? q0 * OpQ::kEs : q0 * g.ldq) + k0 * oq.step;
-    // lines of P that are left (TP: the table's rows are not padded)
-    int64_t lines = TP ? g.kp - k0 * OpP::kSteps : 0;
+    op.init(wave, lane, (int)g.ldp);
+    oq.init(wave, lane, (int)g.ldq);
+    int lines = 0;                // of P left (TP: the table's rows are not padded)
+    int next = blockIdx.x, left = 0;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
-
+    auto begin = [&]() {
+        const Unit u = unit_of(sc, next, BP, BQ);
+        op.begin(g.p, u.p0, g.ldp, TP ? g.kp : g.np, u.k0);
+        oq.begin(g.q, u.q0, g.ldq, TQ ? g.kq : nq, u.k0);
+        if (TP) lines = (int)g.kp - u.k0 * OpP::kSteps;
+        left = u.steps;
+    };
     auto load = [&](int buf) {
+        if (left == 0) return;
         const uint32_t s = lds0 + buf * kStage;
-        if (TP && lines < OpP::kSteps) op.template load<true>(bp, s, wave, lane, (int)lines, (int)g.ldp);
-        else op.template load<false>(bp, s, wave, lane, 0, 0);
-        oq.template load<false>(bq, s + BP * 128, wave, lane, 0, 0);
-        bp += op.step;
-        bq += oq.step;
+        if (TP && lines < OpP::kSteps) op.template load<true>(s, wave, lane, lines, (int)g.ldp);
+        else op.template load<false>(s, wave, lane, 0, 0);
+        oq.template load<false>(s + BP * 128, wave, lane, 0, 0);
         lines -= OpP::kSteps;
+        if (--left == 0) {
+            next += gridDim.x;
+            if (next < sc.units) begin();
+        }
+        asm volatile("" : "+s"(left));            // one loop, not one for each way it can end
     };
 
-    int target[kJ];
-    if constexpr (EPI == kLogits)
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-            const int64_t q = q0 + wave % WQ * (BQ / WQ) + lane % 16 + 16 * j;
-            target[j] = q < nq ? g.target[g.first + q] : -1;
-        }
-
     f32x4 acc[kI][kJ];
-#pragma unroll
-    for (int i = 0; i < kI; ++i)
-#pragma unroll
-        for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-
     // A stage is multiplied in four parts: part c takes half c / 2 of the long axis
     // and half c % 2 of the wave's rows of P.
-    const int wp = wave / WQ, wq = wave % WQ;
     F fp[2][kI / 2], fq[2][kJ];
     auto read = [&](int buf, int c) {
         const char *s = lds + buf * kStage;
         if (c % 2 == 0)
 #pragma unroll
-            for (int j = 0; j < kJ; ++j) fq[c / 2][j] = OpQ::read(s + BP * 128, wq * (BQ / WQ) + 16 * j, c / 2, lane);
+            for (int j = 0; j < kJ; ++j) fq[c / 2][j] = OpQ::read(s + BP * 128, wq * kQ + 16 * j, c / 2, lane);
 #pragma unroll
-        for (int i = 0; i < kI / 2; ++i)
-            fp[c % 2][i] = OpP::read(s, wp * (BP / WP) + 16 * (c % 2 * (kI / 2) + i), c / 2, lane);
+        for (int i = 0; i < kI / 2; ++i) fp[c % 2][i] = OpP::read(s, wp * kP + 16 * (c % 2 * (kI / 2) + i), c / 2, lane);
     };
     auto multiply = [&](int c) {
 #pragma unroll
@@ -382,166 +440,270 @@ __device__ __forceinline__ void product(const Product &g) {
             }
     };
 
-    // Each part is read while the one before is multiplied. When the last part of a
-    // stage has been read by all, the loads of the stage after the next go to its
-    // place, so a load has nearly a stage's time to arrive and a wave meets one
-    // barrier a stage, with products still to do.
-    if (ksteps > 0) load(0);
-    if (ksteps > 1) load(1);
-    if (ksteps > 1) asm volatile("s_waitcnt vmcnt(%0)\n\ts_barrier" : : "n"(kLoadsP + kLoadsQ) : "memory");
-    else asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
-    if (ksteps > 0) read(0, 0);
-    for (int k = 0; k < ksteps; ++k) {
-        const int buf = k & 1;
-        read(buf, 1);
-        __builtin_amdgcn_sched_barrier(0);        // the reads go first, whatever the scheduler thinks
-        multiply(0);
-        __builtin_amdgcn_sched_barrier(0);
-        read(buf, 2);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(1);
-        __builtin_amdgcn_sched_barrier(0);
-        read(buf, 3);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(2);
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
-        if (k + 2 < ksteps) load(buf);
-        if (k + 1 < ksteps) read(buf ^ 1, 0);
-        __builtin_amdgcn_sched_barrier(0);
-        multiply(3);
-    }
-
-    // A lane holds outputs p = pw + 16 i + r, r < 4, of q = qw + 16 j.
-    const int pl = wp * (BP / WP) + lane / 16 * 4, ql = wq * (BQ / WQ) + lane % 16;
-    const int64_t pw = p0 + pl, qw = q0 + ql;
-    const bool whole = p0 + BP <= g.np;
-    // Numbers of two bytes go out through LDS, [q][p], for whole lines: a lane's
-    // four are 8 bytes of a line, 16 lines to an instruction. 16 bytes between
-    // rows keep the 16 on different banks.
-    constexpr int kPitch = 2 * BP + 16;
-    auto put = [&](int i, int j, const uint16_t *h) {
-        __builtin_memcpy(__builtin_assume_aligned(lds + (ql + 16 * j) * kPitch + (pl + 16 * i) * 2, 8), h, 8);
-    };
-    if constexpr (EPI == kLogits) {
+    int target[kJ];
+    auto targets = [&](int u) {
+        if constexpr (EPI == kLogits) {
+            if (u >= sc.units) return;
+            const int64_t q = unit_of(sc, u, BP, BQ).q0 + wq * kQ + lane % 16;
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-            const int64_t q = qw + 16 * j;
-            const bool on = q < nq;
+            for (int j = 0; j < kJ; ++j) target[j] = q + 16 * j < nq ? g.target[g.first + q + 16 * j] : -1;
+        }
+    };
+    // This wave's loads have arrived. The compiler does not count the loads to LDS;
+    // it is told here, where nothing is left to wait for, that the targets are in.
+    auto arrived = [&]() {
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+        if constexpr (EPI == kLogits)
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) asm volatile("" : "+v"(target[j]));
+    };
+
+    if (sc.steps > 0) begin();
+    load(0);
+    load(1);
+    targets(blockIdx.x);
+    arrived();
+    asm volatile("s_barrier" ::: "memory");
+    read(0, 0);
+    int stage = 0;
+    for (int unit = blockIdx.x; unit < sc.units; unit += gridDim.x) {
+        const Unit u = unit_of(sc, unit, BP, BQ);
+#pragma unroll
+        for (int i = 0; i < kI; ++i)
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) acc[i][j] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+        // Each part is read while the one before is multiplied. When the last part of a
+        // stage has been read by all, the loads of the stage after the next go to its
+        // place, so a load has nearly a stage's time to arrive and a wave meets one
+        // barrier a stage, with products still to do. A unit's first part is read with
+        // the last of the unit before, and its first two stages have arrived before
+        // that one's outputs are stored.
+        for (int k = 0; k < u.steps; ++k) {
+            const int buf = (stage + k) & 1;
+            int later = k;
+            asm volatile("" : "+s"(later));       // no first round of its own
+            read(buf, 1);
+            __builtin_amdgcn_sched_barrier(0);    // the reads go first, whatever the scheduler thinks
+            multiply(0);
+            __builtin_amdgcn_sched_barrier(0);
+            read(buf, 2);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(1);
+            __builtin_amdgcn_sched_barrier(0);
+            read(buf, 3);
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(2);
+            if (later > 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            load(buf);
+            read(buf ^ 1, 0);                     // after the last unit: of no use, but there
+            __builtin_amdgcn_sched_barrier(0);
+            multiply(3);
+        }
+        stage += u.steps;
+
+        // A lane holds outputs p = pw + 16 i + r, r < 4, of q = qw + 16 j. What is
+        // stored is stored after the loads under way have arrived: the wait for the
+        // next stage would wait for the stores as well.
+        const int64_t pw = u.p0 + wp * kP + lane / 16 * 4, qw = u.q0 + wq * kQ + lane % 16;
+        const bool whole = u.p0 + BP <= g.np;
+        char *turn = lds + 2 * kStage + wave * kTurn;
+        // 16 rows of kP numbers of two bytes; 16-byte chunk c of row r at c ^ r.
+        constexpr int kChunks = kP / 8;
+        auto put = [&](int i, const uint16_t *h) {
+            const int r = lane % 16, c = 2 * i + lane / 32;
+            __builtin_memcpy(__builtin_assume_aligned(turn + r * kP * 2 + (c ^ (r % kChunks)) * 16 + lane / 16 % 2 * 8, 8), h, 8);
+        };
+        // Rows j of the turned numbers to `out`, whole lines of the wave's columns.
+        auto send = [&](int j, uint16_t *out, int64_t ld, int64_t np) {
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+            constexpr int kDown = 64 / kChunks;
+            const int c = lane % kChunks;
+            const int64_t p = u.p0 + wp * kP + c * 8;
+#pragma unroll
+            for (int r0 = 0; r0 < 16; r0 += kDown) {
+                const int r = r0 + lane / kChunks;
+                const int64_t q = u.q0 + wq * kQ + 16 * j + r;
+                uint16_t h[8];
+                __builtin_memcpy(h, __builtin_assume_aligned(turn + r * kP * 2 + (c ^ (r % kChunks)) * 16, 16), sizeof h);
+                if (q < nq && p < np) {
+                    const int64_t row = EPI == kBf16 && g.map ? (int64_t)g.map[g.first + q] : q;
+                    uint16_t *d = out + row * ld + p;
+                    if (p + 8 <= np) __builtin_memcpy(d, h, sizeof h);
+                    else
+                        for (int k = 0; k < 7; ++k)
+                            if (p + k < np) d[k] = h[k];
+                }
+            }
+            asm volatile("" ::: "memory");
+            __builtin_amdgcn_wave_barrier();
+        };
+
+        if constexpr (EPI == kLogits) {
+            float tops[kJ], sums[kJ], hit[kJ];
+            int yl[kJ];
             if (!whole)
 #pragma unroll
+                for (int j = 0; j < kJ; ++j)
+#pragma unroll
+                    for (int i = 0; i < kI; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (pw + 16 * i + r >= g.np) acc[i][j][r] = -INFINITY;
+#pragma unroll
+            for (int j = 0; j < kJ; ++j) {
+                yl[j] = target[j] - (int)pw;
+                if (yl[j] < 0 || yl[j] >= kP || yl[j] % 16 >= 4) yl[j] = -1;
+                hit[j] = 0.0f;
+                if (__ballot(yl[j] >= 0))
+#pragma unroll
+                    for (int i = 0; i < kI; ++i)
+#pragma unroll
+                        for (int r = 0; r < 4; ++r)
+                            if (yl[j] == 16 * i + r) hit[j] = acc[i][j][r] * kLog2e;
+                float top = -INFINITY;
+#pragma unroll
                 for (int i = 0; i < kI; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (pw + 16 * i + r >= g.np) acc[i][j][r] = -INFINITY;
-            const int yl = target[j] - (int)pw;
-            if (__ballot(yl >= 0 && yl < BP / WP && yl % 16 < 4))
+                    for (int r = 0; r < 4; ++r) top = fmaxf(top, acc[i][j][r]);
+                top = fmaxf(top, __shfl_xor(top, 16));
+                top = fmaxf(top, __shfl_xor(top, 32)) * kLog2e;
+                const float base = (BF16 ? kScaleLog2 : 0.0f) - (top == -INFINITY ? 0.0f : top);
+                float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kI; ++i)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r)
-                        if (yl == 16 * i + r) g.row[q].target = acc[i][j][r] * kLog2e;
-            float top = -INFINITY;
+                    for (int r = 0; r < 4; ++r) {
+                        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, base));
+                        acc[i][j][r] = e;
+                        sum += e;
+                    }
+                sum += __shfl_xor(sum, 16);
+                sum += __shfl_xor(sum, 32);
+                tops[j] = top;
+                sums[j] = BF16 ? sum * 0x1p-15f : sum;
+            }
+            targets(unit + (int)gridDim.x);
+            arrived();
 #pragma unroll
-            for (int i = 0; i < kI; ++i)
-#pragma unroll
-                for (int r = 0; r < 4; ++r) top = fmaxf(top, acc[i][j][r]);
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32)) * kLog2e;
-            const float base = (BF16 ? kScaleLog2 : 0.0f) - (top == -INFINITY ? 0.0f : top);
-            float sum = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kI; ++i) {
-                float e[4];
-#pragma unroll
-                for (int r = 0; r < 4; ++r) {
-                    e[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, base));
-                    sum += e[r];
-                }
+            for (int j = 0; j < kJ; ++j) {
+                const int64_t q = qw + 16 * j;
+                if (yl[j] >= 0) g.row[q].target = hit[j];
+                if (q < nq && lane < 16) g.stat[q * g.subtiles + (u.p0 / kP + wp)] = f32x2{tops[j], sums[j]};
                 if (!g.e) continue;
                 if constexpr (BF16) {
-                    const _Float16 h[4] = {(_Float16)e[0], (_Float16)e[1], (_Float16)e[2], (_Float16)e[3]};
-                    put(i, j, reinterpret_cast<const uint16_t *>(h));
-                } else if (on && pw + 16 * i < g.lde) {
-                    *reinterpret_cast<f32x4 *>(static_cast<float *>(g.e) + q * g.lde + pw + 16 * i) = f32x4{e[0], e[1], e[2], e[3]};
+#pragma unroll
+                    for (int i = 0; i < kI; ++i) {
+                        const _Float16 h[4] = {(_Float16)acc[i][j][0], (_Float16)acc[i][j][1], (_Float16)acc[i][j][2], (_Float16)acc[i][j][3]};
+                        put(i, reinterpret_cast<const uint16_t *>(h));
+                    }
+                    send(j, static_cast<uint16_t *>(g.e), g.lde, g.lde);
+                } else if (q < nq) {
+#pragma unroll
+                    for (int i = 0; i < kI; ++i)
+                        if (pw + 16 * i < g.lde)
+                            *reinterpret_cast<f32x4 *>(static_cast<float *>(g.e) + q * g.lde + pw + 16 * i) = acc[i][j];
                 }
             }
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
-            if (on && lane < 16)
-                g.stat[q * g.subtiles + (p0 / (BP / WP) + wp)] = f32x2{top, BF16 ? sum * 0x1p-15f : sum};
-        }
-    } else {
-        const float scale = g.sums->scale;
+        } else if (u.slot >= 0) {
+            arrived();
+            float *d = g.parts + (int64_t)u.slot * (BP * BQ) + (wq * kQ + lane % 16) * BP + wp * kP + lane / 16 * 4;
 #pragma unroll
-        for (int j = 0; j < kJ; ++j) {
-            const int64_t q = qw + 16 * j;
-            if (EPI == kF32 && q >= nq) continue;
-            const int64_t row = q < nq ? (g.map ? (int64_t)g.map[g.first + q] : q) : -1, at = row * g.ldo + pw;
-            float *f = g.f32 + split * g.f32_split + at;
-            const float *fi = g.f32_in + at;
-            const uint16_t *old = static_cast<const uint16_t *>(g.out) + at;
+            for (int j = 0; j < kJ; ++j)
 #pragma unroll
-            for (int i = 0; i < kI; ++i) {
-                const int64_t left = row < 0 ? 0 : whole ? 4 : g.np - pw - 16 * i;
-                float v[4];
+                for (int i = 0; i < kI; ++i) *reinterpret_cast<f32x4 *>(d + 16 * j * BP + 16 * i) = acc[i][j];
+        } else {
+            arrived();
+            const float scale = g.sums->scale;
 #pragma unroll
-                for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r] * scale;
-                if (g.f32_in) {
-                    float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    if (left >= 4) __builtin_memcpy(x, fi + 16 * i, sizeof x);
-                    else
-                        for (int r = 0; r < 3; ++r)
-                            if (r < left) x[r] = fi[16 * i + r];
+            for (int j = 0; j < kJ; ++j) {
+                const int64_t q = qw + 16 * j;
+                const int64_t row = q < nq ? (g.map ? (int64_t)g.map[g.first + q] : q) : -1, at = row * g.ldo + pw;
+                float *f = g.f32 + at;
+                const float *fi = g.f32_in + at;
+                const uint16_t *old = static_cast<const uint16_t *>(g.out) + at;
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] += x[r];
-                }
-                if constexpr (EPI == kF32) {
-                    if (left >= 4) __builtin_memcpy(f + 16 * i, v, sizeof v);
-                    else
-                        for (int r = 0; r < 3; ++r)
-                            if (r < left) f[16 * i + r] = v[r];
-                } else {
-                    uint16_t h[4] = {0, 0, 0, 0};
-                    if (g.add_out) {
-                        if (left >= 4) __builtin_memcpy(h, old + 16 * i, sizeof h);
+                for (int i = 0; i < kI; ++i) {
+                    const int64_t here = row < 0 ? 0 : whole ? 4 : g.np - pw - 16 * i;
+                    float v[4];
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) v[r] = acc[i][j][r] * scale;
+                    if (g.f32_in) {
+                        float x[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        if (here >= 4) __builtin_memcpy(x, fi + 16 * i, sizeof x);
                         else
                             for (int r = 0; r < 3; ++r)
-                                if (r < left) h[r] = old[16 * i + r];
+                                if (r < here) x[r] = fi[16 * i + r];
 #pragma unroll
-                        for (int r = 0; r < 4; ++r) v[r] += widen(h[r]);
+                        for (int r = 0; r < 4; ++r) v[r] += x[r];
                     }
+                    if constexpr (EPI == kF32) {
+                        if (here >= 4) __builtin_memcpy(f + 16 * i, v, sizeof v);
+                        else
+                            for (int r = 0; r < 3; ++r)
+                                if (r < here) f[16 * i + r] = v[r];
+                    } else {
+                        uint16_t h[4] = {0, 0, 0, 0};
+                        if (g.add_out) {
+                            if (here >= 4) __builtin_memcpy(h, old + 16 * i, sizeof h);
+                            else
+                                for (int r = 0; r < 3; ++r)
+                                    if (r < here) h[r] = old[16 * i + r];
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) h[r] = narrow(v[r]);
-                    put(i, j, h);
+                            for (int r = 0; r < 4; ++r) v[r] += widen(h[r]);
+                        }
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) h[r] = narrow(v[r]);
+                        put(i, h);
+                    }
                 }
+                if constexpr (EPI == kBf16) send(j, static_cast<uint16_t *>(g.out), g.ldo, g.np);
             }
-        }
-    }
-    if constexpr (EPI == kBf16 || (EPI == kLogits && BF16)) {
-        if (EPI == kLogits && !g.e) return;
-        __syncthreads();
-        constexpr int kAcross = BP / 8, kDown = 64 * kWaves / kAcross;    // 16-byte chunks of a line; lines at a time
-        const int64_t p = p0 + threadIdx.x % kAcross * 8;
-        const int64_t np = EPI == kLogits ? g.lde : g.np, ld = EPI == kLogits ? g.lde : g.ldo;
-        uint16_t *out = static_cast<uint16_t *>(EPI == kLogits ? g.e : g.out);
-        if (p >= np) return;
-#pragma unroll 4
-        for (int r = threadIdx.x / kAcross; r < BQ; r += kDown) {
-            if (q0 + r >= nq) break;
-            const int64_t row = EPI == kBf16 && g.map ? (int64_t)g.map[g.first + q0 + r] : q0 + r;
-            uint16_t h[8], *d = out + row * ld + p;
-            __builtin_memcpy(h, __builtin_assume_aligned(lds + r * kPitch + threadIdx.x % kAcross * 16, 16), sizeof h);
-            if (p + 8 <= np) __builtin_memcpy(d, h, sizeof h);
-            else
-                for (int k = 0; k < 7; ++k)
-                    if (p + k < np) d[k] = h[k];
         }
     }
 }
 
-template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ>
+template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE>
 __global__ void __launch_bounds__(64 * WP * WQ, 2) product_kernel(Product g) {
-    product<BF16, EPI, TP, TQ, BP, BQ, WP, WQ>(g);
+    product<BF16, EPI, TP, TQ, BP, BQ, WP, WQ, AT_ONCE>(g);
+}
+
+// The parts of cut tiles, in order, and what a whole tile's epilogue does. Four
+// rows of a tile to a workgroup.
+template <int EPI>
+__global__ void __launch_bounds__(256) join_kernel(Product g, int bp, int bq, int es, int at_once) {
+    const Schedule s = schedule(g, bp, bq, es, at_once);
+    const int per = bq / 4, tile = blockIdx.x / per;
+    if (s.parts == 1 || tile >= s.cut) return;
+    const int64_t nq = g.piece_is_q ? piece_rows(g.sums, g.first, g.piece) : g.nq;
+    int tp, tq;
+    place(s, tile, s.cut, s.whole, &tp, &tq);
+    const int ql = (int)(blockIdx.x % per) * 4 + threadIdx.x / 64;
+    const int64_t q = (int64_t)tq * bq + ql;
+    if (q >= nq) return;
+    const float scale = g.sums->scale;
+    const int64_t row = g.map ? (int64_t)g.map[g.first + q] : q;
+    for (int pl = threadIdx.x % 64 * 4; pl < bp; pl += 256) {
+        const int64_t p = (int64_t)tp * bp + pl, left = g.np - p, at = row * g.ldo + p;
+        if (left <= 0) return;
+        f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+        for (int k = 0; k < s.parts; ++k)
+            v += *reinterpret_cast<const f32x4 *>(g.parts + ((int64_t)(tile * s.parts + k) * bq + ql) * bp + pl);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            if (r >= left) break;
+            float x = v[r] * scale;
+            if (g.f32_in) x += g.f32_in[at + r];
+            if (EPI == kF32) {
+                g.f32[at + r] = x;
+            } else {
+                uint16_t *d = static_cast<uint16_t *>(g.out) + at + r;
+                if (g.add_out) x += widen(*d);
+                *d = narrow(x);
+            }
+        }
+    }
 }
 
 // ------------------------------------------------------- the softmax
@@ -648,35 +810,20 @@ gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *target, int64_t
     __builtin_memcpy(__builtin_assume_aligned(at, 16), out, sizeof out);
 }
 
-// grad_hidden from the binary32 parts of the split product.
-template <bool BF16>
-__global__ void __launch_bounds__(256)
-join_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t first, int64_t piece,
-            const float *parts, int splits, int64_t stride) {
-    const int64_t q = blockIdx.x;
-    if (q >= piece_rows(sums, first, piece)) return;
-    const int64_t row = map[first + q];
-    for (int64_t c = threadIdx.x; c < a.width; c += 256) {
-        float v = 0.0f;
-        for (int s = 0; s < splits; ++s) v += parts[s * stride + q * a.width + c];
-        if (BF16) static_cast<uint16_t *>(a.grad_hidden)[row * a.width + c] = narrow(v);
-        else static_cast<float *>(a.grad_hidden)[row * a.width + c] = v;
-    }
-}
-
 // ------------------------------------------------------- launches
 template <bool BF16, int EPI, bool TP, bool TQ>
 void start_product(const Product &g, int shape, hipStream_t stream) {
-    const dim3 grid((unsigned)(g.tiles_p * g.tiles_q * g.splits));
-    if (shape == 0) product_kernel<BF16, EPI, TP, TQ, 256, 256, 2, 4><<<grid, 512, 0, stream>>>(g);
-    else if (shape == 1) product_kernel<BF16, EPI, TP, TQ, 128, 128, 2, 2><<<grid, 256, 0, stream>>>(g);
-    else product_kernel<BF16, EPI, TP, TQ, 128, 32, 4, 1><<<grid, 256, 0, stream>>>(g);
-}
-
-void set_tiles(Product &g, int shape, int splits) {
-    g.tiles_p = (int)ceil_div(g.np, kTiles[shape].p);
-    g.tiles_q = (int)ceil_div(g.nq, kTiles[shape].q);
-    g.splits = splits;
+    const TileShape t = kTiles[shape];
+    const int64_t tiles = ceil_div(g.np, t.p) * ceil_div(g.nq, t.q);
+    const unsigned grid = (unsigned)(g.slots > 0 || tiles > t.at_once ? t.at_once : tiles);
+    if (shape == 0) product_kernel<BF16, EPI, TP, TQ, 256, 256, 2, 4, kTiles[0].at_once><<<grid, 512, 0, stream>>>(g);
+    else if (shape == 1) product_kernel<BF16, EPI, TP, TQ, 128, 128, 2, 2, kTiles[1].at_once><<<grid, 256, 0, stream>>>(g);
+    else product_kernel<BF16, EPI, TP, TQ, 128, 32, 4, 1, kTiles[2].at_once><<<grid, 256, 0, stream>>>(g);
+    if constexpr (EPI != kLogits)
+        if (g.slots > 0) {
+            const int64_t cut = tiles < t.at_once ? tiles : t.at_once - 1;
+            join_kernel<EPI><<<(unsigned)(cut * (t.q / 4)), 256, 0, stream>>>(g, t.p, t.q, BF16 ? 2 : 4, t.at_once);
+        }
 }
 
 template <bool BF16>
@@ -719,7 +866,6 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
         g.subtiles = p.subtiles;
         g.e = grads ? w + p.e_off : nullptr;
         g.lde = p.vocab_p;
-        set_tiles(g, p.tile_logits, 1);
         start_product<BF16, kLogits, false, false>(g, p.tile_logits, stream);
         softmax_kernel<<<(unsigned)ceil_div(p.piece, 4), 256, 0, stream>>>(a, sums, map, first, p.piece, stat,
                                                                            p.subtiles, rows, losses);
@@ -741,20 +887,12 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
             h.piece_is_q = true;
             h.steps = ceil_div(a.vocab * es, 128);    // every stage has a row of the table
             h.ldo = a.width;
-            set_tiles(h, p.tile_hidden, p.splits);
-            if (p.splits > 1) {
-                h.f32 = reinterpret_cast<float *>(w + p.split_off);
-                h.f32_split = p.piece * a.width;
-                start_product<BF16, kF32, true, false>(h, p.tile_hidden, stream);
-            } else {
-                h.map = map;
-                h.out = a.grad_hidden;
-                h.f32 = static_cast<float *>(a.grad_hidden);
-                start_product<BF16, BF16 ? kBf16 : kF32, true, false>(h, p.tile_hidden, stream);
-            }
-            if (p.splits > 1)
-                join_kernel<BF16><<<(unsigned)p.piece, 256, 0, stream>>>(a, sums, map, first, p.piece, h.f32, p.splits,
-                                                                         h.f32_split);
+            h.slots = p.slots_hidden;
+            h.parts = reinterpret_cast<float *>(w + p.parts_off);
+            h.map = map;
+            h.out = a.grad_hidden;
+            h.f32 = static_cast<float *>(a.grad_hidden);
+            start_product<BF16, BF16 ? kBf16 : kF32, true, false>(h, p.tile_hidden, stream);
         }
         if (a.grad_table) {
             Product t = {};
@@ -763,7 +901,7 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
             t.piece = p.piece;
             t.p = w + p.hidden_off;
             t.ldp = p.width_p * es;
-            t.kp = p.piece_p;
+            t.kp = t.kq = p.piece_p;
             t.np = a.width;
             t.q = w + p.e_off;
             t.ldq = p.vocab_p * es;
@@ -772,7 +910,8 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
             t.ldo = a.width;
             const bool last = k + 1 == p.pieces;
             float *gw = a.table_grad_bf16 ? reinterpret_cast<float *>(w + p.gw_off) : static_cast<float *>(a.grad_table);
-            set_tiles(t, p.tile_table, 1);
+            t.slots = p.slots_table;
+            t.parts = reinterpret_cast<float *>(w + p.parts_off);
             t.f32_in = k > 0 || (!a.table_grad_bf16 && a.accumulate) ? gw : nullptr;
             if (a.table_grad_bf16 && last) {
                 t.out = a.grad_table;

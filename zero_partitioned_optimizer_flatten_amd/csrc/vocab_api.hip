@@ -137,7 +137,7 @@ namespace {
 
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-// The largest tile that still gives every compute unit one.
+// The largest tile that still gives most compute units one.
 int choose_tile(int64_t np, int64_t nq, int64_t splits) {
     if (nq <= 32) return 2;
     if (ceil_div(np, 256) * ceil_div(nq, 256) * splits >= 200) return 0;
@@ -163,13 +163,20 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     p.tile_logits = choose_tile(a.vocab, piece, 1);
     p.sub = kTiles[p.tile_logits].sub;
     p.subtiles = round_up(a.vocab, kTiles[p.tile_logits].p) / p.sub;
-    p.splits = 1;
     p.tile_hidden = choose_tile(a.width, piece, 4);
-    const TileShape s = kTiles[p.tile_hidden];
-    const int64_t tiles = ceil_div(a.width, s.p) * ceil_div(piece, s.q), steps = ceil_div(a.vocab, step);
-    // enough workgroups for every compute unit, of 16 steps at least
-    while (tiles * p.splits < 256 && steps / (p.splits + 1) >= 16) ++p.splits;
     p.tile_table = choose_tile(a.width, a.vocab, 1);
+    // parts of tiles that do not fill a round, as many as 8 of each
+    auto slots = [&](int shape, int64_t np, int64_t nq, int64_t steps) -> int {
+        const TileShape t = kTiles[shape];
+        const int64_t tiles = ceil_div(np, t.p) * ceil_div(nq, t.q);
+        if (steps < 32) return 0;
+        const int64_t n = 8 * (tiles < t.at_once ? tiles : t.at_once);
+        return (int)(n < 1024 ? n : 1024);
+    };
+    p.slots_hidden = a.grad_hidden ? slots(p.tile_hidden, a.width, piece, ceil_div(a.vocab, step)) : 0;
+    p.slots_table = a.grad_table ? slots(p.tile_table, a.width, a.vocab, ceil_div(piece, step)) : 0;
+    auto room = [](int slots, int shape) { return (int64_t)slots * kTiles[shape].p * kTiles[shape].q * 4; };
+    const int64_t parts_h = room(p.slots_hidden, p.tile_hidden), parts_t = room(p.slots_table, p.tile_table);
     int64_t at = 0;
     auto take = [&](int64_t bytes) {
         const int64_t here = at;
@@ -186,7 +193,7 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     p.table_off = p.pack_table ? take(a.vocab * p.width_p * es) : -1;
     p.e_off = grads ? take(p.piece_p * p.vocab_p * es) : -1;
     p.gw_off = a.grad_table && a.table_grad_bf16 && p.pieces > 1 ? take(4 * a.vocab * a.width) : -1;
-    p.split_off = a.grad_hidden && p.splits > 1 ? take(4 * p.splits * piece * a.width) : -1;
+    p.parts_off = take(parts_h > parts_t ? parts_h : parts_t);
     p.bytes = at;
     return p;
 }

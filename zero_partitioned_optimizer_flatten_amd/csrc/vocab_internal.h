@@ -104,12 +104,13 @@ struct HeadRow {
     float share;                  // weight / most
     float target;                 // z_y * log2(e)
 };
-// Tiles of the products: rows of P and of Q, waves, rows of P to a wave.
+// Tiles of the products: rows of P and of Q, rows of P to a wave, and workgroups
+// that run at a time: one, two or four on each of 256 compute units, as LDS lets
+// them.
 struct TileShape {
-    int p, q, waves, sub;
+    int p, q, sub, at_once;
 };
-constexpr TileShape kTiles[] = {{256, 256, 8, 128}, {128, 128, 4, 64}, {128, 32, 4, 32}};
-
+constexpr TileShape kTiles[] = {{256, 256, 128, 256}, {128, 128, 64, 512}, {128, 32, 32, 768}};
 struct HeadPlan {
     int64_t piece, pieces;        // rows of hidden in a piece
     int64_t width_p, vocab_p, piece_p;   // extents padded for the products' long axes
@@ -117,10 +118,10 @@ struct HeadPlan {
     int tile_logits, tile_hidden, tile_table;   // shapes of the three products' tiles
     int sub;                      // vocabulary entries that share a statistic
     int64_t subtiles;             // statistics of a row
-    int splits;                   // of the vocabulary axis in grad_hidden's product
+    int slots_hidden, slots_table;       // room for parts of the gradients' tiles
     // workspace offsets in bytes; -1: not there
     int64_t sum_off, map_off, loss_off, row_off, stat_off, hidden_off, table_off, e_off, gw_off,
-        split_off, bytes;
+        parts_off, bytes;
 };
 struct HeadArgs {
     const void *hidden, *table;
