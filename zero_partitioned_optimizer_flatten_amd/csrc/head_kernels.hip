@@ -530,10 +530,15 @@ __device__ __forceinline__ void product(const Product &g) {
                 if (q < nq && p < np) {
                     const int64_t row = EPI == kBf16 && g.map ? (int64_t)g.map[g.first + q] : q;
                     uint16_t *d = out + row * ld + p;
-                    if (p + 8 <= np) __builtin_memcpy(d, h, sizeof h);
-                    else
+                    if (EPI == kLogits) {             // whole chunks, aligned
+                        typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+                        __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), reinterpret_cast<u32x4 *>(d));
+                    } else if (p + 8 <= np) {
+                        __builtin_memcpy(d, h, sizeof h);
+                    } else {
                         for (int k = 0; k < 7; ++k)
                             if (p + k < np) d[k] = h[k];
+                    }
                 }
             }
             asm volatile("" ::: "memory");
