@@ -120,16 +120,17 @@ EmbedGradPlan plan_embed_grad(int64_t count, int64_t rows, int64_t width) {
     p.sort_groups_log2 = 8;                        // one workgroup to a compute unit
     while ((rows >> p.sort_groups_log2) >= kSortIds) ++p.sort_groups_log2;
     p.ids_per_group = (int)ceil_div(rows, (int64_t)1 << p.sort_groups_log2);
-    // About 512 spans, and at most 256 tokens in one: few partial rows for a
-    // run that is the whole batch, enough waves for short batches.
-    int64_t span = count / 512;
-    p.span = (int)(span < 8 ? 8 : span > 256 ? 256 : span);
+    // About 1024 spans, and at most 256 tokens in one: few partial rows for a
+    // run that is the whole batch, enough waves for short batches. Few tokens
+    // have a wave for each run, and no joining follows (span 1).
+    const int64_t span = count / 1024;
+    p.span = count <= kRunTokens ? 1 : (int)(span < 8 ? 8 : span > 256 ? 256 : span);
     p.spans = ceil_div(count, p.span);
     const int64_t pitch = ceil_div(width, kSpanCols) * kSpanCols;
     p.count_off = 0;
     p.sorted_off = 256;
     p.partial_off = p.sorted_off + ceil_div(count * (int64_t)sizeof(SortedToken), 256) * 256;
-    p.bytes = p.partial_off + (p.spans > 1 ? 2 * p.spans * pitch * (int64_t)sizeof(float) : 0);
+    p.bytes = p.partial_off + (p.spans > 1 && p.span > 1 ? 2 * p.spans * pitch * (int64_t)sizeof(float) : 0);
     return p;
 }
 

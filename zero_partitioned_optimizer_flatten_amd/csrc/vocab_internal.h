@@ -58,10 +58,12 @@ constexpr int kSortWaves = 16;
 struct EmbedGradPlan {
     int sort_groups_log2;         // workgroups of the sort
     int ids_per_group;
-    int span;                     // sorted tokens one wave adds up
+    int span;                     // sorted tokens one wave adds up; 1: a run
     int64_t spans;
     int64_t sorted_off, count_off, partial_off, bytes;   // workspace layout
 };
+// Up to so many tokens the sums go by runs.
+constexpr int kRunTokens = 128;
 // Columns of one wave in the sums.
 constexpr int kSpanCols = 512;
 EmbedGradPlan plan_embed_grad(int64_t count, int64_t rows, int64_t width);

@@ -45,6 +45,30 @@ __device__ __forceinline__ void load8(const void *base, int64_t at, int64_t left
     }
 }
 
+// The same, to be widened later.
+template <bool BF16> struct Raw8 {
+    uint32_t w[BF16 ? 4 : 8];
+    __device__ __forceinline__ void load(const void *base, int64_t at, int64_t left) {
+        if (left >= kVec) {
+            __builtin_memcpy(w, static_cast<const char *>(base) + at * (BF16 ? 2 : 4), sizeof w);
+        } else if (BF16) {
+            const uint16_t *p = static_cast<const uint16_t *>(base) + at;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                w[k] = (2 * k < left ? p[2 * k] : 0u) | (2 * k + 1 < left ? (uint32_t)p[2 * k + 1] << 16 : 0u);
+        } else {
+            const uint32_t *p = static_cast<const uint32_t *>(base) + at;
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) w[k % (BF16 ? 4 : 8)] = k < left ? p[k] : 0u;
+        }
+    }
+    __device__ __forceinline__ void get(float *v) const {
+#pragma unroll
+        for (int k = 0; k < kVec; ++k)
+            v[k] = __uint_as_float(!BF16 ? w[k % (BF16 ? 4 : 8)] : k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+    }
+};
+
 template <bool BF16>
 __device__ __forceinline__ void store8(void *base, int64_t at, int64_t left, const float *v) {
     if (BF16) {
@@ -207,6 +231,9 @@ __device__ __forceinline__ void zero_row(char *p, int64_t bytes, int lane) {
         *reinterpret_cast<uint16_t *>(p + k) = 0;
 }
 
+// Ids a lane has under way.
+constexpr int kSortBatch = 8;
+
 __global__ void __launch_bounds__(64 * kSortWaves)
 sort_kernel(EmbedGradArgs a, int log2_groups, int per_group, SortedToken *sorted, int32_t *total) {
     extern __shared__ int32_t counts[];            // [kSortWaves][per_group], then places
@@ -221,13 +248,27 @@ sort_kernel(EmbedGradArgs a, int log2_groups, int per_group, SortedToken *sorted
     const int64_t last = first + stretch < a.count ? first + stretch : a.count;
     int32_t *mine = counts + wave * per_group;
     int32_t lower = 0, all = 0;
-    for (int64_t i = first + lane; i < last; i += 64) {
-        const int64_t id = load_id(a.ids, a.wide_ids, i);
-        if ((uint64_t)id < (uint64_t)a.rows) {
-            const uint32_t g = (uint32_t)id & mask;
+    int64_t ids[kSortBatch];
+    // kSortBatch * 64 ids from i0, -1 for those outside the table or the stretch
+    auto load = [&](int64_t i0) {
+#pragma unroll
+        for (int k = 0; k < kSortBatch; ++k) {
+            const int64_t i = i0 + 64 * k + lane;
+            ids[k] = i < last ? load_id(a.ids, a.wide_ids, i) : -1;
+        }
+#pragma unroll
+        for (int k = 0; k < kSortBatch; ++k)
+            if ((uint64_t)ids[k] >= (uint64_t)a.rows) ids[k] = -1;
+    };
+    for (int64_t i0 = first; i0 < last; i0 += 64 * kSortBatch) {
+        load(i0);
+#pragma unroll
+        for (int k = 0; k < kSortBatch; ++k) {
+            if (ids[k] < 0) continue;
+            const uint32_t g = (uint32_t)ids[k] & mask;
             lower += g < group;
             ++all;
-            if (g == group) atomicAdd(&mine[(uint32_t)id >> log2_groups], 1);
+            if (g == group) atomicAdd(&mine[(uint32_t)ids[k] >> log2_groups], 1);
         }
     }
     for (int s = 32; s; s /= 2) {
@@ -267,20 +308,23 @@ sort_kernel(EmbedGradArgs a, int log2_groups, int per_group, SortedToken *sorted
         }
     }
     __syncthreads();
-    for (int64_t i0 = first; i0 < last; i0 += 64) {
-        const int64_t i = i0 + lane;
-        const int64_t id = i < last ? load_id(a.ids, a.wide_ids, i) : -1;
-        const bool here = (uint64_t)id < (uint64_t)a.rows && ((uint32_t)id & mask) == group;
-        const int32_t k = here ? (int32_t)((uint32_t)id >> log2_groups) : -1;
-        uint64_t todo = __ballot(here);
-        while (todo) {                             // the ids among these 64, one by one
-            const int leader = __builtin_ctzll(todo);
-            const uint64_t same = __ballot(k == __shfl(k, leader));
-            int32_t at = 0;
-            if (lane == leader) at = atomicAdd(&mine[k], (int32_t)__popcll(same));
-            at = __shfl(at, leader) + __popcll(same & ((1ull << lane) - 1));
-            if ((same >> lane) & 1) sorted[at] = {(int32_t)id, (int32_t)i, begin[k], end[k]};
-            todo &= ~same;
+    for (int64_t i0 = first; i0 < last; i0 += 64 * kSortBatch) {
+        if (stretch > 64 * kSortBatch) load(i0);    // else they are still there
+#pragma unroll
+        for (int b = 0; b < kSortBatch; ++b) {
+            const bool here = ids[b] >= 0 && ((uint32_t)ids[b] & mask) == group;
+            const int32_t k = here ? (int32_t)((uint32_t)ids[b] >> log2_groups) : -1;
+            uint64_t todo = __ballot(here);
+            while (todo) {                           // the ids among these 64, one by one
+                const int leader = __builtin_ctzll(todo);
+                const uint64_t same = __ballot(k == __shfl(k, leader));
+                int32_t at = 0;
+                if (lane == leader) at = atomicAdd(&mine[k], (int32_t)__popcll(same));
+                at = __shfl(at, leader) + __popcll(same & ((1ull << lane) - 1));
+                if ((same >> lane) & 1)
+                    sorted[at] = {(int32_t)ids[b], (int32_t)(i0 + 64 * b + lane), begin[k], end[k]};
+                todo &= ~same;
+            }
         }
     }
     if (a.accumulate) return;
@@ -300,57 +344,90 @@ sort_kernel(EmbedGradArgs a, int log2_groups, int per_group, SortedToken *sorted
 // kernel adds a run's partial rows in the order of the spans. So the work is
 // even whatever the tokens are, one padding token a million times included.
 
+// Rows a lane has under way.
+constexpr int kSpanBatch = 8;
+
+// A whole row of the gradient from its sum; `old` what it holds, to be added to.
 template <bool OBF>
 __device__ __forceinline__ void write_row(const EmbedGradArgs &a, int32_t id, int64_t col,
-                                          const float *sum) {
-    const int64_t left = a.width - col, at = (int64_t)id * a.width + col;
+                                          const float *sum, const Raw8<OBF> &old) {
+    const int64_t left = a.width - col;
     if (left <= 0) return;
-    float v[kVec];
+    float v[kVec], o[kVec];
+    old.get(o);
 #pragma unroll
-    for (int k = 0; k < kVec; ++k) v[k] = sum[k] * a.scale;
-    if (a.accumulate) {
-        float old[kVec];
-        load8<OBF>(a.out, at, left, old);
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) v[k] += old[k];
-    }
-    store8<OBF>(a.out, at, left, v);
+    for (int k = 0; k < kVec; ++k) v[k] = a.accumulate ? sum[k] * a.scale + o[k] : sum[k] * a.scale;
+    store8<OBF>(a.out, (int64_t)id * a.width + col, left, v);
 }
 
-template <bool GBF, bool OBF, bool DROP, bool ALIGNED>
+// RUNS, for few tokens: a span is a run, whatever its length, and the waves of
+// the other tokens have nothing to do.
+template <bool GBF, bool OBF, bool DROP, bool ALIGNED, bool RUNS>
 __global__ void __launch_bounds__(kThreads)
 span_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, int span,
-            int64_t spans, int col_chunks, float *partial, int64_t pitch) {
-    const int64_t unit = (int64_t)blockIdx.x * (kThreads / 64) + threadIdx.x / 64;
+            int col_chunks, float *partial, int64_t pitch) {
+    const int unit = __builtin_amdgcn_readfirstlane(blockIdx.x * (kThreads / 64) + threadIdx.x / 64);
     const int lane = threadIdx.x % 64;
-    const int64_t s = unit / col_chunks;
-    const int64_t col = (unit - s * col_chunks) * kSpanCols + lane * kVec;
-    const int32_t n = *total;
-    const int64_t lo = s * span, hi = lo + span < n ? lo + span : n;
-    if (s >= spans || lo >= n) return;
+    const int s = __builtin_amdgcn_readfirstlane((uint32_t)unit / (uint32_t)col_chunks);
+    const int64_t col = (int64_t)(unit - s * col_chunks) * kSpanCols + lane * kVec;
+    const int n = __builtin_amdgcn_readfirstlane(*total);
+    int64_t lo = (int64_t)s * span;
+    if (lo >= n) return;
+    int64_t hi = lo + span < n ? lo + span : n;
+    if (RUNS) {
+        if (__builtin_amdgcn_readfirstlane(sorted[lo].begin) != lo) return;
+        hi = __builtin_amdgcn_readfirstlane(sorted[lo].end);
+    }
     const int64_t left = a.width - col;
     const uint64_t offset = DROP ? drop_offset(a.drop) : 0;
     float sum[kVec];
 #pragma unroll
     for (int k = 0; k < kVec; ++k) sum[k] = 0.0f;
-    for (int64_t i = lo; i < hi; ++i) {
-        const SortedToken t = sorted[i];
-        if (left > 0) {
-            float v[kVec];
-            load8<GBF>(a.grad_out, (int64_t)t.row * a.width + col, left, v);
-            if (DROP) drop8<ALIGNED>(a.drop, offset, (uint64_t)t.row * a.width + col, v);
+    for (int64_t i0 = lo; i0 < hi; i0 += 64) {
+        const int m = (int)(hi - i0 < 64 ? hi - i0 : 64);
+        SortedToken t = {0, 0, 0, 0};
+        if (lane < m) t = sorted[i0 + lane];
+        // whether a token ends a run that is all in the span
+        const bool ends = lane < m && t.end == i0 + lane + 1 && t.begin >= lo;
+        const uint64_t whole = __ballot(ends);
+        for (int k0 = 0; k0 < m; k0 += kSpanBatch) {
+            Raw8<GBF> raw[kSpanBatch];
+            Raw8<OBF> old[kSpanBatch];
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) sum[k] += v[k];
-        }
-        if (i + 1 == t.end || i + 1 == hi) {
-            if (t.begin >= lo && t.end <= hi) {
-                write_row<OBF>(a, t.id, col, sum);
-            } else if (left > 0) {
-                float *p = partial + (2 * s + (t.begin >= lo)) * pitch + col;
-                __builtin_memcpy(__builtin_assume_aligned(p, 16), sum, sizeof sum);
+            for (int k = 0; k < kSpanBatch; ++k) {
+                const int row = __builtin_amdgcn_readlane(t.row, (k0 + k) % 64);   // 0 behind the last
+                if (left > 0) raw[k].load(a.grad_out, (int64_t)row * a.width + col, left);
             }
+            if (a.accumulate)
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) sum[k] = 0.0f;
+                for (int k = 0; k < kSpanBatch; ++k) {
+                    const int id = __builtin_amdgcn_readlane(t.id, (k0 + k) % 64);
+                    if (left > 0 && whole >> (k0 + k) % 64 & 1) old[k].load(a.out, (int64_t)id * a.width + col, left);
+                }
+#pragma unroll
+            for (int k = 0; k < kSpanBatch; ++k) {
+                if (k0 + k >= m) break;
+                const int row = __builtin_amdgcn_readlane(t.row, k0 + k), end = __builtin_amdgcn_readlane(t.end, k0 + k);
+                if (left > 0) {
+                    float v[kVec];
+                    raw[k].get(v);
+                    if (DROP) drop8<ALIGNED>(a.drop, offset, (uint64_t)row * a.width + col, v);
+#pragma unroll
+                    for (int c = 0; c < kVec; ++c) sum[c] += v[c];
+                }
+                const int64_t i = i0 + k0 + k;
+                if (i + 1 == end || i + 1 == hi) {
+                    const int begin = __builtin_amdgcn_readlane(t.begin, k0 + k);
+                    if (begin >= lo && end <= hi) {
+                        write_row<OBF>(a, __builtin_amdgcn_readlane(t.id, k0 + k), col, sum, old[k]);
+                    } else if (left > 0) {
+                        float *p = partial + (2 * (int64_t)s + (begin >= lo)) * pitch + col;
+                        __builtin_memcpy(__builtin_assume_aligned(p, 16), sum, sizeof sum);
+                    }
+#pragma unroll
+                    for (int c = 0; c < kVec; ++c) sum[c] = 0.0f;
+                }
+            }
         }
     }
 }
@@ -394,7 +471,9 @@ join_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, in
     for (int w = 1; w < kJoinWaves; ++w)
 #pragma unroll
         for (int k = 0; k < kVec; ++k) sum[k] += sums[w][lane * kVec + k];
-    write_row<OBF>(a, t.id, col, sum);
+    Raw8<OBF> old;
+    if (a.accumulate && col < a.width) old.load(a.out, (int64_t)t.id * a.width + col, a.width - col);
+    write_row<OBF>(a, t.id, col, sum, old);
 }
 
 static_assert(kSpanCols == 64 * kVec, "a vector to a lane");
@@ -420,15 +499,19 @@ void start_spans(const EmbedGradArgs &a, const EmbedGradPlan &p, const SortedTok
     const int chunks = (int)ceil_div(a.width, kSpanCols);
     const int64_t pitch = (int64_t)chunks * kSpanCols;
     const dim3 grid((unsigned)ceil_div(p.spans * chunks, kThreads / 64));
-    if (a.drop.limit == 0)
-        span_kernel<GBF, OBF, false, true><<<grid, kThreads, 0, stream>>>(
-            a, sorted, total, p.span, p.spans, chunks, partial, pitch);
-    else if (a.width % kVec == 0)
-        span_kernel<GBF, OBF, true, true><<<grid, kThreads, 0, stream>>>(
-            a, sorted, total, p.span, p.spans, chunks, partial, pitch);
-    else
-        span_kernel<GBF, OBF, true, false><<<grid, kThreads, 0, stream>>>(
-            a, sorted, total, p.span, p.spans, chunks, partial, pitch);
+    const bool aligned = a.width % kVec == 0;
+#define ZERO_SPANS(DROP, ALIGNED, RUNS)                                      \
+    span_kernel<GBF, OBF, DROP, ALIGNED, RUNS><<<grid, kThreads, 0, stream>>>( \
+        a, sorted, total, p.span, chunks, partial, pitch)
+    if (p.span == 1) {
+        if (a.drop.limit == 0) ZERO_SPANS(false, true, true);
+        else ZERO_SPANS(true, false, true);
+        return;
+    }
+    if (a.drop.limit == 0) ZERO_SPANS(false, true, false);
+    else if (aligned) ZERO_SPANS(true, true, false);
+    else ZERO_SPANS(true, false, false);
+#undef ZERO_SPANS
     if (p.spans > 1)
         join_kernel<OBF><<<dim3((unsigned)((p.spans - 1) * chunks)), 64 * kJoinWaves, 0, stream>>>(
             a, sorted, total, p.span, chunks, partial, pitch);
