@@ -528,7 +528,7 @@ typedef struct {
  * be NULL together. Both tables have `dtype`. EINVAL: null or misaligned
  * pointers, ranges past their allocations, unknown dtypes or id sizes, a scale
  * not finite, p outside [0, 1], an output that overlaps an input.
- * EUNSUPPORTED: more than 3.4e10 output elements, 2^31 ids, 2^30 rows. */
+ * EUNSUPPORTED: more than 1.7e10 output elements, 2^31 ids, 2^30 rows. */
 int zero_embed(const void *ids, int32_t id_bytes, int64_t count,
                const void *table, int64_t rows, int64_t width,
                zero_dtype dtype, double scale, const void *position_ids,

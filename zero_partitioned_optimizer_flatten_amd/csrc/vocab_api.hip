@@ -53,7 +53,7 @@ int check_table(int64_t rows, int64_t width, const char *what) {
 
 int check_count(int64_t count, int64_t width) {
     if (count < 0) return fail(ZERO_EINVAL, "count must be >= 0 (got %lld)", (long long)count);
-    if (count > kMaxInt || count * ceil_div(width, 8) > kMaxUnits)
+    if (count > kMaxInt || count * ceil_div(width, 4) > kMaxUnits)
         return fail(ZERO_EUNSUPPORTED, "%lld rows of %lld elements are more than one call takes", (long long)count,
                     (long long)width);
     return ZERO_OK;
@@ -301,7 +301,7 @@ int zero_dropout(const void *x, const void *add, void *out, int64_t count, zero_
     zk::DropoutArgs a = {};
     if (!valid_dtype(dtype)) return fail(ZERO_EINVAL, "unknown dtype %d", (int)dtype);
     if (count < 0) return fail(ZERO_EINVAL, "count must be >= 0 (got %lld)", (long long)count);
-    if (ceil_div(count, 8) > kMaxUnits)
+    if (ceil_div(count, 4) > kMaxUnits)
         return fail(ZERO_EUNSUPPORTED, "%lld elements are more than one call takes", (long long)count);
     if (!drop) return fail(ZERO_EINVAL, "drop is null");
     int rc = check_drop(drop, &a.drop);

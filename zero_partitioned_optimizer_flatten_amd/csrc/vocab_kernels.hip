@@ -2,6 +2,8 @@
 //
 // Arithmetic is binary32; every output is rounded once (nearest, ties to
 // even). No floating-point atomics: the same call gives the same bits.
+#include <type_traits>
+
 #include "vocab_internal.h"
 
 namespace zk {
@@ -12,86 +14,65 @@ constexpr int kVec = 8;           // elements of one vector, one Philox block
 
 // ------------------------------------------------------------ elements
 
-__device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
-
 __device__ __forceinline__ uint16_t narrow(float f) {
     const uint32_t u = __float_as_uint(f);
     if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
     return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
 }
 
-// Eight elements at any alignment of their type; `left` of them exist.
-template <bool BF16>
-__device__ __forceinline__ void load8(const void *base, int64_t at, int64_t left, float *v) {
-    if (BF16) {
-        const uint16_t *p = static_cast<const uint16_t *>(base) + at;
-        if (left >= kVec) {
-            uint16_t h[kVec];
-            __builtin_memcpy(h, p, sizeof h);
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = widen(h[k]);
-        } else {
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = k < left ? widen(p[k]) : 0.0f;
-        }
-    } else {
-        const float *p = static_cast<const float *>(base) + at;
-        if (left >= kVec) {
-            __builtin_memcpy(v, p, kVec * sizeof(float));
-        } else {
-#pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] = k < left ? p[k] : 0.0f;
-        }
-    }
-}
-
-// The same, to be widened later.
-template <bool BF16> struct Raw8 {
-    uint32_t w[BF16 ? 4 : 8];
+// V elements at any alignment of their type, of which `left` exist.
+template <bool BF16, int V = kVec> struct Raw {
+    static constexpr int kWords = V * (BF16 ? 2 : 4) / 4;
+    uint32_t w[kWords];
     __device__ __forceinline__ void load(const void *base, int64_t at, int64_t left) {
-        if (left >= kVec) {
+        if (left >= V) {
             __builtin_memcpy(w, static_cast<const char *>(base) + at * (BF16 ? 2 : 4), sizeof w);
-        } else if (BF16) {
+        } else if constexpr (BF16) {
             const uint16_t *p = static_cast<const uint16_t *>(base) + at;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kWords; ++k)
                 w[k] = (2 * k < left ? p[2 * k] : 0u) | (2 * k + 1 < left ? (uint32_t)p[2 * k + 1] << 16 : 0u);
         } else {
             const uint32_t *p = static_cast<const uint32_t *>(base) + at;
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) w[k % (BF16 ? 4 : 8)] = k < left ? p[k] : 0u;
+            for (int k = 0; k < kWords; ++k) w[k] = k < left ? p[k] : 0u;
         }
+    }
+    __device__ __forceinline__ void clear() {
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) w[k] = 0u;
     }
     __device__ __forceinline__ void get(float *v) const {
 #pragma unroll
-        for (int k = 0; k < kVec; ++k)
-            v[k] = __uint_as_float(!BF16 ? w[k % (BF16 ? 4 : 8)] : k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+        for (int k = 0; k < V; ++k) {
+            if constexpr (BF16) v[k] = __uint_as_float(k % 2 ? w[k / 2] & 0xFFFF0000u : w[k / 2] << 16);
+            else v[k] = __uint_as_float(w[k]);
+        }
     }
 };
 
-template <bool BF16>
-__device__ __forceinline__ void store8(void *base, int64_t at, int64_t left, const float *v) {
-    if (BF16) {
-        uint16_t *p = static_cast<uint16_t *>(base) + at;
-        uint16_t h[kVec];
+// NT: past the caches.
+template <bool BF16, int V = kVec, bool NT = false>
+__device__ __forceinline__ void store(void *base, int64_t at, int64_t left, const float *v) {
+    using T = std::conditional_t<BF16, uint16_t, float>;
+    T *p = static_cast<T *>(base) + at, h[V];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) h[k] = narrow(v[k]);
-        if (left >= kVec) {
-            __builtin_memcpy(p, h, sizeof h);
+    for (int k = 0; k < V; ++k) {
+        if constexpr (BF16) h[k] = narrow(v[k]);
+        else h[k] = v[k];
+    }
+    if (left >= V) {
+        if constexpr (NT) {
+            static_assert(sizeof h == 16, "one vector");
+            typedef __attribute__((ext_vector_type(4), aligned(2))) uint32_t u32x4;
+            __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), reinterpret_cast<u32x4 *>(p));
         } else {
-#pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                if (k < left) p[k] = h[k];
+            __builtin_memcpy(p, h, sizeof h);
         }
     } else {
-        float *p = static_cast<float *>(base) + at;
-        if (left >= kVec) {
-            __builtin_memcpy(p, v, kVec * sizeof(float));
-        } else {
 #pragma unroll
-            for (int k = 0; k < kVec; ++k)
-                if (k < left) p[k] = v[k];
-        }
+        for (int k = 0; k < V; ++k)
+            if (k < left) p[k] = h[k];
     }
 }
 
@@ -127,20 +108,25 @@ __device__ __forceinline__ uint64_t drop_offset(const Drop &d) {
     return d.offset + (d.limit && d.counter ? *d.counter : 0);
 }
 
-// v[k] = keep(first + k) ? v[k] * scale : 0 for eight elements from any place.
-// A dropped element is a selected zero, so NaN and infinity there vanish.
-template <bool ALIGNED>
-__device__ __forceinline__ void drop8(const Drop &d, uint64_t offset, uint64_t first, float *v) {
+// v[k] = keep(first + k) ? v[k] * scale : 0 for V elements, four or eight, from
+// any place; ALIGNED: from a multiple of V. A dropped element is a selected zero,
+// so NaN and infinity there vanish.
+template <bool ALIGNED, int V = kVec>
+__device__ __forceinline__ void drop(const Drop &d, uint64_t offset, uint64_t first, float *v) {
     const Bits8 x = philox(first / kVec, offset, d.key0, d.key1);
-    if (ALIGNED || first % kVec == 0) {
+    const int s = (int)(first % kVec);
+    if (ALIGNED || s % V == 0) {
+        const uint32_t *w = x.w;
+        uint32_t part[V / 2];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) {
-            const uint32_t u = (x.w[k / 2] >> (16 * (k % 2))) & 0xFFFFu;
+        for (int k = 0; k < V / 2; ++k) part[k] = V == kVec || s == 0 ? w[k] : w[(k + kVec / 2 - V / 2) % 4];
+#pragma unroll
+        for (int k = 0; k < V; ++k) {
+            const uint32_t u = (part[k / 2] >> (16 * (k % 2))) & 0xFFFFu;
             v[k] = u >= d.limit ? v[k] * d.scale : 0.0f;
         }
     } else {
         const Bits8 y = philox(first / kVec + 1, offset, d.key0, d.key1);
-        const int s = (int)(first % kVec);
         uint32_t keep = 0;
 #pragma unroll
         for (int k = 0; k < kVec; ++k) {
@@ -149,26 +135,39 @@ __device__ __forceinline__ void drop8(const Drop &d, uint64_t offset, uint64_t f
         }
         keep >>= s;
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) v[k] = (keep >> k) & 1u ? v[k] * d.scale : 0.0f;
+        for (int k = 0; k < V; ++k) v[k] = (keep >> k) & 1u ? v[k] * d.scale : 0.0f;
     }
 }
 
-template <bool BF16, bool ADD>
+// 16 bytes of output to a lane at a time, whole lines to a wave; PER of them to a
+// thread, all asked for before the first is used.
+template <bool BF16, bool ADD, int PER, bool NT>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutArgs a) {
-    const int64_t block = (int64_t)blockIdx.x * kThreads + threadIdx.x;
-    const int64_t at = block * kVec, left = a.count - at;
-    if (left <= 0) return;
-    const uint64_t offset = drop_offset(a.drop);
-    float v[kVec];
-    load8<BF16>(a.x, at, left, v);
-    drop8<true>(a.drop, offset, (uint64_t)at, v);
-    if (ADD) {
-        float r[kVec];
-        load8<BF16>(a.add, at, left, r);
+    constexpr int V = BF16 ? 8 : 4;
+    const int64_t first = ((int64_t)blockIdx.x * (kThreads * PER) + threadIdx.x) * V;
+    Raw<BF16, V> x[PER], r[PER];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) v[k] += r[k];
+    for (int k = 0; k < PER; ++k) {
+        const int64_t at = first + (int64_t)k * kThreads * V, left = a.count - at;
+        if (left <= 0) break;
+        x[k].load(a.x, at, left);
+        if (ADD) r[k].load(a.add, at, left);
     }
-    store8<BF16>(a.out, at, left, v);
+    const uint64_t offset = drop_offset(a.drop);
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        const int64_t at = first + (int64_t)k * kThreads * V, left = a.count - at;
+        if (left <= 0) break;
+        float v[V], w[V];
+        x[k].get(v);
+        drop<true, V>(a.drop, offset, (uint64_t)at, v);
+        if (ADD) {
+            r[k].get(w);
+#pragma unroll
+            for (int c = 0; c < V; ++c) v[c] += w[c];
+        }
+        store<BF16, V, NT>(a.out, at, left, v);
+    }
 }
 
 // -------------------------------------------------------------- lookup
@@ -177,35 +176,51 @@ __device__ __forceinline__ int64_t load_id(const void *ids, bool wide, int64_t i
     return wide ? static_cast<const int64_t *>(ids)[i] : (int64_t) static_cast<const int32_t *>(ids)[i];
 }
 
-// A vector of eight columns of one output row to a thread.
-template <bool TBF, bool OBF, bool POS, bool DROP, bool ALIGNED>
+// 16 bytes of an output row to a lane, PER to a thread: the ids of all, then the
+// rows of all, are asked for before the first is used.
+template <bool TBF, bool OBF, bool POS, bool DROP, bool ALIGNED, int PER, bool NT>
 __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a, uint32_t per_row) {
-    const uint32_t unit = blockIdx.x * kThreads + threadIdx.x;   // a dispatch has fewer than 2^32
-    const int64_t row = unit / per_row;
-    if (row >= a.count) return;
-    const int64_t col = (int64_t)(unit % per_row) * kVec, left = a.width - col;
-    const uint64_t offset = DROP ? drop_offset(a.drop) : 0;
-    const int64_t id = load_id(a.ids, a.wide_ids, row);
-    float v[kVec];
-    if ((uint64_t)id < (uint64_t)a.rows) {
-        load8<TBF>(a.table, id * a.width + col, left, v);
+    constexpr int V = OBF ? 8 : 4;
+    int64_t id[PER], pos[PER];
+    uint32_t row[PER], chunk[PER];
 #pragma unroll
-        for (int k = 0; k < kVec; ++k) v[k] *= a.scale;
-    } else {
-#pragma unroll
-        for (int k = 0; k < kVec; ++k) v[k] = 0.0f;
+    for (int k = 0; k < PER; ++k) {
+        const uint32_t unit = blockIdx.x * (kThreads * PER) + k * kThreads + threadIdx.x;   // below 2^32
+        row[k] = unit / per_row;
+        chunk[k] = unit - row[k] * per_row;
+        if (row[k] >= a.count) break;
+        id[k] = load_id(a.ids, a.wide_ids, row[k]);
+        if (POS) pos[k] = load_id(a.pos_ids, a.wide_ids, row[k]);
     }
-    if (POS) {
-        const int64_t pos = load_id(a.pos_ids, a.wide_ids, row);
-        if ((uint64_t)pos < (uint64_t)a.pos_rows) {
-            float r[kVec];
-            load8<TBF>(a.pos_table, pos * a.width + col, left, r);
+    Raw<TBF, V> x[PER], r[PER];
 #pragma unroll
-            for (int k = 0; k < kVec; ++k) v[k] += r[k];
+    for (int k = 0; k < PER; ++k) {
+        if (row[k] >= a.count) break;
+        const int64_t col = (int64_t)chunk[k] * V, left = a.width - col;
+        if ((uint64_t)id[k] < (uint64_t)a.rows) x[k].load(a.table, id[k] * a.width + col, left);
+        else x[k].clear();
+        if (POS) {
+            if ((uint64_t)pos[k] < (uint64_t)a.pos_rows) r[k].load(a.pos_table, pos[k] * a.width + col, left);
+            else r[k].clear();
         }
     }
-    if (DROP) drop8<ALIGNED>(a.drop, offset, (uint64_t)(row * a.width + col), v);
-    store8<OBF>(a.out, row * a.width + col, left, v);
+    const uint64_t offset = DROP ? drop_offset(a.drop) : 0;
+#pragma unroll
+    for (int k = 0; k < PER; ++k) {
+        if (row[k] >= a.count) break;
+        const int64_t col = (int64_t)chunk[k] * V, at = (int64_t)row[k] * a.width + col;
+        float v[V], w[V];
+        x[k].get(v);
+#pragma unroll
+        for (int c = 0; c < V; ++c) v[c] *= a.scale;
+        if (POS) {
+            r[k].get(w);
+#pragma unroll
+            for (int c = 0; c < V; ++c) v[c] += w[c];
+        }
+        if (DROP) drop<ALIGNED, V>(a.drop, offset, (uint64_t)at, v);
+        store<OBF, V, NT>(a.out, at, a.width - col, v);
+    }
 }
 
 // ------------------------------------------- gradient: tokens, sorted
@@ -350,14 +365,14 @@ constexpr int kSpanBatch = 8;
 // A whole row of the gradient from its sum; `old` what it holds, to be added to.
 template <bool OBF>
 __device__ __forceinline__ void write_row(const EmbedGradArgs &a, int32_t id, int64_t col,
-                                          const float *sum, const Raw8<OBF> &old) {
+                                          const float *sum, const Raw<OBF> &old) {
     const int64_t left = a.width - col;
     if (left <= 0) return;
     float v[kVec], o[kVec];
     old.get(o);
 #pragma unroll
     for (int k = 0; k < kVec; ++k) v[k] = a.accumulate ? sum[k] * a.scale + o[k] : sum[k] * a.scale;
-    store8<OBF>(a.out, (int64_t)id * a.width + col, left, v);
+    store<OBF>(a.out, (int64_t)id * a.width + col, left, v);
 }
 
 // RUNS, for few tokens: a span is a run, whatever its length, and the waves of
@@ -391,8 +406,8 @@ span_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, in
         const bool ends = lane < m && t.end == i0 + lane + 1 && t.begin >= lo;
         const uint64_t whole = __ballot(ends);
         for (int k0 = 0; k0 < m; k0 += kSpanBatch) {
-            Raw8<GBF> raw[kSpanBatch];
-            Raw8<OBF> old[kSpanBatch];
+            Raw<GBF> raw[kSpanBatch];
+            Raw<OBF> old[kSpanBatch];
 #pragma unroll
             for (int k = 0; k < kSpanBatch; ++k) {
                 const int row = __builtin_amdgcn_readlane(t.row, (k0 + k) % 64);   // 0 behind the last
@@ -411,7 +426,7 @@ span_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, in
                 if (left > 0) {
                     float v[kVec];
                     raw[k].get(v);
-                    if (DROP) drop8<ALIGNED>(a.drop, offset, (uint64_t)row * a.width + col, v);
+                    if (DROP) drop<ALIGNED>(a.drop, offset, (uint64_t)row * a.width + col, v);
 #pragma unroll
                     for (int c = 0; c < kVec; ++c) sum[c] += v[c];
                 }
@@ -471,7 +486,7 @@ join_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, in
     for (int w = 1; w < kJoinWaves; ++w)
 #pragma unroll
         for (int k = 0; k < kVec; ++k) sum[k] += sums[w][lane * kVec + k];
-    Raw8<OBF> old;
+    Raw<OBF> old;
     if (a.accumulate && col < a.width) old.load(a.out, (int64_t)t.id * a.width + col, a.width - col);
     write_row<OBF>(a, t.id, col, sum, old);
 }
@@ -480,17 +495,37 @@ static_assert(kSpanCols == 64 * kVec, "a vector to a lane");
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// Vectors to a thread: one while that leaves the device short of work; else four,
+// to have enough bytes on their way, and stores past the caches, which then keep
+// what is read.
+constexpr int64_t kFewVectors = (int64_t)256 * 2048;      // a thread each on every compute unit
+
+template <bool TBF, bool OBF, bool POS, bool DROP, bool ALIGNED>
+void start_embed(const EmbedArgs &a, hipStream_t stream) {
+    const uint32_t per_row = (uint32_t)ceil_div(a.width, OBF ? 8 : 4);
+    const int64_t units = a.count * per_row;
+    if (units <= kFewVectors)
+        embed_kernel<TBF, OBF, POS, DROP, ALIGNED, 1, false>
+            <<<dim3((unsigned)ceil_div(units, kThreads)), kThreads, 0, stream>>>(a, per_row);
+    else
+        embed_kernel<TBF, OBF, POS, DROP, ALIGNED, 4, true>
+            <<<dim3((unsigned)ceil_div(units, kThreads * 4)), kThreads, 0, stream>>>(a, per_row);
+}
+
 template <bool TBF, bool OBF, bool POS>
 void start_embed(const EmbedArgs &a, hipStream_t stream) {
-    const uint32_t per_row = (uint32_t)ceil_div(a.width, kVec);
-    const dim3 grid((unsigned)ceil_div(a.count * per_row, kThreads));
-    const bool aligned = a.width % kVec == 0;
-    if (a.drop.limit == 0)
-        embed_kernel<TBF, OBF, POS, false, true><<<grid, kThreads, 0, stream>>>(a, per_row);
-    else if (aligned)
-        embed_kernel<TBF, OBF, POS, true, true><<<grid, kThreads, 0, stream>>>(a, per_row);
+    if (a.drop.limit == 0) start_embed<TBF, OBF, POS, false, true>(a, stream);
+    else if (a.width % (OBF ? 8 : 4) == 0) start_embed<TBF, OBF, POS, true, true>(a, stream);
+    else start_embed<TBF, OBF, POS, true, false>(a, stream);
+}
+
+template <bool BF16, bool ADD>
+void start_dropout(const DropoutArgs &a, hipStream_t stream) {
+    const int64_t units = ceil_div(a.count, BF16 ? 8 : 4);
+    if (units <= kFewVectors)
+        dropout_kernel<BF16, ADD, 1, false><<<dim3((unsigned)ceil_div(units, kThreads)), kThreads, 0, stream>>>(a);
     else
-        embed_kernel<TBF, OBF, POS, true, false><<<grid, kThreads, 0, stream>>>(a, per_row);
+        dropout_kernel<BF16, ADD, 4, true><<<dim3((unsigned)ceil_div(units, kThreads * 4)), kThreads, 0, stream>>>(a);
 }
 
 template <bool GBF, bool OBF>
@@ -521,13 +556,12 @@ void start_spans(const EmbedGradArgs &a, const EmbedGradPlan &p, const SortedTok
 
 hipError_t launch_dropout(const DropoutArgs &a, hipStream_t stream) {
     if (a.count == 0) return hipSuccess;
-    const dim3 grid((unsigned)ceil_div(a.count, (int64_t)kThreads * kVec));
     if (a.bf16) {
-        if (a.add) dropout_kernel<true, true><<<grid, kThreads, 0, stream>>>(a);
-        else dropout_kernel<true, false><<<grid, kThreads, 0, stream>>>(a);
+        if (a.add) start_dropout<true, true>(a, stream);
+        else start_dropout<true, false>(a, stream);
     } else {
-        if (a.add) dropout_kernel<false, true><<<grid, kThreads, 0, stream>>>(a);
-        else dropout_kernel<false, false><<<grid, kThreads, 0, stream>>>(a);
+        if (a.add) start_dropout<false, true>(a, stream);
+        else start_dropout<false, false>(a, stream);
     }
     return hipGetLastError();
 }
