@@ -786,6 +786,7 @@ gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *target, int64_t
     const int64_t q = blockIdx.y, v = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
     if (q >= round_up(n, 64) || v >= vocab_p) return;
     T *at = static_cast<T *>(e) + q * vocab_p + v, out[V];
+    typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
     if (q < n) {
         const HeadRow s = rows[q];
         const int64_t y = target[first + q];
@@ -794,11 +795,13 @@ gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *target, int64_t
         float x[V];
         if (BF16) {
             _Float16 h[V];
-            __builtin_memcpy(h, __builtin_assume_aligned(at, 16), sizeof h);
+            const u32x4 raw = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(at));
+            __builtin_memcpy(h, &raw, sizeof h);
 #pragma unroll
             for (int j = 0; j < V; ++j) x[j] = (float)h[j];
         } else {
-            __builtin_memcpy(x, __builtin_assume_aligned(at, 16), sizeof x);
+            const u32x4 raw = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(at));
+            __builtin_memcpy(x, &raw, sizeof x);
         }
 #pragma unroll
         for (int j = 0; j < V; ++j) {
@@ -812,7 +815,7 @@ gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *target, int64_t
 #pragma unroll
         for (int j = 0; j < V; ++j) out[j] = 0;
     }
-    __builtin_memcpy(__builtin_assume_aligned(at, 16), out, sizeof out);
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, out), reinterpret_cast<u32x4 *>(at));
 }
 
 // ------------------------------------------------------- launches

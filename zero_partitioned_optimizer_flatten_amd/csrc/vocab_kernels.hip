@@ -240,8 +240,9 @@ __device__ __forceinline__ void zero_row(char *p, int64_t bytes, int lane) {
     if (head > bytes) head = bytes;
     for (int64_t k = 2 * lane; k < head; k += 128) *reinterpret_cast<uint16_t *>(p + k) = 0;
     const int64_t vecs = (bytes - head) / 16;
-    const uint4 z = {0, 0, 0, 0};
-    for (int64_t k = lane; k < vecs; k += 64) *reinterpret_cast<uint4 *>(p + head + 16 * k) = z;
+    typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+    const u32x4 z = {0, 0, 0, 0};
+    for (int64_t k = lane; k < vecs; k += 64) __builtin_nontemporal_store(z, reinterpret_cast<u32x4 *>(p + head + 16 * k));
     for (int64_t k = head + 16 * vecs + 2 * lane; k < bytes; k += 128)
         *reinterpret_cast<uint16_t *>(p + k) = 0;
 }
