@@ -35,10 +35,12 @@ constexpr float kScaleLog2 = 15.0f;
 __host__ __device__ constexpr int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 __host__ __device__ constexpr int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-__device__ __forceinline__ uint16_t narrow(float f) {
-    const uint32_t u = __float_as_uint(f);
-    if ((u & 0x7FFFFFFFu) > 0x7F800000u) return (uint16_t)((u >> 16) | 0x40u);
-    return (uint16_t)((u + 0x7FFFu + ((u >> 16) & 1u)) >> 16);
+// To bf16, nearest, ties to even, NaN kept: two to an instruction.
+__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
+    typedef __attribute__((ext_vector_type(2))) float f32x2_t;
+    typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2_t;
+    const f32x2_t x = {lo, hi};
+    return __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2_t));
 }
 __device__ __forceinline__ float widen(uint16_t h) { return __uint_as_float((uint32_t)h << 16); }
 
@@ -60,9 +62,18 @@ __device__ __forceinline__ int piece_rows(const HeadSums *s, int64_t first, int6
 }
 
 // ------------------------------------------------------- which rows
+// A wave: the loss and the gradient of row i, which takes no part, are zero.
+__device__ __forceinline__ void idle_row(const HeadArgs &a, float *losses, int64_t i, int lane) {
+    if (lane == 0) losses[i] = 0.0f;
+    if (!a.grad_hidden) return;
+    for (int64_t c = lane; c < a.width; c += 64)
+        if (a.bf16) static_cast<uint16_t *>(a.grad_hidden)[i * a.width + c] = 0;
+        else static_cast<float *>(a.grad_hidden)[i * a.width + c] = 0.0f;
+}
+
 // One workgroup: the rows that take part, in order, with their targets, and
-// their weights' sum.
-__global__ void __launch_bounds__(1024) rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target) {
+// their weights' sum; in small calls also what the others get.
+__global__ void __launch_bounds__(1024) rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *idle) {
     __shared__ int32_t found[16];
     __shared__ double parts[16];
     __shared__ float tops[16];
@@ -94,6 +105,9 @@ __global__ void __launch_bounds__(1024) rows_kernel(HeadArgs a, HeadSums *sums, 
             map[at] = (int32_t)i;
             target[at] = (int32_t)load_id(a.targets, a.wide_ids, i);
         }
+        if (idle)
+            for (int k = 0; k < 64 && i0 + 64 * wave + k < a.count; ++k)
+                if (!(mask >> k & 1)) idle_row(a, idle, i0 + 64 * wave + k, lane);
         __syncthreads();
     }
     for (int s = 32; s; s /= 2) {
@@ -197,7 +211,7 @@ struct Schedule {
 // Every lane has the same value; the compiler is not always aware of it.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-__device__ __forceinline__ Schedule schedule(const Product &g, int bp, int bq, int es, int at_once) {
+__device__ __forceinline__ Schedule schedule(const Product &g, int bp, int bq, int es, int at_once, int join) {
     Schedule s;
     int nq = (int)g.nq;
     s.steps = (int)g.steps;
@@ -216,9 +230,9 @@ __device__ __forceinline__ Schedule schedule(const Product &g, int bp, int bq, i
     // in steps: rounds of parts with what a part costs besides, and the joining
     int best = s.steps + 8;
     for (int k = 2; k <= 8 && s.cut > 0; ++k) {
-        if (s.steps < 16 * k || s.cut * k > g.slots) break;
+        if (s.steps < 8 * k || s.cut * k > g.slots) break;
         const int per = uniform((s.steps + k - 1) / k);
-        const int cost = uniform((s.cut * k + at_once - 1) / at_once) * (per + 8) + s.cut * k / 11;
+        const int cost = uniform((s.cut * k + at_once - 1) / at_once) * (per + 8) + s.cut * k / join;
         if (cost < best) best = cost, s.parts = k, s.per = per;
     }
     s.units = s.whole + s.cut * s.parts;
@@ -366,7 +380,7 @@ struct Operand {
     }
 };
 
-template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE>
+template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE, int JOIN>
 __device__ __forceinline__ void product(const Product &g) {
     constexpr int kWaves = WP * WQ;
     constexpr int kP = BP / WP, kQ = BQ / WQ;                 // outputs of a wave
@@ -385,7 +399,7 @@ __device__ __forceinline__ void product(const Product &g) {
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int wp = wave / WQ, wq = wave % WQ;
-    const Schedule sc = schedule(g, BP, BQ, OpP::kEs, AT_ONCE);
+    const Schedule sc = schedule(g, BP, BQ, OpP::kEs, AT_ONCE, JOIN);
     const int64_t nq = g.sums && g.piece_is_q ? piece_rows(g.sums, g.first, g.piece) : g.nq;
     if ((int)blockIdx.x >= sc.units) return;
 
@@ -508,6 +522,8 @@ __device__ __forceinline__ void product(const Product &g) {
         const int64_t pw = u.p0 + wp * kP + lane / 16 * 4, qw = u.q0 + wq * kQ + lane % 16;
         const bool whole = u.p0 + BP <= g.np;
         char *turn = lds + 2 * kStage + wave * kTurn;
+        // whole vectors: those go past the caches, parts of lines would be slow there
+        const bool aligned = EPI == kLogits || (((uintptr_t)g.out | (uintptr_t)(2 * g.ldo)) % 16 == 0);
         // 16 rows of kP numbers of two bytes; 16-byte chunk c of row r at c ^ r.
         constexpr int kChunks = kP / 8;
         auto put = [&](int i, const uint16_t *h) {
@@ -530,7 +546,7 @@ __device__ __forceinline__ void product(const Product &g) {
                 if (q < nq && p < np) {
                     const int64_t row = EPI == kBf16 && g.map ? (int64_t)g.map[g.first + q] : q;
                     uint16_t *d = out + row * ld + p;
-                    if (EPI == kLogits) {             // whole chunks, aligned
+                    if (EPI == kLogits || (aligned && p + 8 <= np)) {
                         typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
                         __builtin_nontemporal_store(__builtin_bit_cast(u32x4, h), reinterpret_cast<u32x4 *>(d));
                     } else if (p + 8 <= np) {
@@ -658,8 +674,8 @@ __device__ __forceinline__ void product(const Product &g) {
 #pragma unroll
                             for (int r = 0; r < 4; ++r) v[r] += widen(h[r]);
                         }
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) h[r] = narrow(v[r]);
+                        const uint32_t w[2] = {narrow2(v[0], v[1]), narrow2(v[2], v[3])};
+                        __builtin_memcpy(h, w, sizeof h);
                         put(i, h);
                     }
                 }
@@ -669,16 +685,16 @@ __device__ __forceinline__ void product(const Product &g) {
     }
 }
 
-template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE>
+template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE, int JOIN>
 __global__ void __launch_bounds__(64 * WP * WQ, 2) product_kernel(Product g) {
-    product<BF16, EPI, TP, TQ, BP, BQ, WP, WQ, AT_ONCE>(g);
+    product<BF16, EPI, TP, TQ, BP, BQ, WP, WQ, AT_ONCE, JOIN>(g);
 }
 
 // The parts of cut tiles, in order, and what a whole tile's epilogue does. Four
 // rows of a tile to a workgroup.
 template <int EPI>
-__global__ void __launch_bounds__(256) join_kernel(Product g, int bp, int bq, int es, int at_once) {
-    const Schedule s = schedule(g, bp, bq, es, at_once);
+__global__ void __launch_bounds__(256) join_kernel(Product g, int bp, int bq, int es, int at_once, int join) {
+    const Schedule s = schedule(g, bp, bq, es, at_once, join);
     const int per = bq / 4, tile = blockIdx.x / per;
     if (s.parts == 1 || tile >= s.cut) return;
     const int64_t nq = g.piece_is_q ? piece_rows(g.sums, g.first, g.piece) : g.nq;
@@ -705,20 +721,16 @@ __global__ void __launch_bounds__(256) join_kernel(Product g, int bp, int bq, in
             } else {
                 uint16_t *d = static_cast<uint16_t *>(g.out) + at + r;
                 if (g.add_out) x += widen(*d);
-                *d = narrow(x);
+                *d = (uint16_t)narrow2(x, 0.0f);
             }
         }
     }
 }
 
 // ------------------------------------------------------- the softmax
-// A wave to a row: its maximum and sum from its tiles', and its loss.
-__global__ void __launch_bounds__(256)
-softmax_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t first, int64_t piece,
-               const f32x2 *stat, int64_t subtiles, HeadRow *rows, float *losses) {
-    const int lane = threadIdx.x % 64;
-    const int64_t q = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-    if (q >= piece_rows(sums, first, piece)) return;
+// A wave: the maximum and sum of row q of the piece from its tiles', and its loss.
+__device__ __forceinline__ void softmax_row(const HeadArgs &a, const HeadSums *sums, const int32_t *map, int64_t first,
+                                            const f32x2 *stat, int64_t subtiles, HeadRow *rows, float *losses, int64_t q, int lane) {
     const f32x2 *s = stat + q * subtiles;
     float top = -INFINITY;
     for (int64_t k = lane; k < subtiles; k += 64) top = fmaxf(top, s[k].x);
@@ -739,10 +751,24 @@ softmax_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t fir
     rows[q].share = share;
 }
 
-// One workgroup: the weighted sum of the losses, in binary64.
+__global__ void __launch_bounds__(256)
+softmax_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t first, int64_t piece,
+               const f32x2 *stat, int64_t subtiles, HeadRow *rows, float *losses) {
+    const int64_t q = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
+    if (q < piece_rows(sums, first, piece))
+        softmax_row(a, sums, map, first, stat, subtiles, rows, losses, q, threadIdx.x % 64);
+}
+
+// One workgroup: the weighted sum of the losses, in binary64; in small calls of the
+// rows' softmax first.
 __global__ void __launch_bounds__(1024)
-loss_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, const float *losses) {
+loss_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, const f32x2 *stat, int64_t subtiles, HeadRow *rows, float *losses) {
     __shared__ double parts[16];
+    if (stat) {
+        for (int64_t q = threadIdx.x / 64; q < sums->rows; q += 16)
+            softmax_row(a, sums, map, 0, stat, subtiles, rows, losses, q, threadIdx.x % 64);
+        __syncthreads();                          // a workgroup sees its own stores
+    }
     double sum = 0.0;
     for (int64_t k = threadIdx.x; k < sums->rows; k += 1024) {
         const int64_t i = map[k];
@@ -763,12 +789,7 @@ __global__ void __launch_bounds__(256) idle_rows_kernel(HeadArgs a, float *losse
     const int lane = threadIdx.x % 64;
     const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
     if (i >= a.count) return;
-    if (takes_part(a, i)) return;
-    if (lane == 0) losses[i] = 0.0f;
-    if (!a.grad_hidden) return;
-    for (int64_t c = lane; c < a.width; c += 64)
-        if (a.bf16) static_cast<uint16_t *>(a.grad_hidden)[i * a.width + c] = 0;
-        else static_cast<float *>(a.grad_hidden)[i * a.width + c] = 0.0f;
+    if (!takes_part(a, i)) idle_row(a, losses, i, lane);
 }
 
 // ------------------------------------------------------- e to G
@@ -804,12 +825,22 @@ gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *target, int64_t
             __builtin_memcpy(x, &raw, sizeof x);
         }
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            float d = x[j] * share;
-            if (v + j == y) d -= s.share;
-            if (v + j >= a.vocab) d = 0.0f;
-            if constexpr (BF16) out[j] = narrow(d);
-            else out[j] = d;
+        for (int j = 0; j < V; ++j) x[j] *= share;
+        if (y >= v && y < v + V)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (v + j == y) x[j] -= s.share;
+        if (v + V > a.vocab)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (v + j >= a.vocab) x[j] = 0.0f;
+        if constexpr (BF16) {
+            uint32_t w[V / 2];
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) w[j] = narrow2(x[2 * j], x[2 * j + 1]);
+            __builtin_memcpy(out, w, sizeof out);
+        } else {
+            __builtin_memcpy(out, x, sizeof out);
         }
     } else {
 #pragma unroll
@@ -824,15 +855,19 @@ void start_product(const Product &g, int shape, hipStream_t stream) {
     const TileShape t = kTiles[shape];
     const int64_t tiles = ceil_div(g.np, t.p) * ceil_div(g.nq, t.q);
     const unsigned grid = (unsigned)(g.slots > 0 || tiles > t.at_once ? t.at_once : tiles);
-    if (shape == 0) product_kernel<BF16, EPI, TP, TQ, 256, 256, 2, 4, kTiles[0].at_once><<<grid, 512, 0, stream>>>(g);
-    else if (shape == 1) product_kernel<BF16, EPI, TP, TQ, 128, 128, 2, 2, kTiles[1].at_once><<<grid, 256, 0, stream>>>(g);
-    else product_kernel<BF16, EPI, TP, TQ, 128, 32, 4, 1, kTiles[2].at_once><<<grid, 256, 0, stream>>>(g);
+    if constexpr (BF16)
+        if (shape == 0) product_kernel<BF16, EPI, TP, TQ, 256, 256, 2, 4, kTiles[0].at_once, kTiles[0].join><<<grid, 512, 0, stream>>>(g);
+    if (shape == 1) product_kernel<BF16, EPI, TP, TQ, 128, 128, 2, 2, kTiles[1].at_once, kTiles[1].join><<<grid, 256, 0, stream>>>(g);
+    if (shape == 2) product_kernel<BF16, EPI, TP, TQ, 128, 32, 4, 1, kTiles[2].at_once, kTiles[2].join><<<grid, 256, 0, stream>>>(g);
     if constexpr (EPI != kLogits)
         if (g.slots > 0) {
             const int64_t cut = tiles < t.at_once ? tiles : t.at_once - 1;
-            join_kernel<EPI><<<(unsigned)(cut * (t.q / 4)), 256, 0, stream>>>(g, t.p, t.q, BF16 ? 2 : 4, t.at_once);
+            join_kernel<EPI><<<(unsigned)(cut * (t.q / 4)), 256, 0, stream>>>(g, t.p, t.q, BF16 ? 2 : 4, t.at_once, t.join);
         }
 }
+
+// Numbers that one workgroup goes through in about the time of a launch.
+constexpr int64_t kSmallCall = 65536;
 
 template <bool BF16>
 hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
@@ -844,8 +879,10 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
     auto *rows = reinterpret_cast<HeadRow *>(w + p.row_off);
     auto *stat = reinterpret_cast<f32x2 *>(w + p.stat_off);
     const bool grads = a.grad_hidden || a.grad_table;
-    rows_kernel<<<1, 1024, 0, stream>>>(a, sums, map, target);
-    if (a.count > 0) idle_rows_kernel<<<(unsigned)ceil_div(a.count, 4), 256, 0, stream>>>(a, losses);
+    const bool small = a.count * (a.grad_hidden ? a.width : 1) <= kSmallCall;
+    rows_kernel<<<1, 1024, 0, stream>>>(a, sums, map, target, small ? losses : nullptr);
+    if (!small) idle_rows_kernel<<<(unsigned)ceil_div(a.count, 4), 256, 0, stream>>>(a, losses);
+    const bool one = p.pieces == 1 && a.count * p.subtiles <= kSmallCall / 4;
     const void *table = a.table;
     if (p.pack_table) {
         pack_kernel<BF16><<<(unsigned)a.vocab, 256, 0, stream>>>(a.table, a.vocab, a.width, nullptr, nullptr, 0,
@@ -875,8 +912,11 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
         g.e = grads ? w + p.e_off : nullptr;
         g.lde = p.vocab_p;
         start_product<BF16, kLogits, false, false>(g, p.tile_logits, stream);
-        softmax_kernel<<<(unsigned)ceil_div(p.piece, 4), 256, 0, stream>>>(a, sums, map, first, p.piece, stat,
-                                                                           p.subtiles, rows, losses);
+        if (one)
+            loss_kernel<<<1, 1024, 0, stream>>>(a, sums, map, stat, p.subtiles, rows, losses);
+        else
+            softmax_kernel<<<(unsigned)ceil_div(p.piece, 4), 256, 0, stream>>>(a, sums, map, first, p.piece, stat, p.subtiles,
+                                                                               rows, losses);
         if (!grads) continue;
         gradient_kernel<BF16><<<dim3((unsigned)ceil_div(p.vocab_p * es, 256 * 16), (unsigned)p.piece_p), 256, 0, stream>>>(
             a, sums, target, first, p.piece, stat, p.subtiles, p.sub, rows, w + p.e_off, p.vocab_p);
@@ -931,7 +971,7 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
             }
         }
     }
-    loss_kernel<<<1, 1024, 0, stream>>>(a, sums, map, losses);
+    if (!one) loss_kernel<<<1, 1024, 0, stream>>>(a, sums, map, nullptr, 0, rows, losses);
     return hipGetLastError();
 }
 

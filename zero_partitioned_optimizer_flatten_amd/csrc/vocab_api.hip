@@ -138,11 +138,31 @@ namespace {
 
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
-// The largest tile that still gives most compute units one.
-int choose_tile(int64_t np, int64_t nq, int64_t splits) {
-    if (nq <= 32) return 2;
-    if (ceil_div(np, 256) * ceil_div(nq, 256) * splits >= 200) return 0;
-    return 1;
+// The tile that takes least time: rounds of as many tiles as run at once, by the
+// stages of a tile and about 8 of its epilogue, with a last round cut into parts as
+// the kernels' schedule does. A stage of a round takes 1, 0.62 and 0.6 by the tile
+// (bf16): the middle and the small tile multiply at 0.8 and 0.3 of the large one's
+// rate, since they bring 2 and 2.5 times as much to LDS for it (2048 rows of GPT-2's
+// head: 665 us with large tiles, 704 with middle, 1105 with small). With fp32 the
+// matrix cores bound all three (8192 x 32000 x 2048: 23.5, 23.7 and 26.5 ms), and the
+// large one is not built.
+int choose_tile(int64_t np, int64_t nq, int64_t steps, bool cut, bool bf16) {
+    int best = 1;
+    double least = 0.0;
+    for (int shape = bf16 ? 0 : 1; shape < 3; ++shape) {
+        const TileShape t = kTiles[shape];
+        const int64_t tiles = ceil_div(np, t.p) * ceil_div(nq, t.q), rest = tiles % t.at_once;
+        double last = rest > 0 ? (double)(steps + 8) : 0.0;
+        if (cut && rest > 0)
+            for (int64_t k = 2; k <= 8 && steps >= 8 * k && rest * k <= 1024; ++k) {
+                const double c = (double)(ceil_div(rest * k, t.at_once) * (ceil_div(steps, k) + 8)) + (double)(rest * k) / t.join;
+                if (c < last) last = c;
+            }
+        const double unit = shape == 0 ? 1.0 : shape == 1 ? (bf16 ? 0.62 : 0.5) : nq <= 32 ? 0.25 : bf16 ? 0.6 : 0.28;
+        const double cost = unit * ((double)(tiles / t.at_once * (steps + 8)) + last);
+        if (least == 0.0 || cost < least) least = cost, best = shape;
+    }
+    return best;
 }
 
 }  // namespace
@@ -161,16 +181,16 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     p.piece = piece;
     p.pieces = a.count > 0 ? ceil_div(a.count, piece) : (a.grad_table ? 1 : 0);
     p.piece_p = round_up(piece, 64);
-    p.tile_logits = choose_tile(a.vocab, piece, 1);
+    p.tile_logits = choose_tile(a.vocab, piece, p.width_p / step, false, a.bf16);
     p.sub = kTiles[p.tile_logits].sub;
     p.subtiles = round_up(a.vocab, kTiles[p.tile_logits].p) / p.sub;
-    p.tile_hidden = choose_tile(a.width, piece, 4);
-    p.tile_table = choose_tile(a.width, a.vocab, 1);
+    p.tile_hidden = choose_tile(a.width, piece, ceil_div(a.vocab, step), true, a.bf16);
+    p.tile_table = choose_tile(a.width, a.vocab, ceil_div(piece, step), true, a.bf16);
     // parts of tiles that do not fill a round, as many as 8 of each
     auto slots = [&](int shape, int64_t np, int64_t nq, int64_t steps) -> int {
         const TileShape t = kTiles[shape];
         const int64_t tiles = ceil_div(np, t.p) * ceil_div(nq, t.q);
-        if (steps < 32) return 0;
+        if (steps < 16) return 0;
         const int64_t n = 8 * (tiles < t.at_once ? tiles : t.at_once);
         return (int)(n < 1024 ? n : 1024);
     };

@@ -111,8 +111,9 @@ struct HeadRow {
 // them.
 struct TileShape {
     int p, q, sub, at_once;
+    int join;                     // parts that are joined in the time of a stage
 };
-constexpr TileShape kTiles[] = {{256, 256, 128, 256}, {128, 128, 64, 512}, {128, 32, 32, 768}};
+constexpr TileShape kTiles[] = {{256, 256, 128, 256, 11}, {128, 128, 64, 512, 25}, {128, 32, 32, 768, 55}};
 struct HeadPlan {
     int64_t piece, pieces;        // rows of hidden in a piece
     int64_t width_p, vocab_p, piece_p;   // extents padded for the products' long axes
