@@ -592,7 +592,7 @@ int zero_head_loss_workspace(int64_t count, int64_t vocab, int64_t width,
  * their last bits. EINVAL: as above, grad_scale not finite, piece_rows < 0, a
  * workspace too small or not 256-byte aligned, overlapping buffers.
  * EUNSUPPORTED: rows of width or vocab elements of 4 MiB or more, pieces of
- * that many rows. */
+ * more than 2^20 rows or 64 GiB, 2^31 rows. */
 int zero_head_loss(const void *hidden, const void *table, zero_dtype dtype,
                    const void *targets, int32_t id_bytes, int64_t count,
                    int64_t vocab, int64_t width, const float *weights,

@@ -68,6 +68,12 @@ def test_head_loss_over_large_tiles(n, vocab, width, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+def test_more_rows_than_a_grid_has_lines(dtype):
+    hidden, table, targets, g = make(70001, 40, 16, dtype, ignored=0.01)
+    run(hidden, table, targets)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 @pytest.mark.parametrize("n,vocab,width", [(1, 50, 16), (70, 1000, 64), (200, 3000, 65)])
 def test_loss_alone(n, vocab, width, dtype):
     hidden, table, targets, g = make(n, vocab, width, dtype, ignored=0.2)

@@ -205,6 +205,7 @@ def test_head_loss_refuses(L):
     refused(L, UNSUPPORTED, call(vocab=2 ** 21), "4 MiB")
     refused(L, UNSUPPORTED, call(width=2 ** 21), "4 MiB")
     refused(L, UNSUPPORTED, call(count=2 ** 31), "more than one call")
+    refused(L, UNSUPPORTED, call(count=2 ** 30, vocab=1000000, piece=2 ** 20), "64 GiB")
     n64 = ctypes.c_int64()
     assert L.zero_head_loss_workspace(20, 50, 16, 1, 1, 1, 1, 0, None) == INVALID
     assert L.zero_head_loss_workspace(20, 50, 16, 1, 1, 1, 5, 0, ctypes.byref(n64)) == INVALID

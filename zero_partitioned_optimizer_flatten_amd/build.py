@@ -35,11 +35,14 @@ def build(verbose: bool = False) -> str:
     return LIB
 
 
-def asm(out_dir: str) -> None:
+KERNELS = ("zero_kernels", "adamw_kernels", "vocab_kernels", "head_kernels")
+
+
+def asm(out_dir: str, names=KERNELS) -> None:
     """Write the gfx950 assembly of the kernels (for inspection)."""
     os.makedirs(out_dir, exist_ok=True)
     flags = [f for f in FLAGS if f not in ("-shared", "-fPIC")]
-    for name in ("zero_kernels", "adamw_kernels", "vocab_kernels", "head_kernels"):
+    for name in names:
         subprocess.check_call([HIPCC, *flags, "--cuda-device-only", "-S",
                                os.path.join(CSRC, name + ".hip"),
                                "-o", os.path.join(out_dir, name + ".s")])

@@ -61,6 +61,53 @@ __device__ __forceinline__ int piece_rows(const HeadSums *s, int64_t first, int6
     return __builtin_amdgcn_readfirstlane((int)(n < 0 ? 0 : n < piece ? n : piece));
 }
 
+// ------------------------------------------------------- copies
+// `dst`, cols_p numbers on a 16-byte address, = `src`, cols numbers anywhere, and
+// zeros behind them; all zeros for a null src. `threads` of them, this one being `at`.
+template <bool BF16>
+__device__ __forceinline__ void pack_row(const void *src, int64_t cols, void *dst, int64_t cols_p, int at, int threads) {
+    using T = typename Elem<BF16>::type;
+    const T *s = static_cast<const T *>(src);
+    T *d = static_cast<T *>(dst);
+    constexpr int V = 16 / sizeof(T);
+    for (int64_t c = (int64_t)at * V; c < cols_p; c += (int64_t)threads * V) {
+        T x[V];
+        if (s && c + V <= cols) {
+            __builtin_memcpy(x, s + c, sizeof x);
+        } else {
+#pragma unroll
+            for (int k = 0; k < V; ++k) x[k] = s && c + k < cols ? s[c + k] : (T)0;
+        }
+        __builtin_memcpy(__builtin_assume_aligned(d + c, 16), x, sizeof x);
+    }
+}
+
+// Row r of the packed hidden states of a piece with n rows.
+template <bool BF16>
+__device__ __forceinline__ void pack_hidden(const HeadArgs &a, const int32_t *map, int64_t first, int n, int64_t r,
+                                            void *packed, int64_t width_p, int at, int threads) {
+    constexpr int es = BF16 ? 2 : 4;
+    const char *src = r < n ? static_cast<const char *>(a.hidden) + (int64_t)map[first + r] * a.width * es : nullptr;
+    pack_row<BF16>(src, a.width, static_cast<char *>(packed) + r * width_p * es, width_p, at, threads);
+}
+
+// The rows of a piece, and zeros up to a whole stage. A workgroup to a row.
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+pack_hidden_kernel(HeadArgs a, const int32_t *map, const HeadSums *sums, int64_t first, int64_t piece, void *packed, int64_t width_p) {
+    const int n = piece_rows(sums, first, piece);
+    if (blockIdx.x < round_up(n, 64)) pack_hidden<BF16>(a, map, first, n, blockIdx.x, packed, width_p, threadIdx.x, 256);
+}
+
+// A table whose rows are not whole stages on 16-byte addresses.
+template <bool BF16>
+__global__ void __launch_bounds__(256) pack_table_kernel(HeadArgs a, void *packed, int64_t width_p) {
+    constexpr int es = BF16 ? 2 : 4;
+    const int64_t r = blockIdx.x;
+    pack_row<BF16>(static_cast<const char *>(a.table) + r * a.width * es, a.width, static_cast<char *>(packed) + r * width_p * es,
+                   width_p, threadIdx.x, 256);
+}
+
 // ------------------------------------------------------- which rows
 // A wave: the loss and the gradient of row i, which takes no part, are zero.
 __device__ __forceinline__ void idle_row(const HeadArgs &a, float *losses, int64_t i, int lane) {
@@ -72,8 +119,11 @@ __device__ __forceinline__ void idle_row(const HeadArgs &a, float *losses, int64
 }
 
 // One workgroup: the rows that take part, in order, with their targets, and
-// their weights' sum; in small calls also what the others get.
-__global__ void __launch_bounds__(1024) rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *idle) {
+// their weights' sum; in small calls also what the others get (idle: the losses)
+// and the rows packed.
+template <bool BF16>
+__global__ void __launch_bounds__(1024)
+rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *idle, void *packed, int64_t width_p) {
     __shared__ int32_t found[16];
     __shared__ double parts[16];
     __shared__ float tops[16];
@@ -128,33 +178,9 @@ __global__ void __launch_bounds__(1024) rows_kernel(HeadArgs a, HeadSums *sums, 
         sums->most = most;
         sums->scale = (float)((double)a.grad_scale * (double)most / (a.mean && weight != 0.0 ? weight : 1.0));
     }
-}
-
-// ------------------------------------------------------- copies
-// dst [rows_p][cols_p] = the mapped rows of src [.][cols], zeros behind them.
-// A row of threads to a destination row.
-template <bool BF16>
-__global__ void __launch_bounds__(256)
-pack_kernel(const void *src, int64_t rows, int64_t cols, const int32_t *map, const HeadSums *sums,
-            int64_t first, void *dst, int64_t rows_p, int64_t cols_p) {
-    using T = typename Elem<BF16>::type;
-    const int64_t r = blockIdx.x;
-    const int64_t n = map ? piece_rows(sums, first, rows) : rows;
-    if (r >= n && r >= round_up(n, 64)) return;
-    const int64_t from = r < n ? (map ? map[first + r] : r) : -1;
-    const T *s = static_cast<const T *>(src) + from * cols;
-    T *d = static_cast<T *>(dst) + r * cols_p;
-    constexpr int V = 16 / sizeof(T);
-    for (int64_t c = (int64_t)threadIdx.x * V; c < cols_p; c += 256 * V) {
-        T x[V];
-        if (from >= 0 && c + V <= cols) {
-            __builtin_memcpy(x, s + c, sizeof x);
-        } else {
-#pragma unroll
-            for (int k = 0; k < V; ++k) x[k] = from >= 0 && c + k < cols ? s[c + k] : (T)0;
-        }
-        __builtin_memcpy(__builtin_assume_aligned(d + c, 16), x, sizeof x);
-    }
+    if (packed)                                   // the map is this workgroup's own, and synchronised
+        for (int64_t r = wave; r < round_up(base, 64); r += 16)
+            pack_hidden<BF16>(a, map, 0, (int)base, r, packed, width_p, lane, 64);
 }
 
 // ------------------------------------------------------- the product
@@ -727,6 +753,75 @@ __global__ void __launch_bounds__(256) join_kernel(Product g, int bp, int bq, in
     }
 }
 
+// ------------------------------------------------------- e to G
+// In place, [rows][vocab_p]; zeros behind the last row up to a whole stage of the
+// product across the rows, and behind the vocabulary.
+struct Gradient {
+    const int32_t *target;        // of the piece's rows
+    const f32x2 *stat;
+    const HeadRow *rows;
+    void *e;
+    int64_t subtiles, vocab_p;
+    int sub;
+};
+
+// 16 bytes of row q, from entry v on, of a piece with n rows.
+template <bool BF16>
+__device__ __forceinline__ void gradient_chunk(const Gradient &g, int64_t vocab, int n, int64_t q, int64_t v) {
+    using T = typename Elem<BF16>::type;
+    constexpr int V = 16 / sizeof(T);
+    T *at = static_cast<T *>(g.e) + q * g.vocab_p + v, out[V];
+    typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+    if (q < n) {
+        const HeadRow s = g.rows[q];
+        const int64_t y = g.target[q];
+        const float share = __builtin_amdgcn_exp2f(g.stat[q * g.subtiles + v / g.sub].x - s.top) * s.inv
+                            * (BF16 ? 0x1p-15f : 1.0f);
+        float x[V];
+        if (BF16) {
+            _Float16 h[V];
+            const u32x4 raw = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(at));
+            __builtin_memcpy(h, &raw, sizeof h);
+#pragma unroll
+            for (int j = 0; j < V; ++j) x[j] = (float)h[j];
+        } else {
+            const u32x4 raw = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(at));
+            __builtin_memcpy(x, &raw, sizeof x);
+        }
+#pragma unroll
+        for (int j = 0; j < V; ++j) x[j] *= share;
+        if (y >= v && y < v + V)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (v + j == y) x[j] -= s.share;
+        if (v + V > vocab)
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (v + j >= vocab) x[j] = 0.0f;
+        if constexpr (BF16) {
+            uint32_t w[V / 2];
+#pragma unroll
+            for (int j = 0; j < V / 2; ++j) w[j] = narrow2(x[2 * j], x[2 * j + 1]);
+            __builtin_memcpy(out, w, sizeof out);
+        } else {
+            __builtin_memcpy(out, x, sizeof out);
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < V; ++j) out[j] = 0;
+    }
+    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, out), reinterpret_cast<u32x4 *>(at));
+}
+
+template <bool BF16>
+__global__ void __launch_bounds__(256)
+gradient_kernel(Gradient g, int64_t vocab, const HeadSums *sums, int64_t first, int64_t piece, uint32_t per_row) {
+    constexpr int V = BF16 ? 8 : 4;
+    const int n = piece_rows(sums, first, piece);
+    const int64_t q = blockIdx.x / per_row, v = ((int64_t)(blockIdx.x % per_row) * 256 + threadIdx.x) * V;
+    if (q < round_up(n, 64) && v < g.vocab_p) gradient_chunk<BF16>(g, vocab, n, q, v);
+}
+
 // ------------------------------------------------------- the softmax
 // A wave: the maximum and sum of row q of the piece from its tiles', and its loss.
 __device__ __forceinline__ void softmax_row(const HeadArgs &a, const HeadSums *sums, const int32_t *map, int64_t first,
@@ -760,14 +855,21 @@ softmax_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t fir
 }
 
 // One workgroup: the weighted sum of the losses, in binary64; in small calls of the
-// rows' softmax first.
+// rows' softmax first, and of e's turning into G (g.e, if there).
+template <bool BF16>
 __global__ void __launch_bounds__(1024)
-loss_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, const f32x2 *stat, int64_t subtiles, HeadRow *rows, float *losses) {
+loss_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, Gradient g, HeadRow *rows, float *losses) {
     __shared__ double parts[16];
-    if (stat) {
-        for (int64_t q = threadIdx.x / 64; q < sums->rows; q += 16)
-            softmax_row(a, sums, map, 0, stat, subtiles, rows, losses, q, threadIdx.x % 64);
+    if (g.stat) {
+        const int n = (int)sums->rows;
+        for (int64_t q = threadIdx.x / 64; q < n; q += 16)
+            softmax_row(a, sums, map, 0, g.stat, g.subtiles, rows, losses, q, threadIdx.x % 64);
         __syncthreads();                          // a workgroup sees its own stores
+        constexpr int V = BF16 ? 8 : 4;
+        const uint32_t per_row = (uint32_t)(g.vocab_p / V);
+        if (g.e)
+            for (uint32_t k = threadIdx.x; k < (uint32_t)round_up(n, 64) * per_row; k += 1024)
+                gradient_chunk<BF16>(g, a.vocab, n, k / per_row, (int64_t)(k % per_row) * V);
     }
     double sum = 0.0;
     for (int64_t k = threadIdx.x; k < sums->rows; k += 1024) {
@@ -786,67 +888,8 @@ loss_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, const f32x2 *s
 
 // losses and rows of grad_hidden that take no part: zero.
 __global__ void __launch_bounds__(256) idle_rows_kernel(HeadArgs a, float *losses) {
-    const int lane = threadIdx.x % 64;
-    const int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-    if (i >= a.count) return;
-    if (!takes_part(a, i)) idle_row(a, losses, i, lane);
-}
-
-// ------------------------------------------------------- e to G
-// In place, [rows][vocab_p]; zeros behind the last row up to a whole stage of the
-// product across the rows, and behind the vocabulary. Eight (four) numbers to a
-// thread, grid (columns, rows).
-template <bool BF16>
-__global__ void __launch_bounds__(256)
-gradient_kernel(HeadArgs a, const HeadSums *sums, const int32_t *target, int64_t first, int64_t piece,
-                const f32x2 *stat, int64_t subtiles, int sub, const HeadRow *rows, void *e,
-                int64_t vocab_p) {
-    using T = typename Elem<BF16>::type;
-    constexpr int V = 16 / sizeof(T);
-    const int n = piece_rows(sums, first, piece);
-    const int64_t q = blockIdx.y, v = ((int64_t)blockIdx.x * 256 + threadIdx.x) * V;
-    if (q >= round_up(n, 64) || v >= vocab_p) return;
-    T *at = static_cast<T *>(e) + q * vocab_p + v, out[V];
-    typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
-    if (q < n) {
-        const HeadRow s = rows[q];
-        const int64_t y = target[first + q];
-        const float share = __builtin_amdgcn_exp2f(stat[q * subtiles + v / sub].x - s.top) * s.inv
-                            * (BF16 ? 0x1p-15f : 1.0f);
-        float x[V];
-        if (BF16) {
-            _Float16 h[V];
-            const u32x4 raw = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(at));
-            __builtin_memcpy(h, &raw, sizeof h);
-#pragma unroll
-            for (int j = 0; j < V; ++j) x[j] = (float)h[j];
-        } else {
-            const u32x4 raw = __builtin_nontemporal_load(reinterpret_cast<const u32x4 *>(at));
-            __builtin_memcpy(x, &raw, sizeof x);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j) x[j] *= share;
-        if (y >= v && y < v + V)
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (v + j == y) x[j] -= s.share;
-        if (v + V > a.vocab)
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                if (v + j >= a.vocab) x[j] = 0.0f;
-        if constexpr (BF16) {
-            uint32_t w[V / 2];
-#pragma unroll
-            for (int j = 0; j < V / 2; ++j) w[j] = narrow2(x[2 * j], x[2 * j + 1]);
-            __builtin_memcpy(out, w, sizeof out);
-        } else {
-            __builtin_memcpy(out, x, sizeof out);
-        }
-    } else {
-#pragma unroll
-        for (int j = 0; j < V; ++j) out[j] = 0;
-    }
-    __builtin_nontemporal_store(__builtin_bit_cast(u32x4, out), reinterpret_cast<u32x4 *>(at));
+    for (int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; i < a.count; i += (int64_t)gridDim.x * 4)
+        if (!takes_part(a, i)) idle_row(a, losses, i, threadIdx.x % 64);
 }
 
 // ------------------------------------------------------- launches
@@ -879,20 +922,22 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
     auto *rows = reinterpret_cast<HeadRow *>(w + p.row_off);
     auto *stat = reinterpret_cast<f32x2 *>(w + p.stat_off);
     const bool grads = a.grad_hidden || a.grad_table;
+    // what one workgroup does in about a launch's time does not get one
     const bool small = a.count * (a.grad_hidden ? a.width : 1) <= kSmallCall;
-    rows_kernel<<<1, 1024, 0, stream>>>(a, sums, map, target, small ? losses : nullptr);
-    if (!small) idle_rows_kernel<<<(unsigned)ceil_div(a.count, 4), 256, 0, stream>>>(a, losses);
+    const bool pack = p.pieces == 1 && round_up(a.count, 64) * p.width_p <= kSmallCall;
     const bool one = p.pieces == 1 && a.count * p.subtiles <= kSmallCall / 4;
+    const bool turn = one && grads && p.piece_p * p.vocab_p <= kSmallCall / 4;
+    rows_kernel<BF16><<<1, 1024, 0, stream>>>(a, sums, map, target, small ? losses : nullptr, pack ? w + p.hidden_off : nullptr, p.width_p);
+    if (!small) idle_rows_kernel<<<(unsigned)(a.count < 65536 ? ceil_div(a.count, 4) : 16384), 256, 0, stream>>>(a, losses);
     const void *table = a.table;
     if (p.pack_table) {
-        pack_kernel<BF16><<<(unsigned)a.vocab, 256, 0, stream>>>(a.table, a.vocab, a.width, nullptr, nullptr, 0,
-                                                                 w + p.table_off, a.vocab, p.width_p);
+        pack_table_kernel<BF16><<<(unsigned)a.vocab, 256, 0, stream>>>(a, w + p.table_off, p.width_p);
         table = w + p.table_off;
     }
     for (int64_t k = 0; k < p.pieces; ++k) {
         const int64_t first = k * p.piece;
-        pack_kernel<BF16><<<(unsigned)p.piece_p, 256, 0, stream>>>(a.hidden, p.piece, a.width, map, sums, first,
-                                                                   w + p.hidden_off, p.piece_p, p.width_p);
+        if (!pack)
+            pack_hidden_kernel<BF16><<<(unsigned)p.piece_p, 256, 0, stream>>>(a, map, sums, first, p.piece, w + p.hidden_off, p.width_p);
         Product g = {};
         g.sums = sums;
         g.first = first;
@@ -912,14 +957,20 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
         g.e = grads ? w + p.e_off : nullptr;
         g.lde = p.vocab_p;
         start_product<BF16, kLogits, false, false>(g, p.tile_logits, stream);
-        if (one)
-            loss_kernel<<<1, 1024, 0, stream>>>(a, sums, map, stat, p.subtiles, rows, losses);
-        else
+        Gradient turned = {target + first, stat, rows, w + p.e_off, p.subtiles, p.vocab_p, p.sub};
+        if (one) {
+            if (!turn) turned.e = nullptr;
+            loss_kernel<BF16><<<1, 1024, 0, stream>>>(a, sums, map, turned, rows, losses);
+            turned.e = w + p.e_off;
+        } else {
             softmax_kernel<<<(unsigned)ceil_div(p.piece, 4), 256, 0, stream>>>(a, sums, map, first, p.piece, stat, p.subtiles,
                                                                                rows, losses);
+        }
         if (!grads) continue;
-        gradient_kernel<BF16><<<dim3((unsigned)ceil_div(p.vocab_p * es, 256 * 16), (unsigned)p.piece_p), 256, 0, stream>>>(
-            a, sums, target, first, p.piece, stat, p.subtiles, p.sub, rows, w + p.e_off, p.vocab_p);
+        if (!turn) {
+            const int64_t per_row = ceil_div(p.vocab_p * es, 256 * 16);
+            gradient_kernel<BF16><<<(unsigned)(p.piece_p * per_row), 256, 0, stream>>>(turned, a.vocab, sums, first, p.piece, (uint32_t)per_row);
+        }
         if (a.grad_hidden) {
             Product h = {};
             h.sums = sums;
@@ -971,7 +1022,7 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
             }
         }
     }
-    if (!one) loss_kernel<<<1, 1024, 0, stream>>>(a, sums, map, nullptr, 0, rows, losses);
+    if (!one) loss_kernel<BF16><<<1, 1024, 0, stream>>>(a, sums, map, Gradient{}, rows, losses);
     return hipGetLastError();
 }
 

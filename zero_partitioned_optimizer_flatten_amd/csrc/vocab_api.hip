@@ -19,6 +19,7 @@ int64_t dtype_size(zero_dtype d) { return d == ZERO_BF16 ? 2 : 4; }
 
 // Rows are addressed by 32-bit offsets inside a tile of 256 of them.
 constexpr int64_t kMaxRowBytes = (int64_t)1 << 22;
+constexpr int64_t kMaxPiece = (int64_t)1 << 20;
 // A dispatch holds fewer than 2^32 work-items.
 constexpr int64_t kMaxUnits = 0xFFFFFF00ll;
 constexpr int64_t kMaxInt = 0x7FFFFFFF;
@@ -105,9 +106,13 @@ int head_sizes(int64_t count, int64_t vocab, int64_t width, zero_dtype dtype, in
     if ((vocab + 128) * es > kMaxRowBytes || (width + 64) * es > kMaxRowBytes)
         return fail(ZERO_EUNSUPPORTED, "table of %lld x %lld: a row of either length must stay under 4 MiB",
                     (long long)vocab, (long long)width);
-    if (piece > 0 && ((piece < count ? piece : count) + 64) * es > kMaxRowBytes)
-        return fail(ZERO_EUNSUPPORTED, "pieces of %lld rows: at most 2^20 (fp32) or 2^21 (bf16), less 64",
-                    (long long)piece);
+    if (piece > kMaxPiece && count > kMaxPiece)
+        return fail(ZERO_EUNSUPPORTED, "pieces of %lld rows: at most 2^20", (long long)piece);
+    // numbers of a piece against the vocabulary are turned 16 bytes to a work-item
+    const int64_t rows = piece > 0 && piece < count ? piece : count;
+    if (piece > 0 && (rows + 63) / 64 * 64 > kMaxUnits / 256 / ceil_div((vocab + 128) * es, 4096))
+        return fail(ZERO_EUNSUPPORTED, "pieces of %lld rows take more than 64 GiB with a vocabulary of %lld", (long long)piece,
+                    (long long)vocab);
     return ZERO_OK;
 }
 
