@@ -237,7 +237,7 @@ struct Schedule {
 // Every lane has the same value; the compiler is not always aware of it.
 __device__ __forceinline__ int uniform(int x) { return __builtin_amdgcn_readfirstlane(x); }
 
-__device__ __forceinline__ Schedule schedule(const Product &g, int bp, int bq, int es, int at_once, int join) {
+__device__ __forceinline__ Schedule schedule(const Product &g, int bp, int bq, int es, int at_once, int join, int part_cost) {
     Schedule s;
     int nq = (int)g.nq;
     s.steps = (int)g.steps;
@@ -253,13 +253,19 @@ __device__ __forceinline__ Schedule schedule(const Product &g, int bp, int bq, i
     s.whole = tiles - s.cut;
     s.parts = 1;
     s.per = s.steps;
-    // in steps: rounds of parts with what a part costs besides, and the joining
-    int best = s.steps + 8;
-    for (int k = 2; k <= 8 && s.cut > 0; ++k) {
-        if (s.steps < 8 * k || s.cut * k > g.slots) break;
-        const int per = uniform((s.steps + k - 1) / k);
-        const int cost = uniform((s.cut * k + at_once - 1) / at_once) * (per + 8) + s.cut * k / join;
-        if (cost < best) best = cost, s.parts = k, s.per = per;
+    if (s.cut > 0 && g.slots > 0) {
+        // Lane k - 1 works out what k parts would take, in steps: rounds of parts with
+        // a part's own cost, the parts' traffic, and the joining one after the other.
+        const int k = threadIdx.x % 64 + 1, per = (s.steps + k - 1) / k;
+        int cost = ((s.cut * k + at_once - 1) / at_once) * (per + part_cost) + (k > 1 ? s.cut * k / join + k / 8 : 0);
+        if (k > 1 && (s.steps < kMinPart * k || s.cut * k > g.slots)) cost = 0x1FFFFFF;
+        int best = (cost < 0x1FFFFFF ? cost : 0x1FFFFFF) * 64 + (k - 1);
+        for (int d = 32; d; d /= 2) {
+            const int other = __shfl_xor(best, d);
+            best = other < best ? other : best;
+        }
+        s.parts = uniform(best % 64 + 1);
+        s.per = uniform((s.steps + s.parts - 1) / s.parts);
     }
     s.units = s.whole + s.cut * s.parts;
     return s;
@@ -425,7 +431,7 @@ __device__ __forceinline__ void product(const Product &g) {
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
     const int wp = wave / WQ, wq = wave % WQ;
-    const Schedule sc = schedule(g, BP, BQ, OpP::kEs, AT_ONCE, JOIN);
+    const Schedule sc = schedule(g, BP, BQ, OpP::kEs, AT_ONCE, JOIN, BF16 ? kPartCost16 : kPartCost32);
     const int64_t nq = g.sums && g.piece_is_q ? piece_rows(g.sums, g.first, g.piece) : g.nq;
     if ((int)blockIdx.x >= sc.units) return;
 
@@ -719,8 +725,8 @@ __global__ void __launch_bounds__(64 * WP * WQ, 2) product_kernel(Product g) {
 // The parts of cut tiles, in order, and what a whole tile's epilogue does. Four
 // rows of a tile to a workgroup.
 template <int EPI>
-__global__ void __launch_bounds__(256) join_kernel(Product g, int bp, int bq, int es, int at_once, int join) {
-    const Schedule s = schedule(g, bp, bq, es, at_once, join);
+__global__ void __launch_bounds__(256) join_kernel(Product g, int bp, int bq, int es, int at_once, int join, int part_cost) {
+    const Schedule s = schedule(g, bp, bq, es, at_once, join, part_cost);
     const int per = bq / 4, tile = blockIdx.x / per;
     if (s.parts == 1 || tile >= s.cut) return;
     const int64_t nq = g.piece_is_q ? piece_rows(g.sums, g.first, g.piece) : g.nq;
@@ -735,6 +741,7 @@ __global__ void __launch_bounds__(256) join_kernel(Product g, int bp, int bq, in
         const int64_t p = (int64_t)tp * bp + pl, left = g.np - p, at = row * g.ldo + p;
         if (left <= 0) return;
         f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 8
         for (int k = 0; k < s.parts; ++k)
             v += *reinterpret_cast<const f32x4 *>(g.parts + ((int64_t)(tile * s.parts + k) * bq + ql) * bp + pl);
 #pragma unroll
@@ -899,13 +906,13 @@ void start_product(const Product &g, int shape, hipStream_t stream) {
     const int64_t tiles = ceil_div(g.np, t.p) * ceil_div(g.nq, t.q);
     const unsigned grid = (unsigned)(g.slots > 0 || tiles > t.at_once ? t.at_once : tiles);
     if constexpr (BF16)
-        if (shape == 0) product_kernel<BF16, EPI, TP, TQ, 256, 256, 2, 4, kTiles[0].at_once, kTiles[0].join><<<grid, 512, 0, stream>>>(g);
-    if (shape == 1) product_kernel<BF16, EPI, TP, TQ, 128, 128, 2, 2, kTiles[1].at_once, kTiles[1].join><<<grid, 256, 0, stream>>>(g);
-    if (shape == 2) product_kernel<BF16, EPI, TP, TQ, 128, 32, 4, 1, kTiles[2].at_once, kTiles[2].join><<<grid, 256, 0, stream>>>(g);
+        if (shape == 0) product_kernel<BF16, EPI, TP, TQ, 256, 256, 2, 4, kTiles[0].at_once, BF16 ? kTiles[0].join : 4 * kTiles[0].join><<<grid, 512, 0, stream>>>(g);
+    if (shape == 1) product_kernel<BF16, EPI, TP, TQ, 128, 128, 2, 2, kTiles[1].at_once, BF16 ? kTiles[1].join : 4 * kTiles[1].join><<<grid, 256, 0, stream>>>(g);
+    if (shape == 2) product_kernel<BF16, EPI, TP, TQ, 128, 32, 4, 1, kTiles[2].at_once, BF16 ? kTiles[2].join : 4 * kTiles[2].join><<<grid, 256, 0, stream>>>(g);
     if constexpr (EPI != kLogits)
         if (g.slots > 0) {
             const int64_t cut = tiles < t.at_once ? tiles : t.at_once - 1;
-            join_kernel<EPI><<<(unsigned)(cut * (t.q / 4)), 256, 0, stream>>>(g, t.p, t.q, BF16 ? 2 : 4, t.at_once, t.join);
+            join_kernel<EPI><<<(unsigned)(cut * (t.q / 4)), 256, 0, stream>>>(g, t.p, t.q, BF16 ? 2 : 4, t.at_once, BF16 ? t.join : 4 * t.join, BF16 ? kPartCost16 : kPartCost32);
         }
 }
 

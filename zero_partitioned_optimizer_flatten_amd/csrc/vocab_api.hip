@@ -143,8 +143,10 @@ namespace {
 
 int64_t round_up(int64_t a, int64_t b) { return ceil_div(a, b) * b; }
 
+constexpr int64_t kMaxSlots = 1024;
+
 // The tile that takes least time: rounds of as many tiles as run at once, by the
-// stages of a tile and about 8 of its epilogue, with a last round cut into parts as
+// stages of a tile and what its epilogue takes, with a last round cut into parts as
 // the kernels' schedule does. A stage of a round takes 1, 0.62 and 0.6 by the tile
 // (bf16): the middle and the small tile multiply at 0.8 and 0.3 of the large one's
 // rate, since they bring 2 and 2.5 times as much to LDS for it (2048 rows of GPT-2's
@@ -157,14 +159,16 @@ int choose_tile(int64_t np, int64_t nq, int64_t steps, bool cut, bool bf16) {
     for (int shape = bf16 ? 0 : 1; shape < 3; ++shape) {
         const TileShape t = kTiles[shape];
         const int64_t tiles = ceil_div(np, t.p) * ceil_div(nq, t.q), rest = tiles % t.at_once;
-        double last = rest > 0 ? (double)(steps + 8) : 0.0;
+        const int64_t part = bf16 ? kPartCost16 : kPartCost32;
+        double last = rest > 0 ? (double)(steps + part) : 0.0;
         if (cut && rest > 0)
-            for (int64_t k = 2; k <= 8 && steps >= 8 * k && rest * k <= 1024; ++k) {
-                const double c = (double)(ceil_div(rest * k, t.at_once) * (ceil_div(steps, k) + 8)) + (double)(rest * k) / t.join;
+            for (int64_t k = 2; k <= kMaxParts && steps >= kMinPart * k && rest * k <= kMaxSlots; ++k) {
+                const double c = (double)(ceil_div(rest * k, t.at_once) * (ceil_div(steps, k) + part) + k / 8)
+                                 + (double)(rest * k) / ((bf16 ? 1 : 4) * t.join);
                 if (c < last) last = c;
             }
         const double unit = shape == 0 ? 1.0 : shape == 1 ? (bf16 ? 0.62 : 0.5) : nq <= 32 ? 0.25 : bf16 ? 0.6 : 0.28;
-        const double cost = unit * ((double)(tiles / t.at_once * (steps + 8)) + last);
+        const double cost = unit * ((double)(tiles / t.at_once * (steps + part)) + last);
         if (least == 0.0 || cost < least) least = cost, best = shape;
     }
     return best;
@@ -191,13 +195,13 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     p.subtiles = round_up(a.vocab, kTiles[p.tile_logits].p) / p.sub;
     p.tile_hidden = choose_tile(a.width, piece, ceil_div(a.vocab, step), true, a.bf16);
     p.tile_table = choose_tile(a.width, a.vocab, ceil_div(piece, step), true, a.bf16);
-    // parts of tiles that do not fill a round, as many as 8 of each
+    // parts of tiles that do not fill a round
     auto slots = [&](int shape, int64_t np, int64_t nq, int64_t steps) -> int {
         const TileShape t = kTiles[shape];
         const int64_t tiles = ceil_div(np, t.p) * ceil_div(nq, t.q);
-        if (steps < 16) return 0;
-        const int64_t n = 8 * (tiles < t.at_once ? tiles : t.at_once);
-        return (int)(n < 1024 ? n : 1024);
+        if (steps < 2 * kMinPart) return 0;
+        const int64_t n = kMaxParts * (tiles < t.at_once ? tiles : t.at_once);
+        return (int)(n < kMaxSlots ? n : kMaxSlots);
     };
     p.slots_hidden = a.grad_hidden ? slots(p.tile_hidden, a.width, piece, ceil_div(a.vocab, step)) : 0;
     p.slots_table = a.grad_table ? slots(p.tile_table, a.width, a.vocab, ceil_div(piece, step)) : 0;

@@ -114,6 +114,10 @@ struct TileShape {
     int join;                     // parts that are joined in the time of a stage
 };
 constexpr TileShape kTiles[] = {{256, 256, 128, 256, 11}, {128, 128, 64, 512, 25}, {128, 32, 32, 768, 55}};
+// A part of a tile: at most kMaxParts of at least kMinPart stages. What it takes
+// besides, in stages, which take several times as long with fp32, where also that
+// many more parts are joined in a stage's time.
+constexpr int kMaxParts = 64, kMinPart = 8, kPartCost16 = 8, kPartCost32 = 2;
 struct HeadPlan {
     int64_t piece, pieces;        // rows of hidden in a piece
     int64_t width_p, vocab_p, piece_p;   // extents padded for the products' long axes
