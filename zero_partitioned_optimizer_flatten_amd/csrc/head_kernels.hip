@@ -120,8 +120,9 @@ __device__ __forceinline__ void idle_row(const HeadArgs &a, float *losses, int64
 
 // One workgroup: the rows that take part, in order, with their targets, and
 // their weights' sum; in small calls also what the others get (idle: the losses)
-// and the rows packed.
-template <bool BF16>
+// and the rows packed. A wave takes kRows * 64 rows at a time, all asked for before
+// the first is used.
+template <bool BF16, int kRows>
 __global__ void __launch_bounds__(1024)
 rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *idle, void *packed, int64_t width_p) {
     __shared__ int32_t found[16];
@@ -131,33 +132,49 @@ rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *id
     int64_t base = 0;
     double weight = 0.0;
     float most = 0.0f;
-    for (int64_t i0 = 0; i0 < a.count; i0 += 1024) {
-        const int64_t i = i0 + threadIdx.x;
-        bool on = false;
-        if (i < a.count) {
-            on = takes_part(a, i);
+    for (int64_t i0 = 0; i0 < a.count; i0 += 1024 * kRows) {
+        const int64_t first = i0 + 64 * kRows * wave + lane;
+        int64_t y[kRows];
+        float w[kRows];
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const int64_t i = first + 64 * k;
+            y[k] = i < a.count ? load_id(a.targets, a.wide_ids, i) : -1;
+            w[k] = !a.weights ? 1.0f : i < a.count ? a.weights[i] : 0.0f;
+        }
+        uint64_t mask[kRows];
+        int mine = 0;
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            const bool on = (uint64_t)y[k] < (uint64_t)a.vocab && w[k] != 0.0f;   // as takes_part()
+            mask[k] = __ballot(on);
+            mine += __popcll(mask[k]);
             if (on) {
-                const float w = a.weights ? a.weights[i] : 1.0f;
-                weight += (double)w;
-                most = fmaxf(most, fabsf(w));
+                weight += (double)w[k];
+                most = fmaxf(most, fabsf(w[k]));
             }
         }
-        const uint64_t mask = __ballot(on);
-        if (lane == 0) found[wave] = __popcll(mask);
+        if (lane == 0) found[wave] = mine;
         __syncthreads();
         int64_t at = base;
-        for (int w = 0; w < 16; ++w) {
-            if (w < wave) at += found[w];
-            base += found[w];
+        for (int x = 0; x < 16; ++x) {
+            if (x < wave) at += found[x];
+            base += found[x];
         }
-        if (on) {
-            at += __popcll(mask & ((1ull << lane) - 1));
-            map[at] = (int32_t)i;
-            target[at] = (int32_t)load_id(a.targets, a.wide_ids, i);
+#pragma unroll
+        for (int k = 0; k < kRows; ++k) {
+            if (mask[k] >> lane & 1) {
+                const int64_t to = at + __popcll(mask[k] & ((1ull << lane) - 1));
+                map[to] = (int32_t)(first + 64 * k);
+                target[to] = (int32_t)y[k];
+            }
+            at += __popcll(mask[k]);
         }
         if (idle)
-            for (int k = 0; k < 64 && i0 + 64 * wave + k < a.count; ++k)
-                if (!(mask >> k & 1)) idle_row(a, idle, i0 + 64 * wave + k, lane);
+#pragma unroll
+            for (int k = 0; k < kRows; ++k)
+                for (int64_t i = first - lane + 64 * k, e = i + 64 < a.count ? i + 64 : a.count, j = i; j < e; ++j)
+                    if (!(mask[k] >> (j - i) & 1)) idle_row(a, idle, j, lane);
         __syncthreads();
     }
     for (int s = 32; s; s /= 2) {
@@ -879,7 +896,9 @@ loss_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, Gradient g, He
                 gradient_chunk<BF16>(g, a.vocab, n, k / per_row, (int64_t)(k % per_row) * V);
     }
     double sum = 0.0;
-    for (int64_t k = threadIdx.x; k < sums->rows; k += 1024) {
+    const int64_t rows_in = sums->rows;
+#pragma unroll 8
+    for (int64_t k = threadIdx.x; k < rows_in; k += 1024) {
         const int64_t i = map[k];
         sum += (a.weights ? (double)a.weights[i] : 1.0) * (double)losses[i];
     }
@@ -934,7 +953,10 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
     const bool pack = p.pieces == 1 && round_up(a.count, 64) * p.width_p <= kSmallCall;
     const bool one = p.pieces == 1 && a.count * p.subtiles <= kSmallCall / 4;
     const bool turn = one && grads && p.piece_p * p.vocab_p <= kSmallCall / 4;
-    rows_kernel<BF16><<<1, 1024, 0, stream>>>(a, sums, map, target, small ? losses : nullptr, pack ? w + p.hidden_off : nullptr, p.width_p);
+    float *idle = small ? losses : nullptr;
+    void *packed = pack ? w + p.hidden_off : nullptr;
+    if (a.count <= 2048) rows_kernel<BF16, 1><<<1, 1024, 0, stream>>>(a, sums, map, target, idle, packed, p.width_p);
+    else rows_kernel<BF16, 8><<<1, 1024, 0, stream>>>(a, sums, map, target, idle, packed, p.width_p);
     if (!small) idle_rows_kernel<<<(unsigned)(a.count < 65536 ? ceil_div(a.count, 4) : 16384), 256, 0, stream>>>(a, losses);
     const void *table = a.table;
     if (p.pack_table) {
