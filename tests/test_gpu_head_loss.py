@@ -68,6 +68,14 @@ def test_head_loss_over_large_tiles(n, vocab, width, dtype):
 
 
 @pytest.mark.parametrize("dtype", [BF, F32])
+@pytest.mark.parametrize("n,vocab,width", [(1, 16640, 128), (3, 16800, 30), (40, 60000, 64), (2, 33000, 129), (9000, 50, 64)])
+def test_few_tiles_of_many_parts(n, vocab, width, dtype):
+    """One tile's long axis is shared out, in parts that do not come out even."""
+    hidden, table, targets, g = make(n, vocab, width, dtype)
+    run(hidden, table, targets)
+
+
+@pytest.mark.parametrize("dtype", [BF, F32])
 def test_more_rows_than_a_grid_has_lines(dtype):
     hidden, table, targets, g = make(70001, 40, 16, dtype, ignored=0.01)
     run(hidden, table, targets)

@@ -228,6 +228,17 @@ def test_head_loss_workspace_covers_every_alignment(L):
     assert ask(1 << 20) - ask(1 << 14) < (1 << 20) * 64
 
 
+@needs_gpp
+def test_parts_of_a_tile_are_never_empty(L):
+    """Cut into about k, every part has a stage and the last one ends with the tile."""
+    per = ctypes.c_int()
+    for steps in [*range(1, 700), 1001, 1875, 4008, 65536]:
+        for k in range(1, 65):
+            parts = L.double_head_parts(steps, k, ctypes.byref(per))
+            assert 1 <= parts <= k
+            assert (parts - 1) * per.value < steps <= parts * per.value, (steps, k)
+
+
 # -------------------------------------------------------------- the binding
 
 class _Tensor(SimpleNamespace):

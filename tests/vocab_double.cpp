@@ -22,6 +22,11 @@ uint32_t double_drop_limit() { return drop.limit; }
 float double_drop_scale() { return drop.scale; }
 int64_t double_head_bytes() { return head.bytes; }
 int64_t double_head_pieces() { return head.pieces; }
+int double_head_parts(int steps, int k, int *per) {
+    const zk::HeadParts h = zk::head_parts(steps, k);
+    *per = h.per;
+    return h.parts;
+}
 
 }
 

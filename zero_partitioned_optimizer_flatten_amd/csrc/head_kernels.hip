@@ -271,18 +271,21 @@ __device__ __forceinline__ Schedule schedule(const Product &g, int bp, int bq, i
     s.parts = 1;
     s.per = s.steps;
     if (s.cut > 0 && g.slots > 0) {
-        // Lane k - 1 works out what k parts would take, in steps: rounds of parts with
-        // a part's own cost, the parts' traffic, and the joining one after the other.
-        const int k = threadIdx.x % 64 + 1, per = (s.steps + k - 1) / k;
-        int cost = ((s.cut * k + at_once - 1) / at_once) * (per + part_cost) + (k > 1 ? s.cut * k / join + k / 8 : 0);
+        // Lane k - 1 works out what about k parts would take, in steps: rounds of parts
+        // with a part's own cost, the parts' traffic, and the joining one after the other.
+        const int wanted = threadIdx.x % 64 + 1;
+        const HeadParts h = head_parts(s.steps, wanted);
+        const int k = h.parts;
+        int cost = ((s.cut * k + at_once - 1) / at_once) * (h.per + part_cost) + (k > 1 ? s.cut * k / join + k / 8 : 0);
         if (k > 1 && (s.steps < kMinPart * k || s.cut * k > g.slots)) cost = 0x1FFFFFF;
-        int best = (cost < 0x1FFFFFF ? cost : 0x1FFFFFF) * 64 + (k - 1);
+        int best = (cost < 0x1FFFFFF ? cost : 0x1FFFFFF) * 64 + (wanted - 1);
         for (int d = 32; d; d /= 2) {
             const int other = __shfl_xor(best, d);
             best = other < best ? other : best;
         }
-        s.parts = uniform(best % 64 + 1);
-        s.per = uniform((s.steps + s.parts - 1) / s.parts);
+        const HeadParts chosen = head_parts(s.steps, best % 64 + 1);
+        s.parts = uniform(chosen.parts);
+        s.per = uniform(chosen.per);
     }
     s.units = s.whole + s.cut * s.parts;
     return s;
@@ -389,7 +392,7 @@ struct Operand {
     // of the other operand, and LDS might hold a NaN.
     template <bool LAST>
     __device__ __forceinline__ void load(uint32_t lds, int wave, int lane, int left, int ld) {
-        const uint32_t bytes = room < 0xFFFFFFFFll ? (uint32_t)room : 0xFFFFFFFFu;
+        const uint32_t bytes = room <= 0 ? 0u : room < 0xFFFFFFFFll ? (uint32_t)room : 0xFFFFFFFFu;
 #pragma unroll
         for (int j = 0; j < LOADS; ++j) {
             int from = at[j];

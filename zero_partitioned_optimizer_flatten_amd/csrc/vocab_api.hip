@@ -162,8 +162,11 @@ int choose_tile(int64_t np, int64_t nq, int64_t steps, bool cut, bool bf16) {
         const int64_t part = bf16 ? kPartCost16 : kPartCost32;
         double last = rest > 0 ? (double)(steps + part) : 0.0;
         if (cut && rest > 0)
-            for (int64_t k = 2; k <= kMaxParts && steps >= kMinPart * k && rest * k <= kMaxSlots; ++k) {
-                const double c = (double)(ceil_div(rest * k, t.at_once) * (ceil_div(steps, k) + part) + k / 8)
+            for (int wanted = 2; wanted <= kMaxParts; ++wanted) {
+                const HeadParts h = head_parts((int)steps, wanted);
+                const int64_t k = h.parts;
+                if (steps < kMinPart * k || rest * k > kMaxSlots) continue;
+                const double c = (double)(ceil_div(rest * k, t.at_once) * (h.per + part) + k / 8)
                                  + (double)(rest * k) / ((bf16 ? 1 : 4) * t.join);
                 if (c < last) last = c;
             }

@@ -118,6 +118,15 @@ constexpr TileShape kTiles[] = {{256, 256, 128, 256, 11}, {128, 128, 64, 512, 25
 // besides, in stages, which take several times as long with fp32, where also that
 // many more parts are joined in a stage's time.
 constexpr int kMaxParts = 64, kMinPart = 8, kPartCost16 = 8, kPartCost32 = 2;
+// Stages of each of about k parts of `steps` stages, the last one's the rest, and
+// how many parts that makes: none is without a stage.
+struct HeadParts {
+    int per, parts;
+};
+__host__ __device__ inline HeadParts head_parts(int steps, int k) {
+    const int per = (steps + k - 1) / k;
+    return {per, per > 0 ? (steps + per - 1) / per : 1};
+}
 struct HeadPlan {
     int64_t piece, pieces;        // rows of hidden in a piece
     int64_t width_p, vocab_p, piece_p;   // extents padded for the products' long axes
