@@ -253,11 +253,11 @@ class _Tensor(SimpleNamespace):
     def numel(self):
         return int(np.prod(self.shape)) if self.shape else 1
 
-    def element_size(self):
-        return self.dtype.itemsize
+    def get_device(self):
+        return self.device.index if self.device.type == "cuda" else -1
 
-    def dim(self):
-        return len(self.shape)
+    def new_empty(self, shape, dtype=None):
+        return tensor((shape,) if isinstance(shape, int) else shape, dtype or self.dtype)
 
     def record_stream(self, s):
         self.used_on.append(s.cuda_stream)
@@ -281,10 +281,9 @@ def binding(monkeypatch):
     fake = SimpleNamespace(zero_embed=took("embed"), zero_embed_grad=took("embed_grad"), zero_dropout=took("dropout"),
                            zero_head_loss=took("head_loss"), zero_embed_grad_workspace=size, zero_head_loss_workspace=size)
     monkeypatch.setattr(vocab, "_lib", lambda: fake)
-    monkeypatch.setattr(vocab, "_stream_handle", lambda s, device: 0)
-    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
-    made = lambda *a, **k: tensor(a[0] if not isinstance(a[0], int) else (a[0],), k.get("dtype") or torch.float32)  # noqa: E731
-    monkeypatch.setattr(vocab.torch, "empty", made)
+    monkeypatch.setattr(vocab, "_raw_stream", lambda index: 0)
+    monkeypatch.setattr(vocab, "_current_device", lambda: 0)
+    monkeypatch.setattr(vocab.torch, "empty_like", lambda x: tensor(x.shape, x.dtype))
     return called
 
 
@@ -329,6 +328,21 @@ def test_binding_refuses(binding, error, call):
     with pytest.raises(error):
         call()
     assert not binding
+
+
+def test_dropout_is_fixed_and_says_what_it_is():
+    d = zero.Dropout(0.25, 7, 9)
+    assert (d.p, d.seed, d.offset, d.counter) == (0.25, 7, 9, None) and "0.25" in repr(d)
+    with pytest.raises(AttributeError):
+        d.p = 0.5
+
+
+def test_signatures_are_the_users():
+    import inspect
+    for f in (zero.embed, zero.embed_grad, zero.dropout, zero.head_loss):
+        names = list(inspect.signature(f).parameters)
+        assert "call" not in names and names[-1] == "stream" and f.__doc__
+    assert list(inspect.signature(zero.embed).parameters)[:2] == ["tokens", "table"]
 
 
 def test_binding_passes_on(binding):

@@ -9,14 +9,21 @@ can be captured in a graph.
 """
 from __future__ import annotations
 
-import contextlib
 import ctypes
-from dataclasses import dataclass
+import functools
+import inspect
 from typing import Optional
 
 import torch
 
-from . import _check, _dtype_code, _stream_handle, _torch_stream, lib
+from . import ZERO_BF16, ZERO_F32, _check, _dtype_code, _raw_stream, _stream_handle, _torch_stream, lib
+
+# Small calls are bound by the host: lookups that it repeats are made once.
+_byref = ctypes.byref
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_DTYPES = {torch.bfloat16: ZERO_BF16, torch.float32: ZERO_F32}
+_ID_BYTES = {torch.int32: 4, torch.int64: 8}
+_WORDS = 1 << 64
 
 
 class _Drop(ctypes.Structure):
@@ -46,166 +53,203 @@ def _lib():
     return L
 
 
-@dataclass(frozen=True)
 class Dropout:
     """Which elements dropout drops: probability p (taken to a multiple of
     2^-16), and the counter-based generator's seed and offset, 64 bits each.
     The forward and the backward call of one place take the same; other steps
     and layers other offsets. counter: one int64 on the device, added to offset
-    when the kernel runs, for steps replayed from a graph."""
-    p: float
-    seed: int
-    offset: int = 0
-    counter: Optional[torch.Tensor] = None
+    when the kernel runs, for steps replayed from a graph. Fixed once made."""
 
-    def _struct(self, device: torch.device) -> _Drop:
-        if not 0 <= self.seed < 1 << 64 or not 0 <= self.offset < 1 << 64:
+    __slots__ = ("_drop", "_counter")
+
+    def __init__(self, p: float, seed: int, offset: int = 0,
+                 counter: Optional[torch.Tensor] = None):
+        if not (0 <= seed < _WORDS and 0 <= offset < _WORDS):
             raise ValueError("seed and offset must be in [0, 2^64)")
-        c = self.counter
-        if c is not None and (c.device != device or c.dtype != torch.int64 or c.numel() != 1):
-            raise ValueError(f"counter must be one int64 on {device}")
-        return _Drop(float(self.p), self.seed, self.offset, None if c is None else c.data_ptr())
+        at = None
+        if counter is not None:
+            if counter.dtype != torch.int64 or counter.numel() != 1 or counter.get_device() < 0:
+                raise ValueError("counter must be one int64 on a cuda device")
+            at = counter.data_ptr()
+        self._counter = counter
+        self._drop = _Drop(p, seed, offset, at)
+
+    p = property(lambda self: self._drop.p)
+    seed = property(lambda self: self._drop.seed)
+    offset = property(lambda self: self._drop.offset)
+    counter = property(lambda self: self._counter)
+
+    def __repr__(self):
+        return f"Dropout(p={self.p}, seed={self.seed}, offset={self.offset}, counter={self._counter})"
 
 
 class _Call:
     """The device and stream of one call, and checks of its tensors."""
 
-    def __init__(self, first: torch.Tensor, what: str, stream):
-        if first.device.type != "cuda":
-            raise ValueError(f"{what} must be on a cuda device, got {first.device}")
-        self.device, self.stream = first.device, stream
-        self.handle = _stream_handle(stream, self.device)
-        self._scopes = None
+    __slots__ = ("index", "stream", "handle")
 
-    def __enter__(self):
-        if self.stream is not None or torch.cuda.current_device() != self.device.index:
-            self._scopes = contextlib.ExitStack()
-            self._scopes.enter_context(torch.cuda.device(self.device))
-            if self.stream is not None:
-                self._scopes.enter_context(
-                    torch.cuda.stream(_torch_stream(self.stream, self.device)))
-        return self
+    def __init__(self, index: int, stream):
+        self.index, self.stream = index, stream
+        if stream is None and _raw_stream is not None:
+            self.handle = _raw_stream(index)
+        else:
+            self.handle = _stream_handle(stream, torch.device("cuda", index))
 
-    def __exit__(self, *exc):
-        if self._scopes is not None:
-            self._scopes.close()
-
-    def ptr(self, x: Optional[torch.Tensor], what: str, dtype=None, shape=None, numel=None):
-        """Address of a contiguous tensor on the call's device; None for None."""
-        if x is None:
-            return None
-        if x.device != self.device:
-            raise ValueError(f"{what} is on {x.device}, the call is on {self.device}")
+    def ptr(self, x: torch.Tensor, what: str, dtype=None, shape=None):
+        """Address of a contiguous tensor on the call's device."""
+        if x.get_device() != self.index:
+            raise ValueError(f"{what} is on {x.device}, the call is on cuda:{self.index}")
         if not x.is_contiguous():
             raise ValueError(f"{what} must be contiguous")
         if dtype is not None and x.dtype != dtype:
             raise TypeError(f"{what} is {x.dtype}, need {dtype}")
         if shape is not None and x.shape != shape:
             raise ValueError(f"{what} has shape {tuple(x.shape)}, need {tuple(shape)}")
-        if numel is not None and x.numel() != numel:
-            raise ValueError(f"{what} has {x.numel()} elements, need {numel}")
         if self.stream is not None:
-            x.record_stream(_torch_stream(self.stream, self.device))
+            x.record_stream(_torch_stream(self.stream, torch.device("cuda", self.index)))
         return x.data_ptr()
 
     def ids(self, x: torch.Tensor, what: str):
         """(address, bytes of an id)"""
-        if x.dtype not in (torch.int32, torch.int64):
+        size = _ID_BYTES.get(x.dtype)
+        if size is None:
             raise TypeError(f"{what} must be int32 or int64, got {x.dtype}")
-        return self.ptr(x, what), x.element_size()
+        return self.ptr(x, what), size
 
     def drop(self, d: Optional[Dropout]):
         if d is None:
             return None
-        if d.counter is not None and self.stream is not None:
-            d.counter.record_stream(_torch_stream(self.stream, self.device))
-        return ctypes.byref(d._struct(self.device))
+        if d._counter is not None:
+            self.ptr(d._counter, "the dropout's counter")
+        return _byref(d._drop)
 
-    def workspace(self, size, *args) -> torch.Tensor:
+    def workspace(self, like: torch.Tensor, size, *args) -> torch.Tensor:
         n = ctypes.c_int64()
-        _check(size(*args, ctypes.byref(n)))
-        return torch.empty(n.value, dtype=torch.uint8, device=self.device)
+        rc = size(*args, _byref(n))
+        if rc:
+            _check(rc)
+        return like.new_empty(n.value, dtype=torch.uint8)
+
+
+def _call(function):
+    """The function of (call, tensor, ...) as one of (tensor, ..., stream=None):
+    on the first tensor's device and the stream given, or its current one."""
+
+    @functools.wraps(function)
+    def call(first, *args, stream=None, **kwargs):
+        index = first.get_device()
+        if index < 0:
+            raise ValueError(f"{function.__name__} runs on a cuda device, got a tensor on {first.device}")
+        c = _Call(index, stream)
+        if stream is None and index == _current_device():
+            return function(c, first, *args, **kwargs)
+        with torch.cuda.device(index), torch.cuda.stream(
+                None if stream is None else _torch_stream(stream, torch.device("cuda", index))):
+            return function(c, first, *args, **kwargs)
+
+    s = inspect.signature(function)
+    p = list(s.parameters.values())[1:]
+    p.append(inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None))
+    call.__signature__ = s.replace(parameters=p)
+    return call
+
+
+def _code(dtype: torch.dtype) -> int:
+    code = _DTYPES.get(dtype)
+    return _dtype_code(dtype) if code is None else code
 
 
 def _table(x: torch.Tensor, what: str):
-    if x.dim() != 2:
-        raise ValueError(f"{what} must have two dimensions, got {tuple(x.shape)}")
-    return x.shape
+    shape = x.shape
+    if len(shape) != 2:
+        raise ValueError(f"{what} must have two dimensions, got {tuple(shape)}")
+    return shape
 
 
-def embed(tokens: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0,
+@_call
+def embed(call, tokens: torch.Tensor, table: torch.Tensor, *, scale: float = 1.0,
           positions: Optional[torch.Tensor] = None, position_table: Optional[torch.Tensor] = None,
           dropout: Optional[Dropout] = None, out: Optional[torch.Tensor] = None,
-          dtype: Optional[torch.dtype] = None, stream=None) -> torch.Tensor:
+          dtype: Optional[torch.dtype] = None) -> torch.Tensor:
     """dropout(scale * table[tokens] + position_table[positions]), of shape
     tokens.shape + (width,). Ids outside a table give a row of zeros. The
     result is `out`, or a new tensor of `dtype` (the table's by default)."""
     rows, width = _table(table, "table")
     if (positions is None) != (position_table is None):
         raise ValueError("positions and position_table come together")
-    with _Call(tokens, "tokens", stream) as c:
-        shape = (*tokens.shape, width)
-        if out is None:
-            out = torch.empty(shape, dtype=dtype or table.dtype, device=c.device)
-        elif dtype is not None and out.dtype != dtype:
-            raise TypeError(f"out is {out.dtype}, dtype asks for {dtype}")
-        ids, size = c.ids(tokens, "tokens")
-        pos = ptable = None
-        prows = 0
-        if positions is not None:
-            if _table(position_table, "position_table")[1] != width:
-                raise ValueError("table and position_table differ in width")
-            pos = c.ptr(positions, "positions", tokens.dtype, tokens.shape)
-            ptable = c.ptr(position_table, "position_table", table.dtype)
-            prows = position_table.shape[0]
-        _check(_lib().zero_embed(ids, size, tokens.numel(), c.ptr(table, "table"), rows, width,
-                                 _dtype_code(table.dtype), float(scale), pos, ptable, prows,
-                                 c.drop(dropout), c.ptr(out, "out", shape=shape),
-                                 _dtype_code(out.dtype), c.handle))
+    ids, size = call.ids(tokens, "tokens")
+    at, shape = call.ptr(table, "table"), tokens.shape + (width,)
+    code = _code(table.dtype)
+    pos = ptable = None
+    prows = 0
+    if positions is not None:
+        prows, pwidth = _table(position_table, "position_table")
+        if pwidth != width:
+            raise ValueError("table and position_table differ in width")
+        pos = call.ptr(positions, "positions", tokens.dtype, tokens.shape)
+        ptable = call.ptr(position_table, "position_table", table.dtype)
+    if out is None:
+        out = table.new_empty(shape) if dtype is None else table.new_empty(shape, dtype=dtype)
+        to = out.data_ptr()
+    else:
+        to = call.ptr(out, "out", dtype, shape)
+    rc = _lib().zero_embed(ids, size, tokens.numel(), at, rows, width, code, scale, pos, ptable,
+                           prows, call.drop(dropout), to,
+                           code if out.dtype == table.dtype else _code(out.dtype), call.handle)
+    if rc:
+        _check(rc)
     return out
 
 
-def embed_grad(grad_out: torch.Tensor, tokens: torch.Tensor, grad_table: torch.Tensor, *,
-               scale: float = 1.0, dropout: Optional[Dropout] = None, accumulate: bool = False,
-               stream=None) -> torch.Tensor:
+@_call
+def embed_grad(call, grad_out: torch.Tensor, tokens: torch.Tensor, grad_table: torch.Tensor, *,
+               scale: float = 1.0, dropout: Optional[Dropout] = None,
+               accumulate: bool = False) -> torch.Tensor:
     """The gradient of embed's table, written into grad_table (rows, width), a
     view of a flat gradient vector for instance, or added to the rows that
     tokens name. The gradient of its position table is embed_grad(grad_out,
     positions, grad_position_table, dropout=dropout)."""
     rows, width = _table(grad_table, "grad_table")
-    with _Call(tokens, "tokens", stream) as c:
-        n = tokens.numel()
-        L = _lib()
-        ids, size = c.ids(tokens, "tokens")
-        g = c.ptr(grad_out, "grad_out", numel=n * width)
-        t = c.ptr(grad_table, "grad_table")
-        gdt, tdt = _dtype_code(grad_out.dtype), _dtype_code(grad_table.dtype)
-        ws = c.workspace(L.zero_embed_grad_workspace, n, rows, width)
-        _check(L.zero_embed_grad(g, gdt, ids, size, n, rows, width, float(scale), c.drop(dropout),
-                                 t, tdt, int(bool(accumulate)), ws.data_ptr(), ws.numel(),
-                                 c.handle))
+    n, L = tokens.numel(), _lib()
+    if grad_out.numel() != n * width:
+        raise ValueError(f"grad_out has {grad_out.numel()} elements, need {n * width}")
+    ids, size = call.ids(tokens, "tokens")
+    g, t = call.ptr(grad_out, "grad_out"), call.ptr(grad_table, "grad_table")
+    gdt, tdt = _code(grad_out.dtype), _code(grad_table.dtype)
+    ws = call.workspace(grad_out, L.zero_embed_grad_workspace, n, rows, width)
+    rc = L.zero_embed_grad(g, gdt, ids, size, n, rows, width, scale, call.drop(dropout), t, tdt,
+                           bool(accumulate), ws.data_ptr(), ws.numel(), call.handle)
+    if rc:
+        _check(rc)
     return grad_table
 
 
-def dropout(x: torch.Tensor, drop: Dropout, *, add: Optional[torch.Tensor] = None,
-            out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+@_call
+def dropout(call, x: torch.Tensor, drop: Dropout, *, add: Optional[torch.Tensor] = None,
+            out: Optional[torch.Tensor] = None) -> torch.Tensor:
     """dropout(x), plus `add` if given; dropout(grad, drop) is its backward.
     out may be x or add."""
-    with _Call(x, "x", stream) as c:
-        if out is None:
-            out = torch.empty_like(x, memory_format=torch.contiguous_format)
-        _check(_lib().zero_dropout(c.ptr(x, "x"), c.ptr(add, "add", x.dtype, x.shape),
-                                   c.ptr(out, "out", x.dtype, x.shape), x.numel(),
-                                   _dtype_code(x.dtype), c.drop(drop), c.handle))
+    at = call.ptr(x, "x")
+    code = _code(x.dtype)
+    residual = None if add is None else call.ptr(add, "add", x.dtype, x.shape)
+    if out is None:
+        out = torch.empty_like(x)
+        to = out.data_ptr()
+    else:
+        to = call.ptr(out, "out", x.dtype, x.shape)
+    rc = _lib().zero_dropout(at, residual, to, x.numel(), code, call.drop(drop), call.handle)
+    if rc:
+        _check(rc)
     return out
 
 
-def head_loss(hidden: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, *,
+@_call
+def head_loss(call, hidden: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, *,
               weights: Optional[torch.Tensor] = None, reduction: str = "mean",
               grad_scale: float = 1.0, losses: Optional[torch.Tensor] = None,
               grad_hidden: Optional[torch.Tensor] = None,
               grad_table: Optional[torch.Tensor] = None, accumulate: bool = False,
-              piece_rows: int = 0, stream=None) -> torch.Tensor:
+              piece_rows: int = 0) -> torch.Tensor:
     """Softmax cross entropy of hidden (..., width) against table (vocab,
     width) at targets (...), as one float32 on the device: the sum over rows of
     weight times loss, divided by the sum of the weights with "mean". Rows
@@ -218,24 +262,24 @@ def head_loss(hidden: torch.Tensor, table: torch.Tensor, targets: torch.Tensor, 
     if reduction not in ("mean", "sum"):
         raise ValueError(f"reduction must be 'mean' or 'sum', got {reduction!r}")
     vocab, width = _table(table, "table")
-    with _Call(hidden, "hidden", stream) as c:
-        L, n = _lib(), targets.numel()
-        if hidden.shape != (*targets.shape, width):
-            raise ValueError(f"hidden has shape {tuple(hidden.shape)}, need "
-                             f"{(*targets.shape, width)}")
-        ids, size = c.ids(targets, "targets")
-        h, t = c.ptr(hidden, "hidden"), c.ptr(table, "table", hidden.dtype)
-        w = c.ptr(weights, "weights", torch.float32, targets.shape)
-        ls = c.ptr(losses, "losses", torch.float32, targets.shape)
-        gh = c.ptr(grad_hidden, "grad_hidden", hidden.dtype, hidden.shape)
-        gt = c.ptr(grad_table, "grad_table", shape=table.shape)
-        dt = _dtype_code(hidden.dtype)
-        gdt = dt if grad_table is None else _dtype_code(grad_table.dtype)
-        ws = c.workspace(L.zero_head_loss_workspace, n, vocab, width, dt, int(gh is not None),
-                         int(gt is not None), gdt, int(piece_rows))
-        loss = torch.empty(1, dtype=torch.float32, device=c.device)
-        _check(L.zero_head_loss(h, t, dt, ids, size, n, vocab, width, w, int(reduction == "mean"),
-                                float(grad_scale), loss.data_ptr(), ls, gh, gt, gdt,
-                                int(bool(accumulate)), int(piece_rows), ws.data_ptr(), ws.numel(),
-                                c.handle))
+    L, n, shape = _lib(), targets.numel(), targets.shape
+    if hidden.shape != shape + (width,):
+        raise ValueError(f"hidden has shape {tuple(hidden.shape)}, need {(*shape, width)}")
+    ids, size = call.ids(targets, "targets")
+    h, t = call.ptr(hidden, "hidden"), call.ptr(table, "table", hidden.dtype)
+    dt = _code(hidden.dtype)
+    w = None if weights is None else call.ptr(weights, "weights", torch.float32, shape)
+    ls = None if losses is None else call.ptr(losses, "losses", torch.float32, shape)
+    gh = None if grad_hidden is None else call.ptr(grad_hidden, "grad_hidden", hidden.dtype, hidden.shape)
+    gt, gdt = None, dt
+    if grad_table is not None:
+        gt, gdt = call.ptr(grad_table, "grad_table", None, table.shape), _code(grad_table.dtype)
+    ws = call.workspace(hidden, L.zero_head_loss_workspace, n, vocab, width, dt, gh is not None,
+                        gt is not None, gdt, piece_rows)
+    loss = hidden.new_empty(1, dtype=torch.float32)
+    rc = L.zero_head_loss(h, t, dt, ids, size, n, vocab, width, w, reduction == "mean", grad_scale,
+                          loss.data_ptr(), ls, gh, gt, gdt, bool(accumulate), piece_rows,
+                          ws.data_ptr(), ws.numel(), call.handle)
+    if rc:
+        _check(rc)
     return loss
