@@ -351,3 +351,13 @@ def test_binding_passes_on(binding):
     zero.dropout(tensor((3, 4)), zero.Dropout(0.1, 1), out=tensor((3, 4)))
     zero.head_loss(tensor((2, 3, 4)), tensor((5, 4)), tensor((2, 3), I64))
     assert binding == ["embed", "embed_grad", "dropout", "head_loss"]
+
+
+def test_binding_takes_every_argument_by_name(binding):
+    zero.embed(table=tensor((5, 4)), tokens=tensor((2, 3), I64))
+    zero.embed_grad(tokens=tensor((2, 3), I64), grad_table=tensor((5, 4)), grad_out=tensor((2, 3, 4)))
+    zero.dropout(drop=zero.Dropout(0.1, 1), x=tensor((3, 4)))
+    zero.head_loss(targets=tensor((2, 3), I64), hidden=tensor((2, 3, 4)), table=tensor((5, 4)))
+    assert binding == ["embed", "embed_grad", "dropout", "head_loss"]
+    with pytest.raises(TypeError, match="needs tokens"):
+        zero.embed(table=tensor((5, 4)))

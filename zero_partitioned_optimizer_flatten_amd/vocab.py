@@ -135,22 +135,26 @@ def _call(function):
     """The function of (call, tensor, ...) as one of (tensor, ..., stream=None):
     on the first tensor's device and the stream given, or its current one."""
 
+    s = inspect.signature(function)
+    p = list(s.parameters.values())[1:]
+
     @functools.wraps(function)
-    def call(first, *args, stream=None, **kwargs):
+    def call(*args, stream=None, **kwargs):
+        first = args[0] if args else kwargs.get(p[0].name)
+        if first is None:
+            raise TypeError(f"{function.__name__} needs {p[0].name}")
         index = first.get_device()
         if index < 0:
             raise ValueError(f"{function.__name__} runs on a cuda device, got a tensor on {first.device}")
         c = _Call(index, stream)
         if stream is None and index == _current_device():
-            return function(c, first, *args, **kwargs)
+            return function(c, *args, **kwargs)
         with torch.cuda.device(index), torch.cuda.stream(
                 None if stream is None else _torch_stream(stream, torch.device("cuda", index))):
-            return function(c, first, *args, **kwargs)
+            return function(c, *args, **kwargs)
 
-    s = inspect.signature(function)
-    p = list(s.parameters.values())[1:]
-    p.append(inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None))
-    call.__signature__ = s.replace(parameters=p)
+    call.__signature__ = s.replace(parameters=[
+        *p, inspect.Parameter("stream", inspect.Parameter.KEYWORD_ONLY, default=None)])
     return call
 
 
