@@ -140,6 +140,23 @@ def test_embed_grad(grad_dtype, table_dtype, count, rows, width, gap, p, how):
         assert torch.equal(again.view(torch.uint8), t.view(torch.uint8))
 
 
+@pytest.mark.parametrize("count", [1, 7, 8, 9, 63, 64, 65, 255, 256, 257])
+@pytest.mark.parametrize("how", ["same", "half", "outside"])
+def test_embed_grad_of_few_tokens(count, how):
+    """Runs shorter and longer than one wave takes, up to the whole batch."""
+    rows, width = 300, 520
+    g = gen(count)
+    tokens = tokens_of(how, count, rows, g)
+    grad = torch.randn(count, width, generator=g).to(BF)
+    old = torch.randn(rows, width, generator=g).to(BF)
+    for accumulate in (False, True):
+        flat, t = placed(old, 3)
+        zero.embed_grad(grad.cuda(), tokens.cuda(), t, dropout=zero.Dropout(0.2, 5), accumulate=accumulate)
+        want, bound = ref.embed_grad(grad, tokens, rows, 1.0, (0.2, 5, 0), old if accumulate else None)
+        ref.check(t, want, bound, accumulate, BF)
+        assert untouched(flat, 3, rows * width)
+
+
 def test_embed_grad_without_tokens():
     empty, old = torch.empty(0, dtype=torch.int64, device="cuda"), torch.ones(300, 5, device="cuda")
     g = torch.empty(0, 5, device="cuda")

@@ -128,10 +128,11 @@ EmbedGradPlan plan_embed_grad(int64_t count, int64_t rows, int64_t width) {
     // About 1024 spans, and at most 256 tokens in one: few partial rows for a
     // run that is the whole batch, enough waves for short batches. Few tokens
     // have a wave for each run, and no joining follows (span 1).
-    const int64_t span = count / 1024;
-    p.span = count <= kRunTokens ? 1 : (int)(span < 8 ? 8 : span > 256 ? 256 : span);
+    const int64_t span = count / 1024, chunks = ceil_div(width, kSpanCols);
+    const bool runs = count <= kRunTokens && count * chunks < (int64_t)1 << 22;     // a dispatch's limit
+    p.span = runs ? 1 : (int)(span < 8 ? 8 : span > 256 ? 256 : span);
     p.spans = ceil_div(count, p.span);
-    const int64_t pitch = ceil_div(width, kSpanCols) * kSpanCols;
+    const int64_t pitch = chunks * kSpanCols;
     p.count_off = 0;
     p.sorted_off = 256;
     p.partial_off = p.sorted_off + ceil_div(count * (int64_t)sizeof(SortedToken), 256) * 256;

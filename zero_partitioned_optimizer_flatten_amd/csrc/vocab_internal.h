@@ -62,8 +62,9 @@ struct EmbedGradPlan {
     int64_t spans;
     int64_t sorted_off, count_off, partial_off, bytes;   // workspace layout
 };
-// Up to so many tokens the sums go by runs.
-constexpr int kRunTokens = 128;
+// Up to so many tokens the sums go by runs: 128 tokens of 768 columns take 8.1 us for
+// 12.5 by spans, 9.8 for 11.4 if they are one id; 256 take 8.4 for 12.8, and 13.2 for 12.
+constexpr int kRunTokens = 256;
 // Columns of one wave in the sums.
 constexpr int kSpanCols = 512;
 EmbedGradPlan plan_embed_grad(int64_t count, int64_t rows, int64_t width);
@@ -107,7 +108,7 @@ struct HeadRow {
     float target;                 // z_y * log2(e)
 };
 // Tiles of the products: rows of P and of Q, rows of P to a wave, and workgroups
-// that run at a time: one, two or four on each of 256 compute units, as LDS lets
+// that run at a time: one, two or three on each of 256 compute units, as LDS lets
 // them.
 struct TileShape {
     int p, q, sub, at_once;

@@ -144,35 +144,27 @@ __device__ __forceinline__ void drop(const Drop &d, uint64_t offset, uint64_t fi
     }
 }
 
-// 16 bytes of output to a lane at a time, whole lines to a wave; PER of them to a
-// thread, all asked for before the first is used.
-template <bool BF16, bool ADD, int PER, bool NT>
+// 16 bytes of output to a lane. Bound by memory: 2^28 bf16 elements take 168 us
+// (1.07 GB, 6.4 TB/s; the random numbers' 20 wide products for 8 elements hide
+// behind it). Two and four vectors to a thread, all asked for before the first is
+// used, took 178 and 180 us: waves enough are under way without.
+template <bool BF16, bool ADD, bool NT>
 __global__ void __launch_bounds__(kThreads) dropout_kernel(DropoutArgs a) {
     constexpr int V = BF16 ? 8 : 4;
-    const int64_t first = ((int64_t)blockIdx.x * (kThreads * PER) + threadIdx.x) * V;
-    Raw<BF16, V> x[PER], r[PER];
+    const int64_t at = ((int64_t)blockIdx.x * kThreads + threadIdx.x) * V, left = a.count - at;
+    if (left <= 0) return;
+    Raw<BF16, V> x, r;
+    float v[V], w[V];
+    x.load(a.x, at, left);
+    if (ADD) r.load(a.add, at, left);
+    x.get(v);
+    drop<true, V>(a.drop, drop_offset(a.drop), (uint64_t)at, v);
+    if (ADD) {
+        r.get(w);
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int64_t at = first + (int64_t)k * kThreads * V, left = a.count - at;
-        if (left <= 0) break;
-        x[k].load(a.x, at, left);
-        if (ADD) r[k].load(a.add, at, left);
+        for (int c = 0; c < V; ++c) v[c] += w[c];
     }
-    const uint64_t offset = drop_offset(a.drop);
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const int64_t at = first + (int64_t)k * kThreads * V, left = a.count - at;
-        if (left <= 0) break;
-        float v[V], w[V];
-        x[k].get(v);
-        drop<true, V>(a.drop, offset, (uint64_t)at, v);
-        if (ADD) {
-            r[k].get(w);
-#pragma unroll
-            for (int c = 0; c < V; ++c) v[c] += w[c];
-        }
-        store<BF16, V, NT>(a.out, at, left, v);
-    }
+    store<BF16, V, NT>(a.out, at, left, v);
 }
 
 // -------------------------------------------------------------- lookup
@@ -181,51 +173,37 @@ __device__ __forceinline__ int64_t load_id(const void *ids, bool wide, int64_t i
     return wide ? static_cast<const int64_t *>(ids)[i] : (int64_t) static_cast<const int32_t *>(ids)[i];
 }
 
-// 16 bytes of an output row to a lane, PER to a thread: the ids of all, then the
-// rows of all, are asked for before the first is used.
-template <bool TBF, bool OBF, bool POS, bool DROP, bool ALIGNED, int PER, bool NT>
+// 16 bytes of an output row to a lane. Bound by memory: 20480 rows of 4096 bf16
+// take 47.4 us (2 x 168 MB, many of the rows read from caches: 7.1 TB/s); with four
+// vectors to a thread 50.0.
+template <bool TBF, bool OBF, bool POS, bool DROP, bool ALIGNED, bool NT>
 __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a, uint32_t per_row) {
     constexpr int V = OBF ? 8 : 4;
-    int64_t id[PER], pos[PER];
-    uint32_t row[PER], chunk[PER];
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        const uint32_t unit = blockIdx.x * (kThreads * PER) + k * kThreads + threadIdx.x;   // below 2^32
-        row[k] = unit / per_row;
-        chunk[k] = unit - row[k] * per_row;
-        if (row[k] >= a.count) break;
-        id[k] = load_id(a.ids, a.wide_ids, row[k]);
-        if (POS) pos[k] = load_id(a.pos_ids, a.wide_ids, row[k]);
+    const uint32_t unit = blockIdx.x * kThreads + threadIdx.x;      // below 2^32
+    const uint32_t row = unit / per_row;
+    if (row >= a.count) return;
+    const int64_t col = (int64_t)(unit - row * per_row) * V, left = a.width - col;
+    const int64_t id = load_id(a.ids, a.wide_ids, row);
+    const int64_t pos = POS ? load_id(a.pos_ids, a.wide_ids, row) : -1;
+    Raw<TBF, V> x, r;
+    if ((uint64_t)id < (uint64_t)a.rows) x.load(a.table, id * a.width + col, left);
+    else x.clear();
+    if (POS) {
+        if ((uint64_t)pos < (uint64_t)a.pos_rows) r.load(a.pos_table, pos * a.width + col, left);
+        else r.clear();
     }
-    Raw<TBF, V> x[PER], r[PER];
+    float v[V], w[V];
+    x.get(v);
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        if (row[k] >= a.count) break;
-        const int64_t col = (int64_t)chunk[k] * V, left = a.width - col;
-        if ((uint64_t)id[k] < (uint64_t)a.rows) x[k].load(a.table, id[k] * a.width + col, left);
-        else x[k].clear();
-        if (POS) {
-            if ((uint64_t)pos[k] < (uint64_t)a.pos_rows) r[k].load(a.pos_table, pos[k] * a.width + col, left);
-            else r[k].clear();
-        }
+    for (int c = 0; c < V; ++c) v[c] *= a.scale;
+    if (POS) {
+        r.get(w);
+#pragma unroll
+        for (int c = 0; c < V; ++c) v[c] += w[c];
     }
-    const uint64_t offset = DROP ? drop_offset(a.drop) : 0;
-#pragma unroll
-    for (int k = 0; k < PER; ++k) {
-        if (row[k] >= a.count) break;
-        const int64_t col = (int64_t)chunk[k] * V, at = (int64_t)row[k] * a.width + col;
-        float v[V], w[V];
-        x[k].get(v);
-#pragma unroll
-        for (int c = 0; c < V; ++c) v[c] *= a.scale;
-        if (POS) {
-            r[k].get(w);
-#pragma unroll
-            for (int c = 0; c < V; ++c) v[c] += w[c];
-        }
-        if (DROP) drop<ALIGNED, V>(a.drop, offset, (uint64_t)at, v);
-        store<OBF, V, NT>(a.out, at, a.width - col, v);
-    }
+    const int64_t at = (int64_t)row * a.width + col;
+    if (DROP) drop<ALIGNED, V>(a.drop, drop_offset(a.drop), (uint64_t)at, v);
+    store<OBF, V, NT>(a.out, at, left, v);
 }
 
 // ------------------------------------------- gradient: tokens, sorted
@@ -381,9 +359,7 @@ __device__ __forceinline__ void write_row(const EmbedGradArgs &a, int32_t id, in
     store<OBF>(a.out, (int64_t)id * a.width + col, left, v);
 }
 
-// RUNS, for few tokens: a span is a run, whatever its length, and the waves of
-// the other tokens have nothing to do.
-template <bool GBF, bool OBF, bool DROP, bool ALIGNED, bool RUNS>
+template <bool GBF, bool OBF, bool DROP, bool ALIGNED>
 __global__ void __launch_bounds__(kThreads)
 span_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, int span,
             int col_chunks, float *partial, int64_t pitch) {
@@ -394,11 +370,7 @@ span_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, in
     const int n = __builtin_amdgcn_readfirstlane(*total);
     int64_t lo = (int64_t)s * span;
     if (lo >= n) return;
-    int64_t hi = lo + span < n ? lo + span : n;
-    if (RUNS) {
-        if (__builtin_amdgcn_readfirstlane(sorted[lo].begin) != lo) return;
-        hi = __builtin_amdgcn_readfirstlane(sorted[lo].end);
-    }
+    const int64_t hi = lo + span < n ? lo + span : n;
     const int64_t left = a.width - col;
     const uint64_t offset = DROP ? drop_offset(a.drop) : 0;
     float sum[kVec];
@@ -453,6 +425,62 @@ span_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, in
     }
 }
 
+// For few tokens, where a joining kernel would take as long as the sums: workgroup
+// (token, columns) adds up the run that begins at the token. Its rows are dealt to
+// the waves in stretches, joined in order; a short run is the first wave's.
+constexpr int kRunWaves = 8;
+
+template <bool GBF, bool OBF, bool DROP>
+__global__ void __launch_bounds__(64 * kRunWaves)
+run_kernel(EmbedGradArgs a, const SortedToken *sorted, const int32_t *total, int col_chunks) {
+    __shared__ __align__(16) float sums[kRunWaves][kSpanCols];
+    const int s = __builtin_amdgcn_readfirstlane(blockIdx.x / (uint32_t)col_chunks);
+    if (s >= *total) return;                       // the whole workgroup, as below
+    const SortedToken t = sorted[s];
+    if (t.begin != s) return;
+    const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+    const int64_t col = (int64_t)(blockIdx.x - (uint32_t)s * col_chunks) * kSpanCols + lane * kVec, left = a.width - col;
+    const int end = __builtin_amdgcn_readfirstlane(t.end), length = end - s;
+    const bool split = length > kSpanBatch;
+    const int each = split ? (length + kRunWaves - 1) / kRunWaves : length;
+    const int lo = s + each * wave, hi = lo + each < end ? lo + each : end;
+    const uint64_t offset = DROP ? drop_offset(a.drop) : 0;
+    Raw<OBF> old;
+    old.clear();
+    if (a.accumulate && wave == 0 && left > 0) old.load(a.out, (int64_t)t.id * a.width + col, left);
+    float sum[kVec];
+#pragma unroll
+    for (int k = 0; k < kVec; ++k) sum[k] = 0.0f;
+    for (int k0 = lo; k0 < hi; k0 += kSpanBatch) {
+        Raw<GBF> raw[kSpanBatch];
+        int row[kSpanBatch];
+#pragma unroll
+        for (int k = 0; k < kSpanBatch; ++k) row[k] = sorted[k0 + k < hi ? k0 + k : hi - 1].row;
+#pragma unroll
+        for (int k = 0; k < kSpanBatch; ++k)
+            if (left > 0) raw[k].load(a.grad_out, (int64_t)row[k] * a.width + col, left);
+#pragma unroll
+        for (int k = 0; k < kSpanBatch; ++k) {
+            if (k0 + k >= hi || left <= 0) break;
+            float v[kVec];
+            raw[k].get(v);
+            if (DROP) drop<false>(a.drop, offset, (uint64_t)row[k] * a.width + col, v);
+#pragma unroll
+            for (int c = 0; c < kVec; ++c) sum[c] += v[c];
+        }
+    }
+    if (split) {
+        __builtin_memcpy(&sums[wave][lane * kVec], sum, sizeof sum);
+        __syncthreads();
+    }
+    if (wave != 0) return;
+    if (split)
+        for (int w = 1; w < kRunWaves; ++w)
+#pragma unroll
+            for (int k = 0; k < kVec; ++k) sum[k] += sums[w][lane * kVec + k];
+    write_row<OBF>(a, t.id, col, sum, old);
+}
+
 // Workgroup (span, columns): the run that begins in the span and goes over its
 // end. Its spans are dealt to the workgroup's waves in stretches, joined in order.
 constexpr int kJoinWaves = 4;
@@ -501,21 +529,18 @@ static_assert(kSpanCols == 64 * kVec, "a vector to a lane");
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Vectors to a thread: one while that leaves the device short of work; else four,
-// to have enough bytes on their way, and stores past the caches, which then keep
-// what is read.
-constexpr int64_t kFewVectors = (int64_t)256 * 2048;      // a thread each on every compute unit
+// An output of more bytes is stored past the caches, which then keep what is read
+// (2^24 bf16 dropped 11.7 us for 14.2, 20480 rows of 4096 looked up 47.4 for 57.4);
+// a smaller one (2^22: 4.9 either way) stays where its reader finds it.
+constexpr int64_t kCachedBytes = (int64_t)8 << 20;
 
 template <bool TBF, bool OBF, bool POS, bool DROP, bool ALIGNED>
 void start_embed(const EmbedArgs &a, hipStream_t stream) {
     const uint32_t per_row = (uint32_t)ceil_div(a.width, OBF ? 8 : 4);
     const int64_t units = a.count * per_row;
-    if (units <= kFewVectors)
-        embed_kernel<TBF, OBF, POS, DROP, ALIGNED, 1, false>
-            <<<dim3((unsigned)ceil_div(units, kThreads)), kThreads, 0, stream>>>(a, per_row);
-    else
-        embed_kernel<TBF, OBF, POS, DROP, ALIGNED, 4, true>
-            <<<dim3((unsigned)ceil_div(units, kThreads * 4)), kThreads, 0, stream>>>(a, per_row);
+    const dim3 grid((unsigned)ceil_div(units, kThreads));
+    if (16 * units <= kCachedBytes) embed_kernel<TBF, OBF, POS, DROP, ALIGNED, false><<<grid, kThreads, 0, stream>>>(a, per_row);
+    else embed_kernel<TBF, OBF, POS, DROP, ALIGNED, true><<<grid, kThreads, 0, stream>>>(a, per_row);
 }
 
 template <bool TBF, bool OBF, bool POS>
@@ -528,10 +553,9 @@ void start_embed(const EmbedArgs &a, hipStream_t stream) {
 template <bool BF16, bool ADD>
 void start_dropout(const DropoutArgs &a, hipStream_t stream) {
     const int64_t units = ceil_div(a.count, BF16 ? 8 : 4);
-    if (units <= kFewVectors)
-        dropout_kernel<BF16, ADD, 1, false><<<dim3((unsigned)ceil_div(units, kThreads)), kThreads, 0, stream>>>(a);
-    else
-        dropout_kernel<BF16, ADD, 4, true><<<dim3((unsigned)ceil_div(units, kThreads * 4)), kThreads, 0, stream>>>(a);
+    const dim3 grid((unsigned)ceil_div(units, kThreads));
+    if (16 * units <= kCachedBytes) dropout_kernel<BF16, ADD, false><<<grid, kThreads, 0, stream>>>(a);
+    else dropout_kernel<BF16, ADD, true><<<grid, kThreads, 0, stream>>>(a);
 }
 
 template <bool GBF, bool OBF>
@@ -539,19 +563,20 @@ void start_spans(const EmbedGradArgs &a, const EmbedGradPlan &p, const SortedTok
                  const int32_t *total, float *partial, hipStream_t stream) {
     const int chunks = (int)ceil_div(a.width, kSpanCols);
     const int64_t pitch = (int64_t)chunks * kSpanCols;
-    const dim3 grid((unsigned)ceil_div(p.spans * chunks, kThreads / 64));
-    const bool aligned = a.width % kVec == 0;
-#define ZERO_SPANS(DROP, ALIGNED, RUNS)                                      \
-    span_kernel<GBF, OBF, DROP, ALIGNED, RUNS><<<grid, kThreads, 0, stream>>>( \
-        a, sorted, total, p.span, chunks, partial, pitch)
     if (p.span == 1) {
-        if (a.drop.limit == 0) ZERO_SPANS(false, true, true);
-        else ZERO_SPANS(true, false, true);
+        const dim3 grid((unsigned)(a.count * chunks));
+        if (a.drop.limit == 0) run_kernel<GBF, OBF, false><<<grid, 64 * kRunWaves, 0, stream>>>(a, sorted, total, chunks);
+        else run_kernel<GBF, OBF, true><<<grid, 64 * kRunWaves, 0, stream>>>(a, sorted, total, chunks);
         return;
     }
-    if (a.drop.limit == 0) ZERO_SPANS(false, true, false);
-    else if (aligned) ZERO_SPANS(true, true, false);
-    else ZERO_SPANS(true, false, false);
+    const dim3 grid((unsigned)ceil_div(p.spans * chunks, kThreads / 64));
+    const bool aligned = a.width % kVec == 0;
+#define ZERO_SPANS(DROP, ALIGNED)                                      \
+    span_kernel<GBF, OBF, DROP, ALIGNED><<<grid, kThreads, 0, stream>>>( \
+        a, sorted, total, p.span, chunks, partial, pitch)
+    if (a.drop.limit == 0) ZERO_SPANS(false, true);
+    else if (aligned) ZERO_SPANS(true, true);
+    else ZERO_SPANS(true, false);
 #undef ZERO_SPANS
     if (p.spans > 1)
         join_kernel<OBF><<<dim3((unsigned)((p.spans - 1) * chunks)), 64 * kJoinWaves, 0, stream>>>(
