@@ -62,70 +62,69 @@ __device__ __forceinline__ int piece_rows(const HeadSums *s, int64_t first, int6
 }
 
 // ------------------------------------------------------- copies
-// `dst`, cols_p numbers on a 16-byte address, = `src`, cols numbers anywhere, and
-// zeros behind them; all zeros for a null src. `threads` of them, this one being `at`.
+// Numbers c.. of `dst`, 16 bytes on a 16-byte address, = those of `src`, cols
+// numbers anywhere, and zeros behind them; all zeros for a null src.
 template <bool BF16>
-__device__ __forceinline__ void pack_row(const void *src, int64_t cols, void *dst, int64_t cols_p, int at, int threads) {
+__device__ __forceinline__ void pack_chunk(const void *src, int64_t cols, void *dst, int64_t c) {
     using T = typename Elem<BF16>::type;
     const T *s = static_cast<const T *>(src);
-    T *d = static_cast<T *>(dst);
     constexpr int V = 16 / sizeof(T);
-    for (int64_t c = (int64_t)at * V; c < cols_p; c += (int64_t)threads * V) {
-        T x[V];
-        if (s && c + V <= cols) {
-            __builtin_memcpy(x, s + c, sizeof x);
-        } else {
+    T x[V];
+    if (s && c + V <= cols) {
+        __builtin_memcpy(x, s + c, sizeof x);
+    } else {
 #pragma unroll
-            for (int k = 0; k < V; ++k) x[k] = s && c + k < cols ? s[c + k] : (T)0;
-        }
-        __builtin_memcpy(__builtin_assume_aligned(d + c, 16), x, sizeof x);
+        for (int k = 0; k < V; ++k) x[k] = s && c + k < cols ? s[c + k] : (T)0;
     }
+    __builtin_memcpy(__builtin_assume_aligned(static_cast<T *>(dst) + c, 16), x, sizeof x);
 }
 
-// Row r of the packed hidden states of a piece with n rows.
+// Chunk c of row r of the packed hidden states of a piece with n rows.
 template <bool BF16>
-__device__ __forceinline__ void pack_hidden(const HeadArgs &a, const int32_t *map, int64_t first, int n, int64_t r,
-                                            void *packed, int64_t width_p, int at, int threads) {
+__device__ __forceinline__ void pack_hidden(const HeadArgs &a, const int32_t *map, int64_t first, int n, int64_t r, int64_t c,
+                                            void *packed, int64_t width_p) {
     constexpr int es = BF16 ? 2 : 4;
     const char *src = r < n ? static_cast<const char *>(a.hidden) + (int64_t)map[first + r] * a.width * es : nullptr;
-    pack_row<BF16>(src, a.width, static_cast<char *>(packed) + r * width_p * es, width_p, at, threads);
+    pack_chunk<BF16>(src, a.width, static_cast<char *>(packed) + r * width_p * es, c);
 }
 
 // The rows of a piece, and zeros up to a whole stage. A workgroup to a row.
 template <bool BF16>
 __global__ void __launch_bounds__(256)
 pack_hidden_kernel(HeadArgs a, const int32_t *map, const HeadSums *sums, int64_t first, int64_t piece, void *packed, int64_t width_p) {
+    constexpr int V = BF16 ? 8 : 4;
     const int n = piece_rows(sums, first, piece);
-    if (blockIdx.x < round_up(n, 64)) pack_hidden<BF16>(a, map, first, n, blockIdx.x, packed, width_p, threadIdx.x, 256);
+    if (blockIdx.x < round_up(n, 64))
+        for (int64_t c = threadIdx.x * V; c < width_p; c += 256 * V)
+            pack_hidden<BF16>(a, map, first, n, blockIdx.x, c, packed, width_p);
 }
 
 // A table whose rows are not whole stages on 16-byte addresses.
 template <bool BF16>
 __global__ void __launch_bounds__(256) pack_table_kernel(HeadArgs a, void *packed, int64_t width_p) {
-    constexpr int es = BF16 ? 2 : 4;
+    constexpr int es = BF16 ? 2 : 4, V = 16 / es;
     const int64_t r = blockIdx.x;
-    pack_row<BF16>(static_cast<const char *>(a.table) + r * a.width * es, a.width, static_cast<char *>(packed) + r * width_p * es,
-                   width_p, threadIdx.x, 256);
+    for (int64_t c = threadIdx.x * V; c < width_p; c += 256 * V)
+        pack_chunk<BF16>(static_cast<const char *>(a.table) + r * a.width * es, a.width, static_cast<char *>(packed) + r * width_p * es, c);
 }
 
 // ------------------------------------------------------- which rows
-// A wave: the loss and the gradient of row i, which takes no part, are zero.
-__device__ __forceinline__ void idle_row(const HeadArgs &a, float *losses, int64_t i, int lane) {
-    if (lane == 0) losses[i] = 0.0f;
-    if (!a.grad_hidden) return;
+// A wave: the gradient of row i, which takes no part, is zero.
+__device__ __forceinline__ void idle_row(const HeadArgs &a, int64_t i, int lane) {
     for (int64_t c = lane; c < a.width; c += 64)
         if (a.bf16) static_cast<uint16_t *>(a.grad_hidden)[i * a.width + c] = 0;
         else static_cast<float *>(a.grad_hidden)[i * a.width + c] = 0.0f;
 }
 
-// One workgroup: the rows that take part, in order, with their targets, and
-// their weights' sum; in small calls also what the others get (idle: the losses)
-// and the rows packed. A wave takes kRows * 64 rows at a time, all asked for before
-// the first is used.
+// One workgroup: the rows that take part, in order, with their targets, and their
+// weights' sum; the others' losses, zeros. In small calls also the others'
+// gradients (idle), and the rows packed. A wave takes kRows * 64 rows at a time,
+// all asked for before the first is used.
 template <bool BF16, int kRows>
 __global__ void __launch_bounds__(1024)
-rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *idle, void *packed, int64_t width_p) {
+rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *losses, bool idle, void *packed, int64_t width_p) {
     __shared__ int32_t found[16];
+    __shared__ uint64_t on[16];
     __shared__ double parts[16];
     __shared__ float tops[16];
     const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
@@ -146,16 +145,19 @@ rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *id
         int mine = 0;
 #pragma unroll
         for (int k = 0; k < kRows; ++k) {
-            const bool on = (uint64_t)y[k] < (uint64_t)a.vocab && w[k] != 0.0f;   // as takes_part()
-            mask[k] = __ballot(on);
+            const bool part = (uint64_t)y[k] < (uint64_t)a.vocab && w[k] != 0.0f;   // as takes_part()
+            mask[k] = __ballot(part);
             mine += __popcll(mask[k]);
-            if (on) {
+            if (part) {
                 weight += (double)w[k];
                 most = fmaxf(most, fabsf(w[k]));
             }
         }
-        if (lane == 0) found[wave] = mine;
+        if (lane == 0) found[wave] = mine, on[wave] = mask[0];
         __syncthreads();
+        if (idle)                                 // one round, of one row a thread
+            for (int i = wave; i < a.count; i += 16)
+                if (!(on[i / 64] >> (i % 64) & 1)) idle_row(a, i, lane);
         int64_t at = base;
         for (int x = 0; x < 16; ++x) {
             if (x < wave) at += found[x];
@@ -170,11 +172,11 @@ rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *id
             }
             at += __popcll(mask[k]);
         }
-        if (idle)
 #pragma unroll
-            for (int k = 0; k < kRows; ++k)
-                for (int64_t i = first - lane + 64 * k, e = i + 64 < a.count ? i + 64 : a.count, j = i; j < e; ++j)
-                    if (!(mask[k] >> (j - i) & 1)) idle_row(a, idle, j, lane);
+        for (int k = 0; k < kRows; ++k) {
+            const int64_t i = first + 64 * k;
+            if (i < a.count && !(mask[k] >> lane & 1)) losses[i] = 0.0f;
+        }
         __syncthreads();
     }
     for (int s = 32; s; s /= 2) {
@@ -195,9 +197,12 @@ rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *id
         sums->most = most;
         sums->scale = (float)((double)a.grad_scale * (double)most / (a.mean && weight != 0.0 ? weight : 1.0));
     }
-    if (packed)                                   // the map is this workgroup's own, and synchronised
-        for (int64_t r = wave; r < round_up(base, 64); r += 16)
-            pack_hidden<BF16>(a, map, 0, (int)base, r, packed, width_p, lane, 64);
+    if (packed) {                                 // the map is this workgroup's own, and synchronised
+        constexpr int V = BF16 ? 8 : 4;
+        const uint32_t per_row = (uint32_t)(width_p / V);
+        for (uint32_t k = threadIdx.x; k < (uint32_t)round_up(base, 64) * per_row; k += 1024)
+            pack_hidden<BF16>(a, map, 0, (int)base, k / per_row, (int64_t)(k % per_row) * V, packed, width_p);
+    }
 }
 
 // ------------------------------------------------------- the product
@@ -850,17 +855,19 @@ gradient_kernel(Gradient g, int64_t vocab, const HeadSums *sums, int64_t first, 
 }
 
 // ------------------------------------------------------- the softmax
-// A wave: the maximum and sum of row q of the piece from its tiles', and its loss.
+// LANES of a wave: the maximum and sum of row q of the piece from its tiles', and
+// its loss.
+template <int LANES>
 __device__ __forceinline__ void softmax_row(const HeadArgs &a, const HeadSums *sums, const int32_t *map, int64_t first,
                                             const f32x2 *stat, int64_t subtiles, HeadRow *rows, float *losses, int64_t q, int lane) {
     const f32x2 *s = stat + q * subtiles;
     float top = -INFINITY;
-    for (int64_t k = lane; k < subtiles; k += 64) top = fmaxf(top, s[k].x);
-    for (int d = 32; d; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
+    for (int64_t k = lane; k < subtiles; k += LANES) top = fmaxf(top, s[k].x);
+    for (int d = LANES / 2; d; d /= 2) top = fmaxf(top, __shfl_xor(top, d));
     const float base = top == -INFINITY ? 0.0f : top;
     float sum = 0.0f;
-    for (int64_t k = lane; k < subtiles; k += 64) sum += s[k].y * __builtin_amdgcn_exp2f(s[k].x - base);
-    for (int d = 32; d; d /= 2) sum += __shfl_xor(sum, d);
+    for (int64_t k = lane; k < subtiles; k += LANES) sum += s[k].y * __builtin_amdgcn_exp2f(s[k].x - base);
+    for (int d = LANES / 2; d; d /= 2) sum += __shfl_xor(sum, d);
     if (lane) return;
     const int64_t i = map[first + q];
     const float w = a.weights ? a.weights[i] : 1.0f;
@@ -878,8 +885,17 @@ softmax_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t fir
                const f32x2 *stat, int64_t subtiles, HeadRow *rows, float *losses) {
     const int64_t q = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
     if (q < piece_rows(sums, first, piece))
-        softmax_row(a, sums, map, first, stat, subtiles, rows, losses, q, threadIdx.x % 64);
+        softmax_row<64>(a, sums, map, first, stat, subtiles, rows, losses, q, threadIdx.x % 64);
 }
+
+// What one workgroup does in about a launch's time, 2.5 us on the device and more on
+// the host, does not get one: rows and numbers of them that it sets to zero (1024 rows
+// of 1000 x 64: 53.5 us so, 48.8 with a launch), and rounds in which each of its
+// threads goes through 16 bytes, or each of its waves (each quarter of one, if there
+// are few) through a row's statistics. With gradients, bf16: 4 rows of 300 x 64 take
+// 22.0 us for 26.1 with a launch for each, 32 of 500 x 64 25.5 for 29.6; with 4 rounds
+// allowed 8 of 4000 x 128 take 38.4 for 32.7.
+constexpr int64_t kSmallRows = 256, kSmallZeros = 65536, kSmallRounds = 2, kFewStats = 64;
 
 // One workgroup: the weighted sum of the losses, in binary64; in small calls of the
 // rows' softmax first, and of e's turning into G (g.e, if there).
@@ -889,8 +905,12 @@ loss_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, Gradient g, He
     __shared__ double parts[16];
     if (g.stat) {
         const int n = (int)sums->rows;
-        for (int64_t q = threadIdx.x / 64; q < n; q += 16)
-            softmax_row(a, sums, map, 0, g.stat, g.subtiles, rows, losses, q, threadIdx.x % 64);
+        if (g.subtiles <= kFewStats)
+            for (int64_t q = threadIdx.x / 16; q < n; q += 64)
+                softmax_row<16>(a, sums, map, 0, g.stat, g.subtiles, rows, losses, q, threadIdx.x % 16);
+        else
+            for (int64_t q = threadIdx.x / 64; q < n; q += 16)
+                softmax_row<64>(a, sums, map, 0, g.stat, g.subtiles, rows, losses, q, threadIdx.x % 64);
         __syncthreads();                          // a workgroup sees its own stores
         constexpr int V = BF16 ? 8 : 4;
         const uint32_t per_row = (uint32_t)(g.vocab_p / V);
@@ -915,10 +935,10 @@ loss_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, Gradient g, He
     }
 }
 
-// losses and rows of grad_hidden that take no part: zero.
-__global__ void __launch_bounds__(256) idle_rows_kernel(HeadArgs a, float *losses) {
+// Rows of grad_hidden that take no part: zero.
+__global__ void __launch_bounds__(256) idle_rows_kernel(HeadArgs a) {
     for (int64_t i = (int64_t)blockIdx.x * 4 + threadIdx.x / 64; i < a.count; i += (int64_t)gridDim.x * 4)
-        if (!takes_part(a, i)) idle_row(a, losses, i, threadIdx.x % 64);
+        if (!takes_part(a, i)) idle_row(a, i, threadIdx.x % 64);
 }
 
 // ------------------------------------------------------- launches
@@ -938,9 +958,6 @@ void start_product(const Product &g, int shape, hipStream_t stream) {
         }
 }
 
-// Numbers that one workgroup goes through in about the time of a launch.
-constexpr int64_t kSmallCall = 65536;
-
 template <bool BF16>
 hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
     char *w = a.workspace;
@@ -951,16 +968,16 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
     auto *rows = reinterpret_cast<HeadRow *>(w + p.row_off);
     auto *stat = reinterpret_cast<f32x2 *>(w + p.stat_off);
     const bool grads = a.grad_hidden || a.grad_table;
-    // what one workgroup does in about a launch's time does not get one
-    const bool small = a.count * (a.grad_hidden ? a.width : 1) <= kSmallCall;
-    const bool pack = p.pieces == 1 && round_up(a.count, 64) * p.width_p <= kSmallCall;
-    const bool one = p.pieces == 1 && a.count * p.subtiles <= kSmallCall / 4;
-    const bool turn = one && grads && p.piece_p * p.vocab_p <= kSmallCall / 4;
-    float *idle = small ? losses : nullptr;
+    const int V = 16 / es;
+    const bool idle = a.grad_hidden && a.count <= kSmallRows && a.count * a.width <= kSmallZeros;
+    const bool pack = p.pieces == 1 && round_up(a.count, 64) * p.width_p <= kSmallRounds * 1024 * V;
+    const int64_t rounds = p.subtiles <= kFewStats ? ceil_div(a.count, 64) : ceil_div(a.count, 16) * ceil_div(p.subtiles, 512);
+    const bool one = p.pieces == 1 && rounds <= kSmallRounds;
+    const bool turn = one && grads && a.count * p.vocab_p <= kSmallRounds * 1024 * V;
     void *packed = pack ? w + p.hidden_off : nullptr;
-    if (a.count <= 2048) rows_kernel<BF16, 1><<<1, 1024, 0, stream>>>(a, sums, map, target, idle, packed, p.width_p);
-    else rows_kernel<BF16, 8><<<1, 1024, 0, stream>>>(a, sums, map, target, idle, packed, p.width_p);
-    if (!small) idle_rows_kernel<<<(unsigned)(a.count < 65536 ? ceil_div(a.count, 4) : 16384), 256, 0, stream>>>(a, losses);
+    if (a.count <= 2048) rows_kernel<BF16, 1><<<1, 1024, 0, stream>>>(a, sums, map, target, losses, idle, packed, p.width_p);
+    else rows_kernel<BF16, 8><<<1, 1024, 0, stream>>>(a, sums, map, target, losses, idle, packed, p.width_p);
+    if (a.grad_hidden && !idle) idle_rows_kernel<<<(unsigned)(a.count < 65536 ? ceil_div(a.count, 4) : 16384), 256, 0, stream>>>(a);
     const void *table = a.table;
     if (p.pack_table) {
         pack_table_kernel<BF16><<<(unsigned)a.vocab, 256, 0, stream>>>(a, w + p.table_off, p.width_p);
