@@ -75,6 +75,15 @@ def test_few_tiles_of_many_parts(n, vocab, width, dtype):
     run(hidden, table, targets)
 
 
+@pytest.mark.parametrize("n", [1, 32, 33, 64, 65, 128, 129, 192, 193, 256])
+@pytest.mark.parametrize("vocab,width", [(17000, 40), (16999, 200), (32768, 320), (32769, 320)])
+def test_few_rows_of_a_long_table(n, vocab, width):
+    """Fewer stages than LDS has places for, as many, and more."""
+    hidden, table, targets, g = make(n, vocab, width, BF, ignored=0.1 if n > 1 else 0.0)
+    run(hidden, table, targets)
+    run(hidden, table, targets, grads=False)
+
+
 @pytest.mark.parametrize("dtype", [BF, F32])
 def test_more_rows_than_a_grid_has_lines(dtype):
     hidden, table, targets, g = make(70001, 40, 16, dtype, ignored=0.01)

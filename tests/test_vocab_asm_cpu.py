@@ -56,9 +56,10 @@ def test_products_run_on_the_matrix_cores_from_lds(kernels):
         assert ("v_mfma_f32_16x16x32_bf16" if bf16 else "v_mfma_f32_16x16x4_f32") in body, name
         assert re.search(r"buffer_load_dwordx4 [^\n]* lds", body), name
         assert ("ds_read_b64_tr_b16" in body) == (bf16 and across), name
+        deep = "ELi1ELi3EEEv" in name or "ELi1ELi4EEEv" in name       # three or four stages in LDS
         for b in blocks(body):
             if b.count("v_mfma") >= 16:
-                assert len(re.findall(r"s_waitcnt vmcnt", b)) <= 1, name
-    # bf16: logits, grad_hidden, grad_table to bf16 and to fp32, in three tiles;
-    # fp32: the same in two
-    assert seen == 4 * 3 + 4 * 2, seen
+                assert len(re.findall(r"s_waitcnt vmcnt", b)) <= (3 if deep else 1), name
+    # bf16: logits, grad_hidden, grad_table to bf16 and to fp32, in three tiles, and
+    # logits in five more; fp32: the same in two
+    assert seen == 4 * 3 + 5 + 4 * 2, seen

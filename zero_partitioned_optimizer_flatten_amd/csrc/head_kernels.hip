@@ -437,7 +437,7 @@ struct Operand {
     }
 };
 
-template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE, int JOIN>
+template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE, int JOIN, int DEPTH>
 __device__ __forceinline__ void product(const Product &g) {
     constexpr int kWaves = WP * WQ;
     constexpr int kP = BP / WP, kQ = BQ / WQ;                 // outputs of a wave
@@ -451,7 +451,7 @@ __device__ __forceinline__ void product(const Product &g) {
     // Outputs of two bytes are turned in LDS, 16 rows of q at a time, a wave its own.
     constexpr bool kTurned = EPI == kBf16 || (EPI == kLogits && BF16);
     constexpr int kTurn = kTurned ? 16 * kP * 2 : 0;
-    __shared__ __align__(1024) char lds[2 * kStage + kWaves * kTurn];
+    __shared__ __align__(1024) char lds[DEPTH * kStage + kWaves * kTurn];
 
     const int lane = threadIdx.x % 64;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -460,13 +460,13 @@ __device__ __forceinline__ void product(const Product &g) {
     const int64_t nq = g.sums && g.piece_is_q ? piece_rows(g.sums, g.first, g.piece) : g.nq;
     if ((int)blockIdx.x >= sc.units) return;
 
-    // The loads run two stages ahead of the products, over the ends of units.
+    // The loads run DEPTH stages ahead of the products, over the ends of units.
     OpP op;
     OpQ oq;
     op.init(wave, lane, (int)g.ldp);
     oq.init(wave, lane, (int)g.ldq);
     int lines = 0;                // of P left (TP: the table's rows are not padded)
-    int next = blockIdx.x, left = 0;
+    int next = blockIdx.x, left = 0, issued = 0;
     const uint32_t lds0 = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(lds_void *)lds);
     auto begin = [&]() {
         const Unit u = unit_of(sc, next, BP, BQ);
@@ -482,6 +482,7 @@ __device__ __forceinline__ void product(const Product &g) {
         else op.template load<false>(s, wave, lane, 0, 0);
         oq.template load<false>(s + BP * 128, wave, lane, 0, 0);
         lines -= OpP::kSteps;
+        if (DEPTH > 2) ++issued;
         if (--left == 0) {
             next += gridDim.x;
             if (next < sc.units) begin();
@@ -530,8 +531,8 @@ __device__ __forceinline__ void product(const Product &g) {
     };
 
     if (sc.steps > 0) begin();
-    load(0);
-    load(1);
+#pragma unroll
+    for (int b = 0; b < DEPTH; ++b) load(b);
     targets(blockIdx.x);
     arrived();
     asm volatile("s_barrier" ::: "memory");
@@ -547,10 +548,10 @@ __device__ __forceinline__ void product(const Product &g) {
         // stage has been read by all, the loads of the stage after the next go to its
         // place, so a load has nearly a stage's time to arrive and a wave meets one
         // barrier a stage, with products still to do. A unit's first part is read with
-        // the last of the unit before, and its first two stages have arrived before
+        // the last of the unit before, and its first DEPTH stages have arrived before
         // that one's outputs are stored.
         for (int k = 0; k < u.steps; ++k) {
-            const int buf = (stage + k) & 1;
+            const int buf = DEPTH == 2 ? (stage + k) & 1 : (unsigned)(stage + k) % DEPTH;
             int later = k;
             asm volatile("" : "+s"(later));       // no first round of its own
             read(buf, 1);
@@ -564,10 +565,19 @@ __device__ __forceinline__ void product(const Product &g) {
             read(buf, 3);
             __builtin_amdgcn_sched_barrier(0);
             multiply(2);
-            if (later > 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            if (DEPTH == 2) {
+                if (later > 0) asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            } else {
+                // all but the loads of the stages after the next: they arrive in order
+                constexpr int kLoads = kLoadsP + kLoadsQ;
+                const int after = uniform(issued - (stage + k) - 2);
+                if (after >= 2) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(2 * kLoads) : "memory");
+                else if (after == 1) asm volatile("s_waitcnt vmcnt(%0)" ::"n"(kLoads) : "memory");
+                else asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            }
             asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
             load(buf);
-            read(buf ^ 1, 0);                     // after the last unit: of no use, but there
+            read(DEPTH == 2 ? buf ^ 1 : (unsigned)(buf + 1) % DEPTH, 0);    // after the last unit: of no use, but there
             __builtin_amdgcn_sched_barrier(0);
             multiply(3);
         }
@@ -578,7 +588,7 @@ __device__ __forceinline__ void product(const Product &g) {
         // next stage would wait for the stores as well.
         const int64_t pw = u.p0 + wp * kP + lane / 16 * 4, qw = u.q0 + wq * kQ + lane % 16;
         const bool whole = u.p0 + BP <= g.np;
-        char *turn = lds + 2 * kStage + wave * kTurn;
+        char *turn = lds + DEPTH * kStage + wave * kTurn;
         // whole vectors: those go past the caches, parts of lines would be slow there
         const bool aligned = EPI == kLogits || (((uintptr_t)g.out | (uintptr_t)(2 * g.ldo)) % 16 == 0);
         // 16 rows of kP numbers of two bytes; 16-byte chunk c of row r at c ^ r.
@@ -742,9 +752,9 @@ __device__ __forceinline__ void product(const Product &g) {
     }
 }
 
-template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE, int JOIN>
-__global__ void __launch_bounds__(64 * WP * WQ, 2) product_kernel(Product g) {
-    product<BF16, EPI, TP, TQ, BP, BQ, WP, WQ, AT_ONCE, JOIN>(g);
+template <bool BF16, int EPI, bool TP, bool TQ, int BP, int BQ, int WP, int WQ, int AT_ONCE, int JOIN, int DEPTH = 2>
+__global__ void __launch_bounds__(64 * WP * WQ, WP * WQ == 4 && DEPTH > 2 ? 1 : 2) product_kernel(Product g) {
+    product<BF16, EPI, TP, TQ, BP, BQ, WP, WQ, AT_ONCE, JOIN, DEPTH>(g);
 }
 
 // The parts of cut tiles, in order, and what a whole tile's epilogue does. Four
@@ -947,6 +957,15 @@ void start_product(const Product &g, int shape, hipStream_t stream) {
     const TileShape t = kTiles[shape];
     const int64_t tiles = ceil_div(g.np, t.p) * ceil_div(g.nq, t.q);
     const unsigned grid = (unsigned)(g.slots > 0 || tiles > t.at_once ? t.at_once : tiles);
+    if constexpr (EPI == kLogits) {
+        if constexpr (BF16) {
+            if (shape == 3) product_kernel<BF16, EPI, TP, TQ, 128, 32, 4, 1, 256, 1, 4><<<grid, 256, 0, stream>>>(g);
+            if (shape == 4) product_kernel<BF16, EPI, TP, TQ, 128, 64, 4, 2, 256, 1, 4><<<grid, 512, 0, stream>>>(g);
+            if (shape == 5) product_kernel<BF16, EPI, TP, TQ, 128, 128, 2, 4, 256, 1, 4><<<grid, 512, 0, stream>>>(g);
+            if (shape == 6) product_kernel<BF16, EPI, TP, TQ, 128, 192, 2, 4, 256, 1, 3><<<grid, 512, 0, stream>>>(g);
+            if (shape == 7) product_kernel<BF16, EPI, TP, TQ, 128, 256, 2, 4, 256, 1, 3><<<grid, 512, 0, stream>>>(g);
+        }
+    }
     if constexpr (BF16)
         if (shape == 0) product_kernel<BF16, EPI, TP, TQ, 256, 256, 2, 4, kTiles[0].at_once, BF16 ? kTiles[0].join : 4 * kTiles[0].join><<<grid, 512, 0, stream>>>(g);
     if (shape == 1) product_kernel<BF16, EPI, TP, TQ, 128, 128, 2, 2, kTiles[1].at_once, BF16 ? kTiles[1].join : 4 * kTiles[1].join><<<grid, 256, 0, stream>>>(g);

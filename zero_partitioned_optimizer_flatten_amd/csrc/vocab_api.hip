@@ -178,6 +178,21 @@ int choose_tile(int64_t np, int64_t nq, int64_t steps, bool cut, bool bf16) {
     return best;
 }
 
+// Few rows: the table is read once, whatever the tile, and what counts is how much of
+// it is under way. One tile to a compute unit, all rows wide, with three or four
+// stages in LDS instead of two, reads 32000 x 5120 bf16 for one row in 75 us (call;
+// the other tiles 96), for 128 in 88 (105), for 192 in 98 (117), for 256 in 115 (130).
+// A table of fewer tiles leaves compute units without one, which costs from about two
+// rows a tile on (16000 x 4096: 160 rows 67 for 73, 256 rows 80 for 75). fp32 is
+// bound by its multiplying (1 row of 32000 x 4096 146 for 149, 48 rows 192 for 179).
+int logits_tile(int64_t vocab, int64_t rows, int64_t steps, bool bf16) {
+    const int64_t tiles = ceil_div(vocab, 128);
+    if (bf16 && tiles <= 256 && rows <= 2 * tiles)
+        for (int shape = 3; shape < 8; ++shape)
+            if (rows <= kTiles[shape].q) return shape;
+    return choose_tile(vocab, rows, steps, false, bf16);
+}
+
 }  // namespace
 
 HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
@@ -194,7 +209,7 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     p.piece = piece;
     p.pieces = a.count > 0 ? ceil_div(a.count, piece) : (a.grad_table ? 1 : 0);
     p.piece_p = round_up(piece, 64);
-    p.tile_logits = choose_tile(a.vocab, piece, p.width_p / step, false, a.bf16);
+    p.tile_logits = logits_tile(a.vocab, piece, p.width_p / step, a.bf16);
     p.sub = kTiles[p.tile_logits].sub;
     p.subtiles = round_up(a.vocab, kTiles[p.tile_logits].p) / p.sub;
     p.tile_hidden = choose_tile(a.width, piece, ceil_div(a.vocab, step), true, a.bf16);

@@ -114,7 +114,10 @@ struct TileShape {
     int p, q, sub, at_once;
     int join;                     // parts that are joined in the time of a stage
 };
-constexpr TileShape kTiles[] = {{256, 256, 128, 256, 11}, {128, 128, 64, 512, 25}, {128, 32, 32, 768, 55}};
+constexpr TileShape kTiles[] = {{256, 256, 128, 256, 11}, {128, 128, 64, 512, 25}, {128, 32, 32, 768, 55},
+                                // for the logits of few rows (logits_tile), not cut
+                                {128, 32, 32, 256, 1}, {128, 64, 32, 256, 1}, {128, 128, 64, 256, 1},
+                                {128, 192, 64, 256, 1}, {128, 256, 64, 256, 1}};
 // A part of a tile: at most kMaxParts of at least kMinPart stages. What it takes
 // besides, in stages, which take several times as long with fp32, where also that
 // many more parts are joined in a stage's time.
