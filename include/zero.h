@@ -545,7 +545,7 @@ int zero_embed_grad_workspace(int64_t count, int64_t rows, int64_t width,
  * written for every v < rows (zeros where no id names it), or, with
  * accumulate != 0, added to the rows that ids name; rows that none names are
  * then not touched. D: the forward call's drop. The sum is in binary32, in an
- * order that count alone fixes. The gradient of a position table is this call
+ * order that ids, count and width fix. The gradient of a position table is this call
  * with the position ids, scale 1 and the same drop. workspace: 256-byte
  * aligned. EINVAL, EUNSUPPORTED as zero_embed; EINVAL also for a workspace
  * that is too small. */
