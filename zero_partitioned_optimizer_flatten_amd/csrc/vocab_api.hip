@@ -125,10 +125,12 @@ EmbedGradPlan plan_embed_grad(int64_t count, int64_t rows, int64_t width) {
     p.sort_groups_log2 = 8;                        // one workgroup to a compute unit
     while ((rows >> p.sort_groups_log2) >= kSortIds) ++p.sort_groups_log2;
     p.ids_per_group = (int)ceil_div(rows, (int64_t)1 << p.sort_groups_log2);
-    // About 1024 spans, and at most 256 tokens in one: few partial rows for a
-    // run that is the whole batch, enough waves for short batches. Few tokens
-    // have a wave for each run, and no joining follows (span 1).
-    const int64_t span = count / 1024, chunks = ceil_div(width, kSpanCols);
+    // About 4096 waves, and 8 to 256 tokens to each: enough to keep loads on their way,
+    // few partial rows. 65536 tokens of 768 columns take 79 us (half the waves 86, a
+    // quarter 109), 16384 of 4096 102 (twice the waves 107, four times 113; fp32 200,
+    // twice the waves 194). Few tokens have a workgroup for each run, and no joining
+    // follows (span 1).
+    const int64_t chunks = ceil_div(width, kSpanCols), span = ceil_div(count * chunks, 4096);
     const bool runs = count <= kRunTokens && count * chunks < (int64_t)1 << 22;     // a dispatch's limit
     p.span = runs ? 1 : (int)(span < 8 ? 8 : span > 256 ? 256 : span);
     p.spans = ceil_div(count, p.span);
