@@ -345,7 +345,7 @@ sort_kernel(EmbedGradArgs a, int log2_groups, int per_group, SortedToken *sorted
 // kernel adds a run's partial rows in the order of the spans. So the work is
 // even whatever the tokens are, one padding token a million times included. Bound by
 // memory: 16384 rows of 4096 bf16 (134 MB), a third of them of one id, take 42 us,
-// and 12 the joining. The sums are in binary32, the partial rows too; a row is rounded once, when it is written.
+// and 7 the joining. The sums are in binary32, the partial rows too; a row is rounded once, when it is written.
 
 // Rows a lane has under way.
 constexpr int kSpanBatch = 8;
