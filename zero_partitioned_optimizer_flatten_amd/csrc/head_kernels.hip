@@ -667,20 +667,23 @@ __device__ __forceinline__ void product(const Product &g) {
 #pragma unroll
                     for (int r = 0; r < 4; ++r) top = fmaxf(top, acc[i][j][r]);
                 top = fmaxf(top, __shfl_xor(top, 16));
-                top = fmaxf(top, __shfl_xor(top, 32)) * kLog2e;
-                const float base = (BF16 ? kScaleLog2 : 0.0f) - (top == -INFINITY ? 0.0f : top);
+                top = fmaxf(top, __shfl_xor(top, 32));
+                // The maximum is subtracted before the factor log2 e: its own e is then 1
+                // exactly, which a product of it, rounded, would miss by 2^-24 of itself
+                // (a certain row's loss would be 1e-5 for 0, on either side, at z = 250).
+                const float from = top == -INFINITY ? 0.0f : top;
                 float sum = 0.0f;
 #pragma unroll
                 for (int i = 0; i < kI; ++i)
 #pragma unroll
                     for (int r = 0; r < 4; ++r) {
-                        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r], kLog2e, base));
+                        const float e = __builtin_amdgcn_exp2f(__builtin_fmaf(acc[i][j][r] - from, kLog2e, BF16 ? kScaleLog2 : 0.0f));
                         acc[i][j][r] = e;
                         sum += e;
                     }
                 sum += __shfl_xor(sum, 16);
                 sum += __shfl_xor(sum, 32);
-                tops[j] = top;
+                tops[j] = top * kLog2e;
                 sums[j] = BF16 ? sum * 0x1p-15f : sum;
             }
             targets(unit + (int)gridDim.x);
@@ -896,8 +899,8 @@ __device__ __forceinline__ void softmax_row(const HeadArgs &a, const HeadSums *s
     const int64_t i = map[first + q];
     const float w = a.weights ? a.weights[i] : 1.0f;
     const float share = w / sums->most;
-    // top - target first: exact where the target is the largest, which is where
-    // the loss is small
+    // Not negative: top >= target, since both are rounded the same way (0 where the
+    // target is the largest), and sum >= 1, since the largest entry's e is 1.
     losses[i] = (float)(((double)(base - rows[q].target) + (double)__builtin_amdgcn_logf(sum)) * kLn2);
     rows[q].top = base;
     rows[q].inv = share / sum;
