@@ -525,9 +525,10 @@ typedef struct {
 /* out[n] = D(scale * table[ids[n]] + position_table[position_ids[n]]) for
  * n < count, with rows of `width` elements; D is dropout over the count *
  * width output elements (drop NULL: none). position_ids and position_table may
- * be NULL together. Both tables have `dtype`. EINVAL: null or misaligned
- * pointers, ranges past their allocations, unknown dtypes or id sizes, a scale
- * not finite, p outside [0, 1], an output that overlaps an input.
+ * be NULL together, and the ids alone where count is 0. Both tables have
+ * `dtype`. EINVAL: null or misaligned pointers, ranges past their allocations,
+ * unknown dtypes or id sizes, a scale not finite, p outside [0, 1], an output
+ * that overlaps an input.
  * EUNSUPPORTED: more than 1.7e10 output elements, 2^31 ids, 2^30 rows. */
 int zero_embed(const void *ids, int32_t id_bytes, int64_t count,
                const void *table, int64_t rows, int64_t width,

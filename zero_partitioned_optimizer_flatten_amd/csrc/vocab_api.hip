@@ -266,9 +266,10 @@ int zero_embed(const void *ids, int32_t id_bytes, int64_t count, const void *tab
     if ((rc = check_drop(drop, &a.drop))) return rc;
     if ((rc = check_ids(ids, id_bytes, count, "ids"))) return rc;
     if ((rc = check_buffer(table, rows * width, dtype_size(dtype), "table"))) return rc;
-    if (!position_ids != !position_table)
+    // no ids have no address: a call without rows may come with the table alone
+    if (!position_ids != !position_table && (position_ids || count > 0))
         return fail(ZERO_EINVAL, "position ids and a position table come together");
-    if (position_ids) {
+    if (position_table) {
         if ((rc = check_table(position_rows, width, "position table"))) return rc;
         if ((rc = check_ids(position_ids, id_bytes, count, "position ids"))) return rc;
         if ((rc = check_buffer(position_table, position_rows * width, dtype_size(dtype), "position table"))) return rc;
