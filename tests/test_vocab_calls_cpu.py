@@ -1,7 +1,15 @@
 """Calls of the vocabulary operators that the documentation allows, or that are
 refused, at the ends of their ranges, against the host code built with g++."""
+import ctypes
+import os
+import subprocess
+
+import pytest
+
+import host_double
 from test_vocab_cpu import INVALID, L, UNSUPPORTED, changed, malloc, needs_gpp, refused, size_of  # noqa: F401
 import zero_partitioned_optimizer_flatten_amd as zero
+from zero_partitioned_optimizer_flatten_amd import build as zb
 
 
 @needs_gpp
@@ -17,3 +25,31 @@ def test_no_rows_have_no_position_ids(L):  # noqa: F811
     refused(L, INVALID, call(prows=11), "run past")
     refused(L, INVALID, call(pos=table, ptable=None), "together")
     refused(L, INVALID, call(count=1, ids=table, out=malloc(L, 2 * width)), "together")
+
+
+@pytest.fixture(scope="module")
+def rules(tmp_path_factory):
+    so = os.path.join(str(tmp_path_factory.mktemp("rules")), "librules.so")
+    subprocess.check_call(["g++", *host_double.FLAGS, "-x", "c++", *[os.path.join(zb.CSRC, n) for n in ("zero_api.hip", "vocab_api.hip")],
+                           *[os.path.join(host_double.TESTS, n) for n in ("host_double.cpp", "vocab_double.cpp", "vocab_rules.cpp")],
+                           "-o", so])
+    lib = ctypes.CDLL(so)
+    lib.rules_turned_with_loss.restype = ctypes.c_int64
+    lib.rules_turned_with_loss.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int, ctypes.c_int64]
+    return lib
+
+
+@needs_gpp
+def test_one_workgroup_turns_few_numbers(rules):
+    """Zeros behind the rows count: a thread of the 1024 goes through six vectors of
+    16 bytes at most, and a call too large for that has a kernel for it."""
+    done = 0
+    for bf16 in (0, 1):
+        for count in (1, 2, 4, 8, 16, 31, 32, 63, 64, 65, 128, 200, 1000):
+            for vocab in (1, 100, 128, 129, 256, 500, 1000, 4000, 8192, 16000, 16384, 50257):
+                turned = rules.rules_turned_with_loss(count, vocab, 64, bf16, 0)
+                assert turned <= 6 * 1024 * (8 if bf16 else 4), (bf16, count, vocab, turned)
+                assert turned == 0 or turned == -(-count // 64) * 64 * (-(-vocab // 128) * 128)
+                assert rules.rules_turned_with_loss(count, vocab, 64, bf16, 1) == (turned if count == 1 else 0)
+                done += turned > 0
+    assert done >= 20, done

@@ -915,15 +915,6 @@ softmax_kernel(HeadArgs a, const HeadSums *sums, const int32_t *map, int64_t fir
         softmax_row<64>(a, sums, map, first, stat, subtiles, rows, losses, q, threadIdx.x % 64);
 }
 
-// What one workgroup does in about a launch's time, 2.5 us on the device and more on
-// the host, does not get one: rows and numbers of them that it sets to zero (1024 rows
-// of 1000 x 64: 53.5 us so, 48.8 with a launch), and rounds in which each of its
-// threads goes through 16 bytes, or each of its waves (each quarter of one, if there
-// are few) through a row's statistics. With gradients, bf16: 4 rows of 300 x 64 take
-// 22.0 us for 26.1 with a launch for each, 32 of 500 x 64 25.5 for 29.6; with 4 rounds
-// allowed 8 of 4000 x 128 take 38.4 for 32.7.
-constexpr int64_t kSmallRows = 256, kSmallZeros = 65536, kSmallRounds = 2, kFewStats = 64;
-
 // One workgroup: the weighted sum of the losses, in binary64; in small calls of the
 // rows' softmax first, and of e's turning into G (g.e, if there).
 template <bool BF16>
@@ -1004,16 +995,10 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
     auto *rows = reinterpret_cast<HeadRow *>(w + p.row_off);
     auto *stat = reinterpret_cast<f32x2 *>(w + p.stat_off);
     const bool grads = a.grad_hidden || a.grad_table;
-    const int V = 16 / es;
-    const bool idle = a.grad_hidden && a.count <= kSmallRows && a.count * a.width <= kSmallZeros;
-    const bool pack = p.pieces == 1 && round_up(a.count, 64) * p.width_p <= kSmallRounds * 1024 * V;
-    const int64_t rounds = p.subtiles <= kFewStats ? ceil_div(a.count, 64) : ceil_div(a.count, 16) * ceil_div(p.subtiles, 512);
-    const bool one = p.pieces == 1 && rounds <= kSmallRounds;
-    const bool turn = one && grads && a.count * p.vocab_p <= kSmallRounds * 1024 * V;
-    void *packed = pack ? w + p.hidden_off : nullptr;
-    if (a.count <= 2048) rows_kernel<BF16, 1><<<1, 1024, 0, stream>>>(a, sums, map, target, losses, idle, packed, p.width_p);
-    else rows_kernel<BF16, 8><<<1, 1024, 0, stream>>>(a, sums, map, target, losses, idle, packed, p.width_p);
-    if (a.grad_hidden && !idle) idle_rows_kernel<<<(unsigned)(a.count < 65536 ? ceil_div(a.count, 4) : 16384), 256, 0, stream>>>(a);
+    void *packed = p.pack_with_rows ? w + p.hidden_off : nullptr;
+    if (a.count <= 2048) rows_kernel<BF16, 1><<<1, 1024, 0, stream>>>(a, sums, map, target, losses, p.idle_with_rows, packed, p.width_p);
+    else rows_kernel<BF16, 8><<<1, 1024, 0, stream>>>(a, sums, map, target, losses, p.idle_with_rows, packed, p.width_p);
+    if (a.grad_hidden && !p.idle_with_rows) idle_rows_kernel<<<(unsigned)(a.count < 65536 ? ceil_div(a.count, 4) : 16384), 256, 0, stream>>>(a);
     const void *table = a.table;
     if (p.pack_table) {
         pack_table_kernel<BF16><<<(unsigned)a.vocab, 256, 0, stream>>>(a, w + p.table_off, p.width_p);
@@ -1021,7 +1006,7 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
     }
     for (int64_t k = 0; k < p.pieces; ++k) {
         const int64_t first = k * p.piece;
-        if (!pack)
+        if (!p.pack_with_rows)
             pack_hidden_kernel<BF16><<<(unsigned)p.piece_p, 256, 0, stream>>>(a, map, sums, first, p.piece, w + p.hidden_off, p.width_p);
         Product g = {};
         g.sums = sums;
@@ -1043,8 +1028,8 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
         g.lde = p.vocab_p;
         start_product<BF16, kLogits, false, false>(g, p.tile_logits, stream);
         Gradient turned = {target + first, stat, rows, w + p.e_off, p.subtiles, p.vocab_p, p.sub};
-        if (one) {
-            if (!turn) turned.e = nullptr;
+        if (p.softmax_with_loss) {
+            if (!p.turn_with_loss) turned.e = nullptr;
             loss_kernel<BF16><<<1, 1024, 0, stream>>>(a, sums, map, turned, rows, losses);
             turned.e = w + p.e_off;
         } else {
@@ -1052,7 +1037,7 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
                                                                                rows, losses);
         }
         if (!grads) continue;
-        if (!turn) {
+        if (!p.turn_with_loss) {
             const int64_t per_row = ceil_div(p.vocab_p * es, 256 * 16);
             gradient_kernel<BF16><<<(unsigned)(p.piece_p * per_row), 256, 0, stream>>>(turned, a.vocab, sums, first, p.piece, (uint32_t)per_row);
         }
@@ -1107,7 +1092,7 @@ hipError_t head(const HeadArgs &a, const HeadPlan &p, hipStream_t stream) {
             }
         }
     }
-    if (!one) loss_kernel<BF16><<<1, 1024, 0, stream>>>(a, sums, map, Gradient{}, rows, losses);
+    if (!p.softmax_with_loss) loss_kernel<BF16><<<1, 1024, 0, stream>>>(a, sums, map, Gradient{}, rows, losses);
     return hipGetLastError();
 }
 

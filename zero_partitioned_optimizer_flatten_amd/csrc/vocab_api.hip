@@ -195,6 +195,28 @@ int logits_tile(int64_t vocab, int64_t rows, int64_t steps, bool bf16) {
     return choose_tile(vocab, rows, steps, false, bf16);
 }
 
+// What one workgroup does in about a launch's time, 2.5 us on the device and more on
+// the host, does not get one: rows and numbers of them that it sets to zero (1024 rows
+// of 1000 x 64: 53.5 us so, 48.8 with a launch), and rounds in which each of its
+// threads goes through 16 bytes, or each of its waves (each quarter of one, if there
+// are few) through a row's statistics. e's turning into G also writes zeros, up to 64
+// rows; those are quicker: three times as many rounds with them. With both gradients,
+// 64 wide, bf16: 8 rows of 256 take 21.6 us for 23.4 with a launch, 32 of 500 (2
+// rounds, 4 with the zeros) 26.4 for 27.8; 64 of 500 (4 and 4) 32.8 for 28.4, 16 of
+// 1000 (2 and 8) 32.6 for 31.5, 1 of 16000 (2 and 125) 55.9 for 34.8; fp32: 4 of 300
+// (0.4 and 6) 28.6 for 29.7, 8 of 500 (1 and 8) 32.1 either way.
+constexpr int64_t kSmallRows = 256, kSmallZeros = 65536, kSmallRounds = 2;
+
+void plan_small(const HeadArgs &a, HeadPlan &p) {
+    const int64_t round = 1024 * (a.bf16 ? 8 : 4), rows = round_up(a.count, 64);
+    const int64_t statistics = p.subtiles <= kFewStats ? ceil_div(a.count, 64) : ceil_div(a.count, 16) * ceil_div(p.subtiles, 512);
+    p.idle_with_rows = a.grad_hidden && a.count <= kSmallRows && a.count * a.width <= kSmallZeros;
+    p.pack_with_rows = p.pieces == 1 && rows * p.width_p <= kSmallRounds * round;
+    p.softmax_with_loss = p.pieces == 1 && statistics <= kSmallRounds;
+    p.turn_with_loss = p.softmax_with_loss && (a.grad_hidden || a.grad_table) && a.count * p.vocab_p <= kSmallRounds * round &&
+                       rows * p.vocab_p <= 3 * kSmallRounds * round;
+}
+
 }  // namespace
 
 HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
@@ -246,6 +268,7 @@ HeadPlan plan_head(const HeadArgs &a, int64_t rows) {
     p.gw_off = a.grad_table && a.table_grad_bf16 && p.pieces > 1 ? take(4 * a.vocab * a.width) : -1;
     p.parts_off = take(parts_h > parts_t ? parts_h : parts_t);
     p.bytes = at;
+    plan_small(a, p);
     return p;
 }
 

@@ -100,6 +100,8 @@ struct HeadSums {
     float most;                   // largest |weight|
     float scale;                  // grad_scale * most (/ the weights' sum)
 };
+// A row of at most so many statistics is a quarter wave's in the loss's workgroup.
+constexpr int kFewStats = 64;
 // Of each row that takes part, in the order of the piece.
 struct HeadRow {
     float top;                    // largest z * log2(e)
@@ -139,6 +141,8 @@ struct HeadPlan {
     int sub;                      // vocabulary entries that share a statistic
     int64_t subtiles;             // statistics of a row
     int slots_hidden, slots_table;       // room for parts of the gradients' tiles
+    // small calls: what a kernel of one workgroup does besides, instead of a launch
+    bool idle_with_rows, pack_with_rows, softmax_with_loss, turn_with_loss;
     // workspace offsets in bytes; -1: not there
     int64_t sum_off, map_off, loss_off, row_off, stat_off, hidden_off, table_off, e_off, gw_off,
         parts_off, bytes;
