@@ -7,7 +7,7 @@ import subprocess
 import pytest
 
 import host_double
-from test_vocab_cpu import INVALID, L, UNSUPPORTED, changed, malloc, needs_gpp, refused, size_of  # noqa: F401
+from test_vocab_cpu import INVALID, L, UNSUPPORTED, changed, head_args, malloc, needs_gpp, refused, size_of  # noqa: F401
 import zero_partitioned_optimizer_flatten_amd as zero
 from zero_partitioned_optimizer_flatten_amd import build as zb
 
@@ -25,6 +25,26 @@ def test_no_rows_have_no_position_ids(L):  # noqa: F811
     refused(L, INVALID, call(prows=11), "run past")
     refused(L, INVALID, call(pos=table, ptable=None), "together")
     refused(L, INVALID, call(count=1, ids=table, out=malloc(L, 2 * width)), "together")
+
+
+@needs_gpp
+@pytest.mark.parametrize("dtype", [0, 1])
+@pytest.mark.parametrize("piece", [0, 50])
+def test_workspace_is_enough_for_a_table_off_16_bytes(L, dtype, piece):  # noqa: F811
+    """Such a table is copied, also where its rows are whole stages; the size call
+    does not see its address and has to count the copy."""
+    vocab, width, es = 1000, 64, 2 if dtype else 4
+    args, need = head_args(L, dtype, dtype, piece, count=300, vocab=vocab, width=width)
+    t = malloc(L, es * (vocab * width + 1))
+    assert t % 16 == 0
+    used = {}
+    for off in (0, es):
+        assert L.zero_head_loss(*changed(args, t=t + off)) == zero.ZERO_OK, L.zero_last_error()
+        used[off] = L.double_head_bytes()
+        assert used[off] <= need
+    assert used[es] == used[0] + es * vocab * width
+    # with the losses' place in it too, it is what the size call says
+    refused(L, INVALID, lambda: L.zero_head_loss(*changed(args, t=t + es, losses=None, bytes=need - 1)), "needs")
 
 
 @pytest.fixture(scope="module")
