@@ -548,8 +548,11 @@ int zero_embed_grad_workspace(int64_t count, int64_t rows, int64_t width,
  * then not touched. D: the forward call's drop. The sum is in binary32, in an
  * order that ids, count and width fix. The gradient of a position table is this call
  * with the position ids, scale 1 and the same drop. workspace: 256-byte
- * aligned. EINVAL, EUNSUPPORTED as zero_embed; EINVAL also for a workspace
- * that is too small. */
+ * aligned. The sorting reads the ids once for every 512 rows of the table (that
+ * number to the next power of two, 256 at least), which passes the sums for
+ * batches of 10^5 ids or tables of 10^6 rows. EINVAL, EUNSUPPORTED as
+ * zero_embed; EINVAL also for a workspace that is too small, EUNSUPPORTED where
+ * 2^42 ids would have to be read. */
 int zero_embed_grad(const void *grad_out, zero_dtype grad_dtype,
                     const void *ids, int32_t id_bytes, int64_t count,
                     int64_t rows, int64_t width, double scale,

@@ -54,7 +54,8 @@ def rules(tmp_path_factory):
                            *[os.path.join(host_double.TESTS, n) for n in ("host_double.cpp", "vocab_double.cpp", "vocab_rules.cpp")],
                            "-o", so])
     lib = ctypes.CDLL(so)
-    lib.rules_turned_with_loss.restype = ctypes.c_int64
+    lib.rules_turned_with_loss.restype = lib.rules_sort_groups.restype = ctypes.c_int64
+    lib.rules_sort_groups.argtypes = [ctypes.c_int64, ctypes.c_int64, ctypes.c_void_p]
     lib.rules_turned_with_loss.argtypes = [ctypes.c_int64] * 3 + [ctypes.c_int, ctypes.c_int64]
     return lib
 
@@ -73,3 +74,26 @@ def test_one_workgroup_turns_few_numbers(rules):
                 assert rules.rules_turned_with_loss(count, vocab, 64, bf16, 1) == (turned if count == 1 else 0)
                 done += turned > 0
     assert done >= 20, done
+
+
+@needs_gpp
+def test_sort_groups_are_no_more_than_the_ids_need(rules):
+    ids = ctypes.c_int()
+    for rows in (1, 255, 256, 257, 50257, 131071, 131072, 131073, 262144, 262145, 1 << 20, (1 << 30) - 1, 1 << 30):
+        groups = rules.rules_sort_groups(1000, rows, ctypes.byref(ids))
+        assert ids.value <= 512 and ids.value * groups >= rows
+        assert groups == 256 or groups // 2 * 512 < rows, (rows, groups)
+
+
+@needs_gpp
+@pytest.mark.parametrize("rows,most", [(1 << 30, 1 << 21), (1 << 26, 1 << 25), ((1 << 22) + 1, 1 << 28), (1 << 20, (1 << 31) - 1)])
+def test_sort_that_takes_the_device_for_long_is_refused(L, rows, most):  # noqa: F811
+    """2^42 ids read, by rows / 512 workgroups; ordinary tables take any number."""
+    n = ctypes.c_int64()
+    size = L.zero_embed_grad_workspace
+    assert size(most, rows, 1, ctypes.byref(n)) == zero.ZERO_OK, L.zero_last_error()
+    if most < (1 << 31) - 1:
+        assert size(most + 1, rows, 1, ctypes.byref(n)) == UNSUPPORTED
+        p = malloc(L, 4096)
+        refused(L, UNSUPPORTED, lambda: L.zero_embed_grad(p, 0, p, 8, most + 1, rows, 1, 1.0, None, p, 0, 1, p, 1 << 50, None),
+                "more than one call")

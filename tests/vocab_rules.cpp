@@ -16,4 +16,11 @@ int64_t rules_turned_with_loss(int64_t count, int64_t vocab, int64_t width, int 
     return p.turn_with_loss ? p.piece_p * p.vocab_p : 0;
 }
 
+// Workgroups of the sort, and ids of each.
+int64_t rules_sort_groups(int64_t count, int64_t rows, int *ids) {
+    const zk::EmbedGradPlan p = zk::plan_embed_grad(count, rows, 8);
+    *ids = p.ids_per_group;
+    return (int64_t)1 << p.sort_groups_log2;
+}
+
 }

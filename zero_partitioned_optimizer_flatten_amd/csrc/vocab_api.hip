@@ -116,14 +116,28 @@ int head_sizes(int64_t count, int64_t vocab, int64_t width, zero_dtype dtype, in
     return ZERO_OK;
 }
 
+// The sort's workgroups read every id each: at most so many in all, about 5 s of them.
+constexpr int64_t kMaxSortReads = (int64_t)1 << 42;
+
+int check_sort(const zk::EmbedGradPlan &p, int64_t count, int64_t rows) {
+    if (count > kMaxSortReads >> p.sort_groups_log2)
+        return fail(ZERO_EUNSUPPORTED, "%lld ids of a table of %lld rows are more than one call takes", (long long)count,
+                    (long long)rows);
+    return ZERO_OK;
+}
+
 }  // namespace
 
 namespace zk {
 
 EmbedGradPlan plan_embed_grad(int64_t count, int64_t rows, int64_t width) {
     EmbedGradPlan p;
-    p.sort_groups_log2 = 8;                        // one workgroup to a compute unit
-    while ((rows >> p.sort_groups_log2) >= kSortIds) ++p.sort_groups_log2;
+    // One workgroup to a compute unit, and more for tables of more than 131072 rows. Each
+    // reads every token, up to 0.9e12 a second in all: 32768 tokens (64 columns) take 32 us
+    // of 131072 rows, 43 of 2^18 and 115 of 2^20 with 2048 workgroups, 2^20 tokens of 2^20
+    // rows 2.6 ms. check_sort() refuses what would take the device for long.
+    p.sort_groups_log2 = 8;
+    while (ceil_div(rows, (int64_t)1 << p.sort_groups_log2) > kSortIds) ++p.sort_groups_log2;
     p.ids_per_group = (int)ceil_div(rows, (int64_t)1 << p.sort_groups_log2);
     // About 4096 waves, and 8 to 256 tokens to each: enough to keep loads on their way,
     // few partial rows. 65536 tokens of 768 columns take 79 us (half the waves 86, a
@@ -325,7 +339,9 @@ int zero_embed_grad_workspace(int64_t count, int64_t rows, int64_t width, int64_
     if (rc) return rc;
     if ((rc = check_count(count, width))) return rc;
     if (!bytes) return fail(ZERO_EINVAL, "null bytes");
-    *bytes = zk::plan_embed_grad(count, rows, width).bytes;
+    const zk::EmbedGradPlan p = zk::plan_embed_grad(count, rows, width);
+    if ((rc = check_sort(p, count, rows))) return rc;
+    *bytes = p.bytes;
     return ZERO_OK;
 }
 
@@ -339,6 +355,8 @@ int zero_embed_grad(const void *grad_out, zero_dtype grad_dtype, const void *ids
     if (rc) return rc;
     if (!valid_dtype(grad_dtype) || !valid_dtype(table_dtype)) return fail(ZERO_EINVAL, "unknown dtype");
     if ((rc = check_count(count, width))) return rc;
+    const zk::EmbedGradPlan p = zk::plan_embed_grad(count, rows, width);
+    if ((rc = check_sort(p, count, rows))) return rc;
     if ((rc = check_scale(scale))) return rc;
     if ((rc = check_drop(drop, &a.drop))) return rc;
     if ((rc = check_ids(ids, id_bytes, count, "ids"))) return rc;
@@ -348,7 +366,6 @@ int zero_embed_grad(const void *grad_out, zero_dtype grad_dtype, const void *ids
     if (overlap(grad_table, bytes, grad_out, count * width * dtype_size(grad_dtype)) ||
         overlap(grad_table, bytes, ids, count * id_bytes))
         return fail(ZERO_EINVAL, "grad_table overlaps an input");
-    const zk::EmbedGradPlan p = zk::plan_embed_grad(count, rows, width);
     if ((rc = check_workspace(workspace, workspace_bytes, p.bytes))) return rc;
     if (overlap(workspace, p.bytes, grad_out, count * width * dtype_size(grad_dtype)) ||
         overlap(workspace, p.bytes, grad_table, bytes) || overlap(workspace, p.bytes, ids, count * id_bytes))
