@@ -361,14 +361,18 @@ __device__ __forceinline__ f32x4 mma(f32x4 p, f32x4 q, f32x4 c) {
 // 16 bytes a lane, from base + from, to LDS at `lds` + 16 * lane; nothing from
 // base + bytes on is read. In assembly, since the compiler would otherwise wait
 // for all such loads before it reads LDS across lanes (ds_read_b64_tr_b16); the
-// waits are the loop's own. No register is written.
+// waits are the loop's own. No vector register is written; m0 is, which the compiler
+// has to know of, though it warns of every reserved register that is named.
 __device__ __forceinline__ void load_to_lds(const char *base, uint32_t bytes, int from, uint32_t lds) {
     typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
     const u32x4 r = {(uint32_t)(uintptr_t)base, (uint32_t)((uintptr_t)base >> 32) & 0xFFFFu, bytes, 0x00027000u};
+#pragma clang diagnostic push
+#pragma clang diagnostic ignored "-Winline-asm"
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
                  :
                  : "s"(lds), "v"(from), "s"(r)
-                 : "memory");
+                 : "m0", "memory");
+#pragma clang diagnostic pop
 }
 
 // One operand's tile of a stage: B rows and 128 bytes of the long axis, from
