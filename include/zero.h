@@ -590,10 +590,11 @@ int zero_head_loss_workspace(int64_t count, int64_t vocab, int64_t width,
  * The logits are never kept: rows are worked through in pieces of piece_rows
  * (0: as many as need a GiB for one number of `dtype` each against the whole
  * vocabulary), whose exponentials are turned into G and multiplied before the
- * next piece's. Products add in binary32; G is rounded to `dtype` before it is
- * multiplied, so with bf16 operands an fp32 grad_table is a sum of products
- * whose one factor was rounded to 8 bits. Results depend on piece_rows in
- * their last bits. EINVAL: as above, grad_scale not finite, piece_rows < 0, a
+ * next piece's. Products add in binary32; G, its row's weight over the largest
+ * included, is rounded to `dtype` before it is multiplied, so with bf16 operands
+ * an fp32 grad_table is a sum of products whose one factor was rounded to 8
+ * bits. losses are not negative where the logits are finite. Results depend on
+ * piece_rows in their last bits. EINVAL: as above, grad_scale not finite, piece_rows < 0, a
  * workspace too small or not 256-byte aligned, overlapping buffers.
  * EUNSUPPORTED: rows of width or vocab elements of 4 MiB or more, pieces of
  * more than 2^20 rows or 64 GiB, 2^31 rows. */

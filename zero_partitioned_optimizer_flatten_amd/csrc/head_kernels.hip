@@ -17,13 +17,14 @@
 // entries with p = 0 would all be off by the same; so they are -1 and exact. Rows
 // that take no part (target outside the table, weight 0) are left out of all products.
 //
-// Bound by the products, which run at the power limit: GPT-2's head (8192 rows of
-// 768 against 50257) takes 2.09 ms with both gradients, three products of 627, 554
-// and 554 us (1010 to 1140 TFLOP/s) and 269 for e's turning into G; 6553 rows of 4096
-// against 32000 take 4.5 ms, three of 1370 to 1456 (1180 to 1260 TFLOP/s, where a
-// library product of these shapes reaches 1261). With fp32 1023 x 16001 x 1025 takes
-// 0.96 ms, three of 274 to 304 us (110 to 123 TFLOP/s; a library product of 8192^3
-// 153).
+// Bound by the products, under which the clock falls from 2400 MHz to 2150 or 2220:
+// GPT-2's head (8192 rows of 768 against 50257) takes 2.10 ms with both gradients,
+// three products of 650, 559 and 556 us (970 to 1140 TFLOP/s; library products of
+// these shapes, at 1990 to 2080 MHz, 574, 637 and 666) and 270 for e's turning into G;
+// 6553 rows of 4096 against 32000 take 4.5 to 4.6 ms, three of 1389, 1427 and 1465
+// (1170 to 1240 TFLOP/s; the library's 1171, 1751 and 1578). With fp32 1023 x 16001 x
+// 1025 takes 0.96 ms, three of 282 to 312 us (108 to 119 TFLOP/s; a library product
+// of 8192^3 153).
 #include "vocab_internal.h"
 
 namespace zk {
@@ -218,8 +219,8 @@ rows_kernel(HeadArgs a, HeadSums *sums, int32_t *map, int32_t *target, float *lo
 // those along k a whole number of 128-byte stages. A workgroup makes BP x BQ outputs
 // with WP x WQ waves; a stage of both operands, 128 bytes of k, goes straight from
 // memory to LDS while the stage before it is multiplied. What is not kept, and why:
-// the 32 x 32 x 16 instruction, fewer cycles but 5% more time at the power limit
-// (4.76 ms for 4.54); 128 x 128 outputs to a wave (registers spill).
+// the 32 x 32 x 16 instruction, fewer cycles but 5% more time (4.76 ms for 4.54);
+// 128 x 128 outputs to a wave (registers spill).
 //
 // LDS holds a row's 128 bytes as eight 16-byte chunks, chunk c at place
 // c ^ (row % 8): then the 16 rows that a fragment reads at one chunk lie on
@@ -817,8 +818,10 @@ __global__ void __launch_bounds__(256) join_kernel(Product g, int bp, int bq, in
 // In place, [rows][vocab_p]; zeros behind the last row up to a whole stage of the
 // product across the rows, and behind the vocabulary. G is rounded to the operands'
 // type, as the matrix cores take it: with bf16 by up to 2^-8 of itself, which the
-// products' sums average. Bound by memory: 8192
-// rows of 50304 bf16 take 269 us (1.65 GB, 6.1 TB/s).
+// products' sums average. At the target of a certain row that is -1, exact, times the
+// row's weight over the largest, which is not: with weights both gradients are off by
+// 2.2e-3 of their norm, without by 1.75e-3, of which 1.66e-3 is their own rounding to
+// bf16. Bound by memory: 8192 rows of 50304 bf16 take 270 us (1.65 GB, 6.1 TB/s).
 struct Gradient {
     const int32_t *target;        // of the piece's rows
     const f32x2 *stat;

@@ -199,8 +199,10 @@ int choose_tile(int64_t np, int64_t nq, int64_t steps, bool cut, bool bf16) {
 // stages in LDS instead of two, reads 32000 x 5120 bf16 for one row in 75 us (call;
 // the other tiles 96), for 128 in 88 (105), for 192 in 98 (117), for 256 in 115 (130).
 // A table of fewer tiles leaves compute units without one, which costs from about two
-// rows a tile on (16000 x 4096: 160 rows 67 for 73, 256 rows 80 for 75). fp32 is
-// bound by its multiplying (1 row of 32000 x 4096 146 for 149, 48 rows 192 for 179).
+// rows a tile on (16000 x 4096: 160 rows 67 for 73, 256 rows 80 for 75). A table of more
+// goes by the other tiles: 4096 wide, one row and 128 rows of 32768 entries take 78 and
+// 81 us, of 33024 85 and 104, of 50257 114 and 120 (3.6 and 3.4 TB/s), of 128256 234 and
+// 264 (4.5 and 4.0). fp32 is bound by its multiplying (1 row of 32000 x 4096 146 for 149, 48 rows 192 for 179).
 int logits_tile(int64_t vocab, int64_t rows, int64_t steps, bool bf16) {
     const int64_t tiles = ceil_div(vocab, 128);
     if (bf16 && tiles <= 256 && rows <= 2 * tiles)

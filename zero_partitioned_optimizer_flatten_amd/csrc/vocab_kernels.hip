@@ -215,9 +215,15 @@ __global__ void __launch_bounds__(kThreads) embed_kernel(EmbedArgs a, uint32_t p
 // sorted list begins. A second reading places its tokens, each wave its own
 // stretch of the batch in order, so equal ids keep the order they came in and
 // their sum is always added up the same way. When the gradient is written and
-// not added to, the rows of ids that no token names are set to zero here. Bound by
-// the round trips of its two readings (8192 tokens 9 us) and then by those zeros
-// (16384 tokens, 32000 rows of 4096 bf16: 52 us).
+// not added to, the rows of ids that no token names are set to zero here.
+//
+// Up to 8192 tokens a wave's ids stay in its registers and the second reading is left
+// out. Those take 9 us, of which a workgroup's own 6.7 (text's tokens, 50257 rows):
+// clearing its counts 0.5, reading and counting 1.6, the waves' sums 1.2, begins and
+// places 1.2, placing 2.2. Beyond, counting and placing grow with the tokens of a wave
+// (131072: 23 and 34 of 59), and where most tokens are of one id their additions to one
+// number queue up (8192 of one id 12 us in its workgroup, 131072 150). Written and not
+// added to, the zeros follow: 16384 tokens, 32000 rows of 4096 bf16 take 51 us.
 
 __device__ __forceinline__ void zero_row(char *p, int64_t bytes, int lane) {
     // 2-byte elements up to a 16-byte line, whole vectors, the rest

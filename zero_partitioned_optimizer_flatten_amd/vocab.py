@@ -6,6 +6,10 @@ As in the rest of the binding: checks and marshalling, the work runs in the
 library's kernels on the current stream of the tensors' device (or `stream`).
 Results and workspaces come from torch's allocator on that stream, so a call
 can be captured in a graph.
+
+None of the calls is an autograd function, whatever its tensors require: results
+do not require gradients (embed_grad, dropout and head_loss are the backward
+calls), and tensors written in place do not count it as a new version.
 """
 from __future__ import annotations
 
