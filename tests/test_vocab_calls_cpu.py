@@ -10,6 +10,7 @@ import host_double
 from test_vocab_cpu import INVALID, L, UNSUPPORTED, changed, head_args, malloc, needs_gpp, refused, size_of  # noqa: F401
 import zero_partitioned_optimizer_flatten_amd as zero
 from zero_partitioned_optimizer_flatten_amd import build as zb
+from zero_partitioned_optimizer_flatten_amd import vocab
 
 
 @needs_gpp
@@ -45,6 +46,26 @@ def test_workspace_is_enough_for_a_table_off_16_bytes(L, dtype, piece):  # noqa:
     assert used[es] == used[0] + es * vocab * width
     # with the losses' place in it too, it is what the size call says
     refused(L, INVALID, lambda: L.zero_head_loss(*changed(args, t=t + es, losses=None, bytes=need - 1)), "needs")
+
+
+@needs_gpp
+def test_outputs_over_the_dropout_counter_are_refused(L):  # noqa: F811
+    """Every workgroup reads it, at no certain time."""
+    n, rows, width = 6, 10, 8
+    ids, table, x = malloc(L, 8 * n), malloc(L, 4 * rows * width), malloc(L, 4 * n * width)
+    need = size_of(L, L.zero_embed_grad_workspace, n, rows, width)
+    out, ws, apart = malloc(L, 4 * rows * width), malloc(L, need), malloc(L, 8)
+    drop = lambda at: ctypes.byref(vocab._Drop(0.5, 1, 2, at))  # noqa: E731
+    calls = {
+        out: [lambda d: L.zero_embed(ids, 8, n, table, rows, width, 0, 1.0, None, None, 0, d, out, 0, None),
+              lambda d: L.zero_dropout(x, None, out, n * width, 0, d, None),
+              lambda d: L.zero_embed_grad(x, 0, ids, 8, n, rows, width, 1.0, d, out, 0, 0, ws, need, None)],
+        ws: [lambda d: L.zero_embed_grad(x, 0, ids, 8, n, rows, width, 1.0, d, out, 0, 0, ws, need, None)]}
+    for at, of in calls.items():
+        for call in of:
+            assert call(drop(apart)) == zero.ZERO_OK, L.zero_last_error()
+            refused(L, INVALID, lambda: call(drop(at)), "overlap")
+            refused(L, INVALID, lambda: call(drop(at + 8 * (n - 1))), "overlap")
 
 
 @pytest.fixture(scope="module")

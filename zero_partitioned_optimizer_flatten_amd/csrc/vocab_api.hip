@@ -82,6 +82,9 @@ int check_drop(const zero_drop *d, zk::Drop *out) {
     return ZERO_OK;
 }
 
+// Whether `bytes` bytes at p hold dropout's counter, which every workgroup reads.
+bool holds_counter(const void *p, int64_t bytes, const zero_drop *d) { return d && overlap(p, bytes, d->counter, 8); }
+
 int check_scale(double scale) {
     if (!std::isfinite((float)scale)) return fail(ZERO_EINVAL, "scale must be finite in fp32 (got %g)", scale);
     return ZERO_OK;
@@ -317,7 +320,7 @@ int zero_embed(const void *ids, int32_t id_bytes, int64_t count, const void *tab
     const int64_t bytes = count * width * dtype_size(out_dtype);
     if (overlap(out, bytes, table, rows * width * dtype_size(dtype)) || overlap(out, bytes, ids, count * id_bytes) ||
         overlap(out, bytes, position_table, position_rows * width * dtype_size(dtype)) ||
-        overlap(out, bytes, position_ids, count * id_bytes))
+        overlap(out, bytes, position_ids, count * id_bytes) || holds_counter(out, bytes, drop))
         return fail(ZERO_EINVAL, "out overlaps an input");
     a.ids = ids;
     a.pos_ids = position_ids;
@@ -366,11 +369,12 @@ int zero_embed_grad(const void *grad_out, zero_dtype grad_dtype, const void *ids
     if ((rc = check_buffer(grad_table, rows * width, dtype_size(table_dtype), "grad_table"))) return rc;
     const int64_t bytes = rows * width * dtype_size(table_dtype);
     if (overlap(grad_table, bytes, grad_out, count * width * dtype_size(grad_dtype)) ||
-        overlap(grad_table, bytes, ids, count * id_bytes))
+        overlap(grad_table, bytes, ids, count * id_bytes) || holds_counter(grad_table, bytes, drop))
         return fail(ZERO_EINVAL, "grad_table overlaps an input");
     if ((rc = check_workspace(workspace, workspace_bytes, p.bytes))) return rc;
     if (overlap(workspace, p.bytes, grad_out, count * width * dtype_size(grad_dtype)) ||
-        overlap(workspace, p.bytes, grad_table, bytes) || overlap(workspace, p.bytes, ids, count * id_bytes))
+        overlap(workspace, p.bytes, grad_table, bytes) || overlap(workspace, p.bytes, ids, count * id_bytes) ||
+        holds_counter(workspace, p.bytes, drop))
         return fail(ZERO_EINVAL, "workspace overlaps another buffer");
     a.grad_out = grad_out;
     a.grad_bf16 = grad_dtype == ZERO_BF16;
@@ -407,6 +411,7 @@ int zero_dropout(const void *x, const void *add, void *out, int64_t count, zero_
     if ((out != x && overlap(out, count * es, x, count * es)) ||
         (add && out != add && overlap(out, count * es, add, count * es)))
         return fail(ZERO_EINVAL, "out overlaps an input without being it");
+    if (holds_counter(out, count * es, drop)) return fail(ZERO_EINVAL, "out overlaps the dropout counter");
     a.x = x;
     a.add = add;
     a.out = out;
